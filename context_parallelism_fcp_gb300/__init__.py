@@ -35,6 +35,12 @@ __all__ = [
     "block_attn_bwd_tiles_banded",
     "reshuffle",
     "FcpAttention",
+    "PagedCache",
+    "CacheBatch",
+    "cache_write",
+    "cache_read",
+    "paged_attn",
+    "PagedAttention",
     "MASK_FULL",
     "MASK_CAUSAL_DIAG",
     "EXPORTED_SYMBOLS",
@@ -99,6 +105,16 @@ class _View(ctypes.Structure):
     ]
 
 
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scales", "v_scales", "status")] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "hkv", "page_size", "head_dim", "dtype", "reserved")]
+
+
+class _CacheBatchStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cu_new", "lens", "block_table")] + [
+        (n, ctypes.c_int32) for n in ("n_seqs", "max_pages", "total_new", "max_new")]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -136,6 +152,11 @@ _SIGNATURES = {
     "fcp_bwd_static_scratch_bytes": (_SZ, []),
     "fcp_block_attn_bwd_static_scratch": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P]),
     "fcp_reshuffle": (_ST, [_P, _P, _P, _P, _I32, _I32, _I32, _P]),
+    "fcp_cache_write": (_ST, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_CacheBatchStruct), _P, _P, _P]),
+    "fcp_cache_read": (_ST, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_CacheBatchStruct), _P, _P, _P]),
+    "fcp_paged_attn_workspace_bytes": (_SZ, [_I32]),
+    "fcp_paged_attn": (_ST, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_CacheBatchStruct), _P, _I32, _I32, _P, _P, _P,
+                             _SZ, _P]),
     "fcp_selftest_bounded_wait": (_ST, [_P, _P]),
     "fcp_device_error": (_ST, [_P, ctypes.POINTER(_I32), _P]),
     "fcp_plan_free": (None, [_P]),
@@ -598,3 +619,12 @@ class FcpAttention:
         code = device_error(self.d_plan, stream)
         if code:
             raise FcpError(6, "device", f"error word 0x{code:x}")
+
+
+def __getattr__(name):
+    # the paged cache needs torch, which importing the package (its host plan) does not
+    if name in ("PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention"):
+        from . import paged
+
+        return getattr(paged, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

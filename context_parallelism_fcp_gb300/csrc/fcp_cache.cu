@@ -1,0 +1,258 @@
+// Writing rows of K and V into the pages of a paged cache (quantising them where the cache is
+// e4m3), and reading them back as bf16.
+//
+// Row r = (token, KV head) with channels x: an e4m3 cache stores k = the smallest integer
+// >= -126 with max|x| <= 448 * 2^k, and the codes e4m3(x * 2^-k), rounded to nearest even: the
+// only rounding there is, since the product with a power of two is exact. Reading gives
+// code * 2^k, exact in bf16 (a code has 4 significant bits) while it is a normal number. A row
+// with an infinity or NaN in it gets the NaN scale and zero codes: it reads back as NaN.
+//
+// Both directions are bound by HBM: 2 * T * Hkv rows in and out, nothing reused. One warp
+// moves whole rows, D / 8 lanes to a row, 16 bytes of bf16 to a lane.
+#include <algorithm>
+
+#include "fcp_paged.h"
+
+namespace fcp {
+
+fcp_status paged_args(const fcp_cache* c, const fcp_cache_batch* b, PagedArgs* out) {
+  if (c == nullptr || b == nullptr || out == nullptr) return FCP_ERR_INVALID;
+  if (c->n_pages < 0 || c->hkv <= 0 || c->page_size <= 0 || b->n_seqs < 0 || b->max_pages < 0 || b->total_new < 0 ||
+      b->max_new < 0)
+    return FCP_ERR_INVALID;
+  if (c->dtype != FCP_CACHE_BF16 && c->dtype != FCP_CACHE_E4M3) return FCP_ERR_INVALID;
+  if (c->head_dim != 64 && c->head_dim != 128) return FCP_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return FCP_ERR_UNSUPPORTED;
+  if (static_cast<long long>(b->max_pages) * c->page_size > INT32_MAX) return FCP_ERR_UNSUPPORTED;
+  if (b->n_seqs > 65536) return FCP_ERR_UNSUPPORTED;
+  if (c->status == nullptr || !aligned16(c->status)) return FCP_ERR_INVALID;
+  if (b->n_seqs > 0 && (!b->cu_new || !b->lens || (b->max_pages > 0 && !b->block_table))) return FCP_ERR_INVALID;
+  if (c->n_pages > 0) {
+    if (!c->k_pages || !c->v_pages || !aligned16(c->k_pages) || !aligned16(c->v_pages)) return FCP_ERR_INVALID;
+    if (c->dtype == FCP_CACHE_E4M3 &&
+        (!c->k_scales || !c->v_scales || !aligned16(c->k_scales) || !aligned16(c->v_scales)))
+      return FCP_ERR_INVALID;
+  }
+  PagedArgs p;
+  p.cu = b->cu_new;
+  p.lens = b->lens;
+  p.table = b->block_table;
+  p.n_seqs = b->n_seqs;
+  p.max_pages = b->max_pages;
+  p.n_pages = c->n_pages;
+  p.hkv = c->hkv;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+  p.total_new = b->total_new;
+  p.k_pages = static_cast<uint8_t*>(c->k_pages);
+  p.v_pages = static_cast<uint8_t*>(c->v_pages);
+  p.k_scales = c->k_scales;
+  p.v_scales = c->v_scales;
+  p.status = c->status;
+  if (c->n_pages == 0) p.k_pages = p.v_pages = p.k_scales = p.v_scales = reinterpret_cast<uint8_t*>(c->status);
+  *out = p;
+  return FCP_OK;
+}
+
+namespace {
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveTokens = 32;   // packed rows of a block
+constexpr int kCoarse = 1024;     // row offsets kept in shared memory
+
+// The cache row (page * page_size + offset, to which a head adds its stride) of each of the
+// block's tokens; -1 for rows behind the last sequence, rows before their sequence's first
+// position and rows whose page is outside the cache.
+struct TokenPlace {
+  int32_t page, off;
+};
+
+__device__ __forceinline__ void find_places(const PagedArgs& p, int t0, TokenPlace* place, int* coarse) {
+  // The last i with cu[i] <= t: every `step`-th offset is searched in shared memory and the
+  // rest in memory, so that the dependent reads are few however many sequences there are.
+  const int step = (p.n_seqs + kCoarse) / kCoarse;
+  const int n_coarse = (p.n_seqs + step) / step;  // offsets 0, step, ... <= n_seqs
+  for (int j = threadIdx.x; j < n_coarse; j += kMoveThreads) coarse[j] = __ldg(p.cu + j * step);
+  __syncthreads();
+  if (threadIdx.x < kMoveTokens) {
+    const int t = t0 + threadIdx.x;
+    TokenPlace r{-1, 0};
+    if (t < p.total_new) {
+      int lo = 0, hi = n_coarse;  // coarse[lo] <= t < coarse[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (coarse[mid] <= t) lo = mid; else hi = mid;
+      }
+      int i = lo * step, e = min(i + step, p.n_seqs);
+      while (e - i > 1) {
+        const int mid = (i + e) >> 1;
+        if (__ldg(p.cu + mid) <= t) i = mid; else e = mid;
+      }
+      if (i < p.n_seqs) {
+        const SeqShape s = seq_shape(p, i, true);
+        if (t >= s.a && t < s.a + s.n) {
+          const int pos = s.len - s.n + (t - s.a);
+          if (pos >= 0) {
+            const int page = __ldg(p.table + static_cast<long long>(i) * p.max_pages + (pos >> p.page_shift));
+            if (page >= 0 && page < p.n_pages) {
+              r.page = page;
+              r.off = pos & ((1 << p.page_shift) - 1);
+            } else {
+              atomicCAS(p.status, 0, kErrCachePage);
+            }
+          }
+        }
+      }
+    }
+    place[threadIdx.x] = r;
+  }
+  __syncthreads();
+}
+
+// Quantise the 8 channels of this lane (of a row shared by LPR lanes): 8 codes and the row's scale byte.
+template <int LPR>
+__device__ __forceinline__ uint2 quantise(const uint4 x, uint32_t& scale_byte) {
+  float v[8];
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  // the largest magnitude as bf16 bits: non-finite values order above every finite one
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (top >= 0x7f80u) {
+    scale_byte = 255;
+    return make_uint2(0u, 0u);
+  }
+  // max|x| = 1.m * 2^e <= 1.75 * 2^(8 + k): k = e - 8, or e - 7 where 1.m > 1.75 (mantissa over 0x60)
+  const int e = static_cast<int>(top >> 7) - 127;
+  const int k = top == 0 ? 0 : max(e - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0), -126);
+  scale_byte = static_cast<uint32_t>(k + 127);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  // 256 * 2^120 would be the one product that bf16 cannot hold
+  const float most = k == 120 ? 240.f : 448.f;
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float y0 = fminf(fmaxf(v[2 * i] * inv, -most), most), y1 = fminf(fmaxf(v[2 * i + 1] * inv, -most), most);
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+__device__ __forceinline__ uint4 dequantise(const uint2 c, float scale) {
+  // code values are exact in bf16; their product with a power of two is rounded at most where
+  // it leaves bf16's normal range
+  uint32_t r[4];
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t a = e4m3x2_to_bf16x2(__byte_perm(w[i], 0, 0x1404));  // codes 0, 1
+    const uint32_t b = e4m3x2_to_bf16x2(__byte_perm(w[i], 0, 0x3424));  // codes 2, 3
+    const uint32_t p[2] = {a, b};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const __nv_bfloat162 y =
+          __floats2bfloat162_rn(__uint_as_float(p[j] << 16) * scale, __uint_as_float(p[j] & 0xffff0000u) * scale);
+      r[2 * i + j] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// grid (ceil(T / 32), ceil(Hkv / heads per block), 2: K or V)
+template <int D, bool kE4M3, bool kRead>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, uint4* __restrict__ k, uint4* __restrict__ v,
+                                                            int heads) {
+  constexpr int LPR = D / 8;                       // lanes to a row
+  constexpr int kPass = kMoveThreads / LPR;        // rows of one pass over the block
+  constexpr int kPasses = kMoveTokens / kPass;     // passes to a head
+  __shared__ TokenPlace place[kMoveTokens];
+  __shared__ int coarse[kCoarse];
+  const int t0 = blockIdx.x * kMoveTokens;
+  find_places(p, t0, place, coarse);
+  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, p.hkv);
+  uint4* rows = blockIdx.z ? v : k;
+  uint8_t* pages = blockIdx.z ? p.v_pages : p.k_pages;
+  uint8_t* scales = blockIdx.z ? p.v_scales : p.k_scales;
+  const int sub = threadIdx.x / LPR, l = threadIdx.x % LPR;
+  TokenPlace at[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) at[i] = place[i * kPass + sub];
+#pragma unroll 2
+  for (int h = h0; h < h1; ++h) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int t = t0 + i * kPass + sub;
+      const bool on = at[i].page >= 0;
+      const long long row = on ? page_row(p, at[i].page, h) + at[i].off : 0;
+      const long long mine = (static_cast<long long>(h) * p.total_new + t) * LPR + l;
+      if constexpr (!kE4M3) {
+        uint4* cell = reinterpret_cast<uint4*>(pages) + row * LPR + l;
+        if (on) {
+          if constexpr (kRead) rows[mine] = *cell; else *cell = rows[mine];
+        }
+      } else {
+        uint2* cell = reinterpret_cast<uint2*>(pages) + row * LPR + l;
+        if constexpr (kRead) {
+          if (on) rows[mine] = dequantise(*cell, e8m0_to_float(scales[row]));
+        } else {
+          const uint4 x = on ? rows[mine] : make_uint4(0u, 0u, 0u, 0u);
+          uint32_t byte;
+          const uint2 codes = quantise<LPR>(x, byte);
+          if (on) {
+            *cell = codes;
+            if (l == 0) scales[row] = static_cast<uint8_t>(byte);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int D, bool kRead>
+fcp_status launch_move(const PagedArgs& p, int dtype, void* k, void* v, cudaStream_t s) {
+  const unsigned bx = static_cast<unsigned>((p.total_new + kMoveTokens - 1) / kMoveTokens);
+  // whole rows of heads stay in one block while that leaves enough blocks for the GPU
+  int heads = p.hkv;
+  while (heads > 1 && 2ll * bx * ((p.hkv + heads - 1) / heads) < 1216) heads = (heads + 1) / 2;
+  const dim3 grid(bx, static_cast<unsigned>((p.hkv + heads - 1) / heads), 2);
+  if (grid.y > 65535u) return FCP_ERR_UNSUPPORTED;
+  uint4* pk = static_cast<uint4*>(k);
+  uint4* pv = static_cast<uint4*>(v);
+  if (dtype == FCP_CACHE_E4M3)
+    move_kernel<D, true, kRead><<<grid, kMoveThreads, 0, s>>>(p, pk, pv, heads);
+  else
+    move_kernel<D, false, kRead><<<grid, kMoveThreads, 0, s>>>(p, pk, pv, heads);
+  FCP_CUDA_TRY(cudaGetLastError(), kRead ? "cache read launch" : "cache write launch");
+  return FCP_OK;
+}
+
+template <bool kRead>
+fcp_status move(const fcp_cache* cache, const fcp_cache_batch* batch, void* k, void* v, void* stream) {
+  PagedArgs p;
+  if (const fcp_status st = paged_args(cache, batch, &p); st != FCP_OK) return st;
+  if (p.total_new == 0 || p.n_seqs == 0) return FCP_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return FCP_ERR_INVALID;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cache->head_dim == 128 ? launch_move<128, kRead>(p, cache->dtype, k, v, s)
+                                : launch_move<64, kRead>(p, cache->dtype, k, v, s);
+}
+
+}  // namespace
+}  // namespace fcp
+
+extern "C" fcp_status fcp_cache_write(const fcp_cache* cache, const fcp_cache_batch* batch, const void* k,
+                                      const void* v, void* stream) {
+  return fcp::move<false>(cache, batch, const_cast<void*>(k), const_cast<void*>(v), stream);
+}
+
+extern "C" fcp_status fcp_cache_read(const fcp_cache* cache, const fcp_cache_batch* batch, void* k, void* v,
+                                     void* stream) {
+  return fcp::move<true>(cache, batch, k, v, stream);
+}

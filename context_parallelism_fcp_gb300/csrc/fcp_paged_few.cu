@@ -1,0 +1,541 @@
+// Attention of few new rows for each cached sequence (single tokens, drafted tokens) over a
+// paged cache, and the entry point of the attention over a paged cache.
+//
+// For a KV head the rows are (new token, query head) pairs, 16 or 32 to a unit, so every query
+// head of the group and every drafted token shares one pass over the keys: HBM traffic is the
+// cache once, at 4 * rows flops for every 2 bytes read: far below what the tensor cores need,
+// so the kernel is bound by HBM and its business is to keep enough bytes in flight. Each warp
+// takes every fourth 16-key chunk of its block's piece and runs its own pipeline of cp.async
+// stages (a chunk lies in one page because pages are multiples of 16 keys) and its own running
+// softmax; warps meet only at the end of a piece. S = Q K^T and O += P V are m16n8k16 products
+// with float32 sums: with 16 rows tcgen05's 128-row tile would be seven eighths empty, and
+// both units are far faster than the loads.
+//
+// K is read from shared memory 16 bytes to a lane: the product over channels does not care for
+// their order, so lane j of a quad takes 8 (bf16) or 16 (e4m3) neighbouring channels and Q's
+// fragments are laid out the same way. V goes through ldmatrix.trans; for e4m3 the 16-bit
+// elements that it transposes are channel pairs, whose low and high bytes become the fragments
+// of two 8-channel tiles. 16-byte pieces of a row are XOR-swizzled so that neither reading has
+// bank conflicts.
+#include <algorithm>
+#include <cmath>
+
+#include "fcp_paged_sched.cuh"
+
+namespace fcp {
+namespace {
+
+using namespace dev;
+
+constexpr int kWarps = 4;
+constexpr int kFewThreads = kWarps * 32;
+constexpr int kChunk = 16;                  // keys of a stage
+constexpr float kGrow = 8.0f;               // a row maximum is raised when it grows by over 2^8
+constexpr int kStageBudget = 96 * 1024;     // shared memory for stages: two blocks fit an SM
+
+template <int D, bool kE4M3>
+struct FewCfg {
+  static constexpr int kRowBytes = kE4M3 ? D : 2 * D;
+  static constexpr int kPieces = kRowBytes / 16;               // 16-byte pieces of a row
+  static constexpr int kTile = kChunk * kRowBytes;             // K or V of a chunk
+  static constexpr int kStage = 2 * kTile + (kE4M3 ? 32 : 0);  // + 16 K scales, 16 V scales
+  static constexpr int kStagesRaw = kStageBudget / (kWarps * kStage);
+  static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
+  static constexpr int kWarpBytes = kStages * kStage;
+};
+
+// Where piece c of row r lies in a tile. Rows of 128 bytes and more: 8 rows of one piece, and
+// pieces 0-3 of two neighbouring rows, fall on different banks; rows of 64 bytes share a line
+// of banks two by two.
+template <int kRowBytes>
+__device__ __forceinline__ int piece_at(int r, int c) {
+  if constexpr (kRowBytes == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  else return r * kRowBytes + ((c ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 in, float32 out
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct Piece {
+  int valid, i, h, u, a, n, len, end, ga, gb, slot;
+};
+
+template <int D, bool kE4M3, int MT>
+__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
+  using C = FewCfg<D, kE4M3>;
+  using P = FewRows<16 * MT>;
+  constexpr int kRows = P::kRows;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Line<kFewThreads> line;
+  __shared__ Piece shared_piece;
+  __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = lane >> 2, j = lane & 3;  // this lane's fragment rows (row, row + 8) and columns
+  const int b = blockIdx.x, blocks = gridDim.x;
+  build_line<P, kFewThreads>(a, line, b == 0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long total = line.prefix[kFewThreads];
+  const long long w0 = share_begin(total, b, blocks), w1 = share_begin(total, b + 1, blocks);
+  if (w0 >= w1) return;
+
+  const uint32_t stages = smem_u32(smem) + warp * C::kWarpBytes;
+  float* sums = reinterpret_cast<float*>(smem);  // [kWarps][kRows][D], over the stages at a piece's end
+  static_assert(kWarps * kRows * D * 4 <= kStageBudget, "the warps' sums fit the stages");
+  const int page_mask = (1 << a.c.page_shift) - 1;
+
+  Walk<P> w;
+  bool walking = true;
+  if (threadIdx.x == 0) walking = seek<P, kFewThreads>(a, line, w0, w);
+  for (bool first = true;; first = false) {
+    if (threadIdx.x == 0) {
+      if (!first) w.next(a);
+      Piece p;
+      p.valid = walking && w.i < a.c.n_seqs && w.f0 < w1;
+      if (p.valid) {
+        p.i = w.i;
+        p.h = w.h;
+        p.u = w.u;
+        p.a = w.s.a;
+        p.n = w.s.n;
+        p.len = w.s.len;
+        p.end = w.end;
+        p.ga = static_cast<int>(max(w0 - w.f0, 0ll));
+        p.gb = static_cast<int>(min(w1 - w.f0, static_cast<long long>(w.g)));
+        p.slot = piece_slot(b, p.ga, p.gb, w.g);
+      }
+      shared_piece = p;
+    }
+    __syncthreads();
+    const Piece p = shared_piece;
+    if (!p.valid) break;
+    const SeqShape s{p.a, p.n, p.len};
+
+    // this lane's rows (2 for each 16-row tile): query row, first key it does not see
+    uint32_t q[MT][D / 16][4];
+    int lim[MT][2];
+    int lim_min = p.len;
+    if (a.causal) {
+      int tok, head;
+      P::row(s, a.group, p.u, 0, tok, head);
+      lim_min = s.len - s.n + tok + 1;
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        int tok, head;
+        const bool on = P::row(s, a.group, p.u, 16 * t + 8 * x + row, tok, head);
+        lim[t][x] = !on || !a.causal ? s.len : s.len - s.n + tok + 1;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + (static_cast<long long>(p.h * a.group + (on ? head : 0)) * a.c.total_new + s.a + (on ? tok : 0)) * D);
+        if constexpr (kE4M3) {
+          // 64 channels: lane j has channels 16 j .. 16 j + 15, in products 0-3 of the 64
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint4 v = on ? __ldg(src + c * 8 + 2 * j + y) : make_uint4(0, 0, 0, 0);
+              q[t][4 * c + 2 * y][x] = v.x;
+              q[t][4 * c + 2 * y][2 + x] = v.y;
+              q[t][4 * c + 2 * y + 1][x] = v.z;
+              q[t][4 * c + 2 * y + 1][2 + x] = v.w;
+            }
+        } else {
+          // 32 channels: lane j has channels 8 j .. 8 j + 7, in products 0-1 of the 32
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const uint4 v = on ? __ldg(src + c * 4 + j) : make_uint4(0, 0, 0, 0);
+            q[t][2 * c][x] = v.x;
+            q[t][2 * c][2 + x] = v.y;
+            q[t][2 * c + 1][x] = v.z;
+            q[t][2 * c + 1][2 + x] = v.w;
+          }
+        }
+      }
+
+    float m[MT][2], l[MT][2], acc[MT][D / 8][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        m[t][x] = -INFINITY;
+        l[t][x] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][c][e] = 0.f;
+    }
+
+    // chunks of this warp: keys k0 + 16 * (warp + 4 n) below kend
+    const int k0 = p.ga * kGranule, kend = min(p.gb * kGranule, p.end);
+    const int* table = a.c.table + static_cast<long long>(p.i) * a.c.max_pages;
+    auto page_of = [&](int key) -> int { return key < kend ? __ldg(table + (key >> a.c.page_shift)) : 0; };
+    int issue_key = k0 + kChunk * warp;
+    int issue_page = page_of(issue_key);
+    int issue_stage = 0;
+    auto issue = [&]() {
+      const int key = issue_key;
+      if (key < kend) {
+        bool ok = issue_page >= 0 && issue_page < a.c.n_pages;
+        if (!ok && lane == 0) atomicCAS(a.c.status, 0, kErrCachePage);
+        const long long r0 = ok ? page_row(a.c, issue_page, p.h) + (key & page_mask) : 0;
+        issue_key += kChunk * kWarps;
+        issue_page = page_of(issue_key);
+        const uint32_t dst = stages + issue_stage * C::kStage;
+        constexpr int kPer = 32 / C::kPieces;  // rows of one instruction
+#pragma unroll
+        for (int x = 0; x < kChunk / kPer; ++x) {
+          const int r = x * kPer + lane / C::kPieces, c = lane % C::kPieces;
+          const long long at = (r0 + r) * C::kRowBytes + c * 16;
+          const bool on = ok && key + r < s.len;  // rows behind the last key may hold anything
+          cp_async16(dst + piece_at<C::kRowBytes>(r, c), a.c.k_pages + (on ? at : 0), on);
+          cp_async16(dst + C::kTile + piece_at<C::kRowBytes>(r, c), a.c.v_pages + (on ? at : 0), on);
+        }
+        if constexpr (kE4M3) {
+          if (lane < 2) cp_async16(dst + 2 * C::kTile + 16 * lane, (lane ? a.c.v_scales : a.c.k_scales) + r0, ok);
+        }
+      }
+      cp_commit();
+      issue_stage = issue_stage + 1 == C::kStages ? 0 : issue_stage + 1;
+    };
+#pragma unroll
+    for (int x = 0; x < C::kStages - 1; ++x) issue();
+
+    int stage = 0;
+    for (int key = k0 + kChunk * warp; key < kend; key += kChunk * kWarps) {
+      cp_wait<C::kStages - 2>();
+      __syncwarp();  // this chunk has arrived, and every lane is done with the stage that is filled next
+      issue();
+      const uint32_t kt = stages + stage * C::kStage, vt = kt + C::kTile;
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+
+      float sc[MT][2][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[t][y][e] = 0.f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if constexpr (kE4M3) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 v = lds16(kt + piece_at<C::kRowBytes>(8 * y + row, 4 * c + j));
+            const uint32_t raw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t b0 = e4m3x2_to_bf16x2(__byte_perm(raw[x], 0, 0x1404));
+              const uint32_t b1 = e4m3x2_to_bf16x2(__byte_perm(raw[x], 0, 0x3424));
+#pragma unroll
+              for (int t = 0; t < MT; ++t) mma16816(sc[t][y], q[t][4 * c + x], b0, b1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const uint4 v = lds16(kt + piece_at<C::kRowBytes>(8 * y + row, 4 * c + j));
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              mma16816(sc[t][y], q[t][2 * c], v.x, v.y);
+              mma16816(sc[t][y], q[t][2 * c + 1], v.z, v.w);
+            }
+          }
+        }
+      }
+      // scores in log2 units; columns of this lane: keys key + 8 y + 2 j + {0, 1}
+      float vs[2][2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float f0 = a.scale_log2, f1 = a.scale_log2;
+        if constexpr (kE4M3) {
+          const uint32_t kb = lds_u16(kt + 2 * C::kTile + 8 * y + 2 * j);
+          const uint32_t vb = lds_u16(kt + 2 * C::kTile + 16 + 8 * y + 2 * j);
+          f0 *= e8m0_to_float(kb & 255u);
+          f1 *= e8m0_to_float(kb >> 8);
+          vs[y][0] = e8m0_to_float(vb & 255u);
+          vs[y][1] = e8m0_to_float(vb >> 8);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          sc[t][y][0] *= f0;
+          sc[t][y][1] *= f1;
+          sc[t][y][2] *= f0;
+          sc[t][y][3] *= f1;
+        }
+      }
+      const bool masked = key + kChunk > lim_min;  // some row does not see the whole chunk
+      if (masked) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key + 8 * y + 2 * j + (e & 1) >= lim[t][e >> 1]) sc[t][y][e] = -INFINITY;
+      }
+      // raise the running maxima only when some row's grew by more than 2^8: P stays below 2^8
+      bool grow = false;
+      float top[MT][2];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          top[t][x] = fmaxf(fmaxf(sc[t][0][2 * x], sc[t][0][2 * x + 1]), fmaxf(sc[t][1][2 * x], sc[t][1][2 * x + 1]));
+          grow = grow || top[t][x] > m[t][x] + kGrow;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = top[t][x];
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mx = fmaxf(mx, m[t][x]);
+            const float f = mx == -INFINITY ? 1.f : fast_exp2(m[t][x] - mx);
+            m[t][x] = mx;
+            l[t][x] *= f;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              acc[t][c][2 * x] *= f;
+              acc[t][c][2 * x + 1] *= f;
+            }
+          }
+      }
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float mb = m[t][x] == -INFINITY ? 0.f : m[t][x];
+            float p0 = fast_exp2(sc[t][y][2 * x] - mb);
+            float p1 = fast_exp2(sc[t][y][2 * x + 1] - mb);
+            l[t][x] += p0 + p1;
+            if constexpr (kE4M3) {
+              // V's scale goes with P; a key that the row does not see keeps its exact zero,
+              // whatever its scale
+              const int k = key + 8 * y + 2 * j;
+              p0 = masked && k >= lim[t][x] ? 0.f : p0 * vs[y][0];
+              p1 = masked && k + 1 >= lim[t][x] ? 0.f : p1 * vs[y][1];
+            }
+            pa[t][2 * y + x] = pack_bf16(p0, p1);  // P in bf16: off by 2^-9 of itself at most
+          }
+      const int vr = (lane & 7) + (lane & 8);  // ldmatrix: keys 0-7, 8-15, then the next piece
+#pragma unroll
+      for (int c = 0; c < C::kPieces; c += 2) {
+        uint32_t f[4];
+        ldsm4_trans(vt + piece_at<C::kRowBytes>(vr, c + (lane >> 4)), f);
+        if constexpr (kE4M3) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t even0 = e4m3x2_to_bf16x2((f[2 * y] & 0x00ff00ffu) << 8);
+            const uint32_t even1 = e4m3x2_to_bf16x2((f[2 * y + 1] & 0x00ff00ffu) << 8);
+            const uint32_t odd0 = e4m3x2_to_bf16x2(f[2 * y]);
+            const uint32_t odd1 = e4m3x2_to_bf16x2(f[2 * y + 1]);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              mma16816(acc[t][2 * (c + y)], pa[t], even0, even1);
+              mma16816(acc[t][2 * (c + y) + 1], pa[t], odd0, odd1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            mma16816(acc[t][c], pa[t], f[0], f[1]);
+            mma16816(acc[t][c + 1], pa[t], f[2], f[3]);
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+
+    // the warps' sums meet: every row relative to the largest of the warps' maxima
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float sum = l[t][x];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        l[t][x] = sum;
+        if (j == 0) warp_m[warp][16 * t + 8 * x + row] = m[t][x];
+      }
+    __syncthreads();  // also: every warp is done with its stages
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = 16 * t + 8 * x + row;
+        float mx = warp_m[0][r];
+#pragma unroll
+        for (int y = 1; y < kWarps; ++y) mx = fmaxf(mx, warp_m[y][r]);
+        const float f = mx == -INFINITY ? 0.f : fast_exp2(m[t][x] - mx);
+        if (j == 0) warp_l[warp][r] = l[t][x] * f;
+        float* dst = sums + (static_cast<size_t>(warp) * kRows + r) * D;
+        if constexpr (kE4M3) {
+          // tiles 2 c and 2 c + 1 hold the even and odd channels of piece c: 4 in a row
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            reinterpret_cast<float4*>(dst + 16 * c)[j] =
+                make_float4(acc[t][2 * c][2 * x] * f, acc[t][2 * c + 1][2 * x] * f, acc[t][2 * c][2 * x + 1] * f,
+                            acc[t][2 * c + 1][2 * x + 1] * f);
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            reinterpret_cast<float2*>(dst + 8 * c)[j] = make_float2(acc[t][c][2 * x] * f, acc[t][c][2 * x + 1] * f);
+        }
+      }
+    __syncthreads();
+    constexpr int kLanes = D / 4;
+    for (int x = threadIdx.x; x < kRows * kLanes; x += kFewThreads) {
+      const int r = x / kLanes, c = x % kLanes;
+      int tok, head;
+      if (!P::row(s, a.group, p.u, r, tok, head)) continue;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f, mx = -INFINITY;
+#pragma unroll
+      for (int y = 0; y < kWarps; ++y) {
+        const float4 v = reinterpret_cast<const float4*>(sums + (static_cast<size_t>(y) * kRows + r) * D)[c];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+        sum += warp_l[y][r];
+        mx = fmaxf(mx, warp_m[y][r]);
+      }
+      if (p.slot < 0) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const long long at = static_cast<long long>(p.h * a.group + head) * a.c.total_new + s.a + tok;
+        uint2 pk;
+        pk.x = pack_bf16(o.x * inv, o.y * inv);
+        pk.y = pack_bf16(o.z * inv, o.w * inv);
+        reinterpret_cast<uint2*>(a.o + at * D)[c] = pk;
+        if (c == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+      } else {
+        const long long at = static_cast<long long>(p.slot) * kRows + r;
+        reinterpret_cast<float4*>(a.part_o + at * D)[c] = o;
+        if (c == 0) a.part_ml[at] = make_float2(mx, sum);
+      }
+    }
+    __syncthreads();  // the stages and the shared piece are free again
+  }
+}
+
+constexpr int kMaxFewBlocks = 320;   // two blocks to each of up to 160 SMs
+
+size_t few_workspace(int rows, int d) {
+  return static_cast<size_t>(2 * kMaxFewBlocks) * rows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2));
+}
+
+fcp_status sm_count(int* n) {
+  int dev = 0;
+  FCP_CUDA_TRY(cudaGetDevice(&dev), "paged attention device");
+  FCP_CUDA_TRY(cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev), "paged attention SM count");
+  return FCP_OK;
+}
+
+template <class P, int D>
+fcp_status launch_merge(const AttnArgs& a, int blocks, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, P::kRows / (128 / (D / 4)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<P, D>, a, blocks), "paged merge launch");
+  return FCP_OK;
+}
+
+template <int D, bool kE4M3, int MT>
+fcp_status launch_few(AttnArgs a, void* workspace, cudaStream_t s) {
+  using C = FewCfg<D, kE4M3>;
+  using P = FewRows<16 * MT>;
+  constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * D * 4);
+  int n_sm = 0;
+  if (const fcp_status st = sm_count(&n_sm); st != FCP_OK) return st;
+  const int blocks = std::min(2 * n_sm, kMaxFewBlocks);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * kMaxFewBlocks) * P::kRows * D);
+  FCP_CUDA_TRY(cudaFuncSetAttribute(few_kernel<D, kE4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+               "paged attention smem attribute");
+  few_kernel<D, kE4M3, MT><<<blocks, kFewThreads, kSmem, s>>>(a);
+  FCP_CUDA_TRY(cudaGetLastError(), "paged attention launch");
+  return launch_merge<P, D>(a, blocks, s);
+}
+
+template <int D>
+fcp_status launch_attn(const AttnArgs& a, int dtype, int max_new, void* workspace, cudaStream_t s) {
+  const bool wide = static_cast<long long>(max_new) * a.group > 16;
+  if (dtype == FCP_CACHE_E4M3)
+    return wide ? launch_few<D, true, 2>(a, workspace, s) : launch_few<D, true, 1>(a, workspace, s);
+  return wide ? launch_few<D, false, 2>(a, workspace, s) : launch_few<D, false, 1>(a, workspace, s);
+}
+
+}  // namespace
+}  // namespace fcp
+
+using namespace fcp;
+
+extern "C" size_t fcp_paged_attn_workspace_bytes(int32_t head_dim) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return few_workspace(32, head_dim);
+}
+
+extern "C" fcp_status fcp_paged_attn(const fcp_cache* cache, const fcp_cache_batch* batch, const void* q, int32_t hq,
+                                     int32_t causal, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  AttnArgs a;
+  if (const fcp_status st = paged_args(cache, batch, &a.c); st != FCP_OK) return st;
+  if (hq <= 0 || hq % cache->hkv != 0) return FCP_ERR_INVALID;
+  if (a.c.total_new == 0 || a.c.n_seqs == 0) return FCP_OK;
+  if (!q || !o || !lse || !workspace || !aligned16(q) || !aligned16(o) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return FCP_ERR_INVALID;
+  if (workspace_bytes < fcp_paged_attn_workspace_bytes(cache->head_dim)) return FCP_ERR_INVALID;
+  a.group = hq / cache->hkv;
+  a.causal = causal ? 1 : 0;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(cache->head_dim)));
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cache->head_dim == 128 ? launch_attn<128>(a, cache->dtype, batch->max_new, workspace, s)
+                                : launch_attn<64>(a, cache->dtype, batch->max_new, workspace, s);
+}

@@ -352,6 +352,87 @@ fcp_status fcp_block_attn_bwd_static_scratch(const fcp_plan* plan, const void* d
 fcp_status fcp_reshuffle(const fcp_plan* plan, const void* d_plan, const void* src, void* dst, int32_t heads,
                          int32_t row_bytes, int32_t direction, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Paged key/value cache and the attention that reads it (no counterpart on the pages, which
+ * stop at training: what a trained model answers with). A cache holds one layer's K and V in
+ * pages of page_size tokens:
+ *   k_pages, v_pages   [n_pages, Hkv, page_size, D], bf16 or e4m3
+ *   k_scales, v_scales [n_pages, Hkv, page_size] bytes, e4m3 caches only: the row (token, head)
+ *                      stands for code * 2^(byte - 127); byte 255 makes it NaN
+ * all contiguous and 16-byte aligned. page_size is a power of two, 16 to 4096; D is 64 or 128.
+ * status is one int32 on the device (16-byte aligned, zero at first), the error word of every call that uses
+ * the cache; read and clear it with fcp_device_error. 0x50: a sequence's offsets or length do
+ * not fit the batch (its rows are left as they were); 0x51: a block-table entry that was needed
+ * lies outside [0, n_pages) (a write or read leaves its row out, attention counts its keys as
+ * zeros). Neither stops the rest of the batch, and nothing outside the buffers is touched.
+ *
+ * A batch brings new tokens for n_seqs sequences, packed over total_new rows as everywhere in
+ * this library (tensors are [heads, total_new, D]): sequence i owns rows [cu_new[i],
+ * cu_new[i+1]), which may be none. lens[i] counts its tokens in the cache WITH the new ones, so
+ * its new token j is position lens[i] - n_i + j; position p is row p % page_size of page
+ * block_table[i][p / page_size]. The three arrays are int32 on the device and are read by the
+ * kernels, so a captured graph replays with whatever they hold then. Entries of block_table
+ * past a sequence's length are never looked at. Rows behind the last sequence (total_new >
+ * cu_new[n_seqs]) are left as they were. max_new says how many new tokens a sequence has at
+ * most; it only chooses the kernel (a wrong value costs time, never correctness). Several
+ * sequences may share pages for reading; two rows written to one place in one call leave one
+ * of them, or a mixture of both, there. */
+typedef enum { FCP_CACHE_BF16 = 0, FCP_CACHE_E4M3 = 1 } fcp_cache_dtype;
+
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int32_t* status;
+  int32_t n_pages, hkv, page_size, head_dim, dtype, reserved;
+} fcp_cache;
+
+typedef struct {
+  const int32_t* cu_new;      /* [n_seqs + 1] */
+  const int32_t* lens;        /* [n_seqs] */
+  const int32_t* block_table; /* [n_seqs, max_pages] */
+  int32_t n_seqs, max_pages, total_new, max_new;
+} fcp_cache_batch;
+
+/* Write the new tokens' K and V (bf16 [Hkv, total_new, D]) into their pages. An e4m3 cache
+ * quantises each row: with k the smallest integer >= -126 such that max|x| <= 448 * 2^k (k = 0
+ * for a row of zeros), the codes are x * 2^-k rounded to nearest even (at most 240 where k = 120:
+ * 256 * 2^120 is past bf16's range) and the scale byte is k + 127; a row that holds an infinity or NaN gets byte 255 and codes of zero. New tokens
+ * whose position is negative (n_i > lens[i]) are left out. Errors: FCP_ERR_INVALID (nulls,
+ * negative sizes, misaligned or missing buffers, an unknown dtype), FCP_ERR_UNSUPPORTED (D,
+ * page_size, more than 65536 sequences or 2^31 - 1 positions), FCP_ERR_CUDA. */
+fcp_status fcp_cache_write(const fcp_cache* cache, const fcp_cache_batch* batch, const void* k, const void* v,
+                           void* stream);
+
+/* The inverse: read the same rows of the cache back into bf16 k and v [Hkv, total_new, D]. A
+ * batch with n_i = lens[i] reads whole sequences, packed as fcp_block_attn_fwd takes them.
+ * Exact for a bf16 cache, and for an e4m3 one whose value code * 2^k is a normal bf16 number;
+ * writing what was read stores the same values again. Errors as fcp_cache_write. */
+fcp_status fcp_cache_read(const fcp_cache* cache, const fcp_cache_batch* batch, void* k, void* v, void* stream);
+
+/* Bytes of fcp_paged_attn's workspace: partial results of the groups that are split over
+ * blocks. It does not depend on the batch. 0 for an unsupported D. */
+size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
+
+/* Attention of the new tokens over their sequences' cached rows (Section 2.2's formula; Section
+ * 2.3's merge joins what was split): for every new token at position p of its sequence and every
+ * query head h, the softmax of q . k / sqrt(D) over the sequence's keys 0 .. p (causal != 0) or
+ * 0 .. lens[i] - 1 (causal = 0) of KV head h / (Hq / Hkv), giving o (bf16) and the natural
+ * log-sum-exp lse. q and o are [Hq, total_new, D], lse [Hq, total_new] float32. The new tokens'
+ * own K and V have to be in the cache already (fcp_cache_write). An e4m3 cache gives the
+ * attention over what fcp_cache_read returns. A row that sees no key gets o = 0, lse = -inf.
+ * Rows of the pages past a sequence's length may hold anything, NaN included; a NaN or infinity
+ * that a bf16 cache holds in V at a position of the sequence itself may reach the rows of the
+ * same batch that come before it. Sums, maxima and the softmax's statistics are float32; P is
+ * rounded to bf16 for the product with V. Results do not depend on timing: no atomics are
+ * used. workspace: fcp_paged_attn_workspace_bytes, 256-byte aligned, its contents need not be
+ * kept or cleared; calls whose work may overlap need one each. Errors: FCP_ERR_INVALID (also
+ * hq % hkv, a small or misaligned workspace), FCP_ERR_UNSUPPORTED and FCP_ERR_CUDA as
+ * fcp_cache_write. */
+fcp_status fcp_paged_attn(const fcp_cache* cache, const fcp_cache_batch* batch, const void* q, int32_t hq,
+                          int32_t causal, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, copy the device plan's error word to *code (0 = none; else the
  * kernel and wait that gave up) and clear it. Returns FCP_ERR_DEVICE if it was set. */
 fcp_status fcp_device_error(const void* d_plan, int32_t* code, void* stream);
