@@ -105,8 +105,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
   build_line<P, kFewThreads>(a, line, b == 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long total = line.prefix[kFewThreads];
-  const long long w0 = share_begin(total, b, blocks), w1 = share_begin(total, b + 1, blocks);
-  if (w0 >= w1) return;
+  const Shares sh(total, blocks);
+  if (threadIdx.x == 0) a.split[b].last = b;
+  if (b >= sh.blocks) return;
+  const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
 
   const uint32_t stages = smem_u32(smem) + warp * C::kWarpBytes;
   float* sums = reinterpret_cast<float*>(smem);  // [kWarps][kRows][D], over the stages at a piece's end
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
         p.ga = static_cast<int>(max(w0 - w.f0, 0ll));
         p.gb = static_cast<int>(min(w1 - w.f0, static_cast<long long>(w.g)));
         p.slot = piece_slot(b, p.ga, p.gb, w.g);
+        if (p.ga == 0 && p.gb < w.g) a.split[b] = SplitGroup{sh.owner(w.f0 + w.g - 1), w.s.a, w.s.n, w.h, w.u, {}};
       }
       shared_piece = p;
     }
@@ -455,10 +458,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
   }
 }
 
-constexpr int kMaxFewBlocks = 320;   // two blocks to each of up to 160 SMs
-
 size_t few_workspace(int rows, int d) {
-  return static_cast<size_t>(2 * kMaxFewBlocks) * rows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2));
+  return static_cast<size_t>(2 * kMaxBlocks) * rows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
+         kMaxBlocks * sizeof(SplitGroup);
 }
 
 fcp_status sm_count(int* n) {
@@ -471,15 +473,15 @@ fcp_status sm_count(int* n) {
 template <class P, int D>
 fcp_status launch_merge(const AttnArgs& a, int blocks, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, P::kRows / (128 / (D / 4)));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(blocks, 16);
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<P, D>, a, blocks), "paged merge launch");
+  FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<P, D>, a), "paged merge launch");
   return FCP_OK;
 }
 
@@ -490,9 +492,10 @@ fcp_status launch_few(AttnArgs a, void* workspace, cudaStream_t s) {
   constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * D * 4);
   int n_sm = 0;
   if (const fcp_status st = sm_count(&n_sm); st != FCP_OK) return st;
-  const int blocks = std::min(2 * n_sm, kMaxFewBlocks);
+  const int blocks = std::min(2 * n_sm, kMaxBlocks);
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * kMaxFewBlocks) * P::kRows * D);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * kMaxBlocks) * P::kRows * D);
+  a.split = reinterpret_cast<SplitGroup*>(a.part_ml + static_cast<size_t>(2 * kMaxBlocks) * P::kRows);
   FCP_CUDA_TRY(cudaFuncSetAttribute(few_kernel<D, kE4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
                "paged attention smem attribute");
   few_kernel<D, kE4M3, MT><<<blocks, kFewThreads, kSmem, s>>>(a);

@@ -15,7 +15,10 @@
 
 namespace fcp {
 
-constexpr int kGranule = 128;  // keys
+constexpr int kGranule = 128;    // keys
+constexpr int kMaxBlocks = 320;  // two blocks to each of up to 160 SMs
+
+struct SplitGroup;
 
 struct AttnArgs {
   PagedArgs c;
@@ -26,6 +29,7 @@ struct AttnArgs {
   float* lse;          // [Hq, T]
   float* part_o;       // [2 * blocks, kRows, D] unnormalised sums
   float2* part_ml;     // [2 * blocks, kRows] (row maximum in log2 units, row sum)
+  SplitGroup* split;     // [blocks]
   const __nv_bfloat16* q;
 };
 
@@ -159,9 +163,24 @@ __device__ __forceinline__ bool seek(const AttnArgs& a, const Line<kThreads>& li
   return true;
 }
 
-__device__ __forceinline__ long long share_begin(long long total, int b, int blocks) {
-  return total / blocks * b + total % blocks * b / blocks;
-}
+// The blocks' shares of a line of `total` granules: block b < blocks takes [begin(b), begin(b +
+// 1)), at least one granule (blocks is less than the grid where there are fewer granules).
+struct Shares {
+  long long base;
+  int rem, blocks;
+  __device__ __forceinline__ Shares(long long total, int grid)
+      : blocks(static_cast<int>(min(total, static_cast<long long>(grid)))) {
+    base = blocks > 0 ? total / blocks : 0;
+    rem = static_cast<int>(total - base * blocks);
+  }
+  __device__ __forceinline__ long long begin(int b) const { return base * b + rem * b / blocks; }
+  // The block that takes granule f.
+  __device__ __forceinline__ int owner(long long f) const {
+    int b = static_cast<int>(f / (base + 1));
+    while (begin(b + 1) <= f) ++b;
+    return b;
+  }
+};
 
 // Where a block's piece [ga, gb) of a group of g granules goes: the output itself when it is the
 // whole group, else the block's slot for a group it continues (0) or begins (1).
@@ -169,57 +188,91 @@ __device__ __forceinline__ int piece_slot(int b, int ga, int gb, int g) {
   return ga == 0 && gb == g ? -1 : 2 * b + (ga == 0 ? 1 : 0);
 }
 
-// Joins the pieces of the group that block b of the attention begins and does not finish: with
-// M the largest of the pieces' maxima, O = sum 2^(m - M) o / sum 2^(m - M) l. grid (blocks,
-// row slices): the pieces are read once, from L2, and most blocks find nothing to join.
-template <class P, int D>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const AttnArgs a, int blocks) {
-  __shared__ Line<128> line;
-  const int b = blockIdx.x;
-  build_line<P, 128>(a, line, false);
-  const long long total = line.prefix[128];
-  const long long w0 = share_begin(total, b, blocks), w1 = share_begin(total, b + 1, blocks);
-  Walk<P> w;
-  const bool mine = w0 < w1 && w1 < total && seek<P, 128>(a, line, w1 - 1, w) && w.f0 >= w0 && w.f0 + w.g > w1;
-  // the pieces are written (every block waits, so that this grid never ends before the attention)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!mine) return;
-  int last = b + 1;
-  while (last + 1 < blocks && share_begin(total, last + 1, blocks) < w.f0 + w.g) ++last;
+// The group that a block begins and does not finish, for the merge: blocks (b, last] continue it
+// (last = b: there is none).
+struct SplitGroup {
+  int32_t last, a, n, h, u;
+  int32_t reserved[3];
+};
+static_assert(sizeof(SplitGroup) == 32, "two 16-byte loads");
 
-  constexpr int kLanes = D / 4;              // threads to a row, 4 channels each
-  constexpr int kPer = 128 / kLanes;         // rows at a time
-  const int lane = threadIdx.x % kLanes;
-  for (int r = blockIdx.y * kPer + threadIdx.x / kLanes; r < P::kRows; r += kPer * gridDim.y) {
+// Joins the pieces of the groups that blocks split: with M the largest of a row's maxima,
+// O = sum 2^(m - M) o / sum 2^(m - M) l, over the pieces in their order. grid (blocks, row
+// slices); a block takes one row after another, its warps every fourth piece of it. Launched
+// so that it may start while the attention still runs: it waits for it in the kernel.
+constexpr int kMergeWarps = 4;
+template <class P, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const AttnArgs a) {
+  constexpr int kPieceLanes = D / 4;                             // lanes of a piece, 4 channels each
+  constexpr int kAtOnce = kMergeWarps * 32 / kPieceLanes;        // pieces at a time
+  __shared__ float weight[kMaxBlocks];
+  __shared__ float2 warp_ml[kMergeWarps];
+  __shared__ float4 part[kAtOnce][kPieceLanes];
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SplitGroup g = a.split[b];
+  const int count = g.last - b + 1;
+  if (count <= 1) return;
+  const SeqShape s{g.a, g.n, 0};
+  for (int r = blockIdx.y; r < P::kRows; r += gridDim.y) {
     int tok, head;
-    if (!P::row(w.s, a.group, w.u, r, tok, head)) continue;
+    if (!P::row(s, a.group, g.u, r, tok, head)) continue;
+    // piece x is in block b's second slot or block b + x's first
+    auto slot = [&](int x) { return static_cast<long long>(2 * (b + x) + (x == 0)) * P::kRows + r; };
     float m = -INFINITY;
-    for (int x = b; x <= last; ++x) {
-      if (x > b && share_begin(total, x, blocks) == share_begin(total, x + 1, blocks)) continue;
-      m = fmaxf(m, __ldcg(&a.part_ml[static_cast<long long>(2 * x + (x == b)) * P::kRows + r].x));
-    }
+    for (int x = tid; x < count; x += 32 * kMergeWarps) m = fmaxf(m, a.part_ml[slot(x)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) warp_ml[warp].x = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, warp_ml[w].x);
     const float mb = m == -INFINITY ? 0.f : m;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-    for (int x = b; x <= last; ++x) {
-      if (x > b && share_begin(total, x, blocks) == share_begin(total, x + 1, blocks)) continue;
-      const long long at = static_cast<long long>(2 * x + (x == b)) * P::kRows + r;
-      const float2 ml = __ldcg(&a.part_ml[at]);
+    for (int x = tid; x < count; x += 32 * kMergeWarps) {
+      const float2 ml = a.part_ml[slot(x)];
       const float f = exp2f(ml.x - mb);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
+      weight[x] = f;
       l = fmaf(f, ml.y, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) warp_ml[warp].y = l;
+    __syncthreads();
+    const int c = tid % kPieceLanes, x0 = tid / kPieceLanes;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = x0; x < count; x += kAtOnce) {
+      const float4 y = reinterpret_cast<const float4*>(a.part_o + slot(x) * D)[c];
+      const float f = weight[x];
       acc.x = fmaf(f, y.x, acc.x);
       acc.y = fmaf(f, y.y, acc.y);
       acc.z = fmaf(f, y.z, acc.z);
       acc.w = fmaf(f, y.w, acc.w);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const long long row = static_cast<long long>(w.h * a.group + head) * a.c.total_new + w.s.a + tok;
-    uint2 pk;
-    pk.x = dev::pack_bf16(acc.x * inv, acc.y * inv);
-    pk.y = dev::pack_bf16(acc.z * inv, acc.w * inv);
-    reinterpret_cast<uint2*>(a.o + row * D)[lane] = pk;
-    if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    part[x0][c] = acc;
+    __syncthreads();
+    if (tid < kPieceLanes) {
+      l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) l += warp_ml[w].y;
+#pragma unroll
+      for (int x = 1; x < kAtOnce; ++x) {
+        const float4 y = part[x][c];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const long long row = static_cast<long long>(g.h * a.group + head) * a.c.total_new + s.a + tok;
+      uint2 pk;
+      pk.x = dev::pack_bf16(acc.x * inv, acc.y * inv);
+      pk.y = dev::pack_bf16(acc.z * inv, acc.w * inv);
+      reinterpret_cast<uint2*>(a.o + row * D)[c] = pk;
+      if (c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+    __syncthreads();
   }
 }
 

@@ -12,17 +12,26 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _CacheStruct, _CacheBatchStruct, _check, _need, _stream, device_error, FcpError, lib
+from . import _CacheBatchStruct, _CacheStruct, _check, _need, _stream, device_error, FcpError, lib
 
 __all__ = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention"]
 
 _DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
 
-def _here(device) -> None:
-    """Kernels run on the current device, so that is where the tensors have to be."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {device}, the current device is cuda:{torch.cuda.current_device()}")
+def _here(device, stream) -> int:
+    """The stream to launch on. Kernels run on the current device, so that is where the tensors
+    have to be."""
+    index = torch._C._cuda_getDevice()
+    if device.index != index:
+        raise ValueError(f"the cache is on {device}, the current device is cuda:{index}")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+
+
+def _want(t, dtype, shape, name) -> None:
+    """_need, at the cost of a step's few microseconds in mind: the usual case is checked first."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, shape, name)
 
 
 class PagedCache:
@@ -117,12 +126,13 @@ class CacheBatch:
 
 def _move(fn, name, cache: PagedCache, batch: CacheBatch, k, v, stream) -> None:
     shape = (cache.hkv, batch.total_new, cache.head_dim)
-    _need(k, torch.bfloat16, shape, "k")
-    _need(v, torch.bfloat16, shape, "v")
+    _want(k, torch.bfloat16, shape, "k")
+    _want(v, torch.bfloat16, shape, "v")
     if not (k.device == v.device == batch.device == cache.device):
         raise ValueError("k, v, the batch and the cache must be on one device")
-    _here(cache.device)
-    _check(fn(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), _stream(stream)), name)
+    status = fn(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), _here(cache.device, stream))
+    if status:
+        _check(status, name)
 
 
 def cache_write(cache: PagedCache, batch: CacheBatch, k, v, stream=None) -> None:
@@ -141,17 +151,18 @@ def paged_attn(cache: PagedCache, batch: CacheBatch, q, o, lse, workspace, causa
     """Attention of the new tokens' queries q [Hq, total_new, D] over their sequences' cached rows,
     into o (bf16, as q) and lse (float32 [Hq, total_new]) (fcp_paged_attn). The new tokens' K and V
     must be in the cache. workspace: a CUDA uint8 tensor of fcp_paged_attn_workspace_bytes(D)."""
-    _need(q, torch.bfloat16, None, "q")
-    if q.dim() != 3 or q.shape[1] != batch.total_new or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q must have shape [Hq, {batch.total_new}, {cache.head_dim}], got {tuple(q.shape)}")
-    _need(o, torch.bfloat16, q.shape, "o")
-    _need(lse, torch.float32, q.shape[:2], "lse")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [Hq, total_new, D]")
+    shape = (q.shape[0], batch.total_new, cache.head_dim)
+    _want(q, torch.bfloat16, shape, "q")
+    _want(o, torch.bfloat16, shape, "o")
+    _want(lse, torch.float32, shape[:2], "lse")
     if not (q.device == o.device == lse.device == workspace.device == batch.device == cache.device):
         raise ValueError("q, o, lse, the workspace, the batch and the cache must be on one device")
-    _here(cache.device)
-    _check(lib().fcp_paged_attn(cache._ref, batch._ref, q.data_ptr(), q.shape[0], 1 if causal else 0, o.data_ptr(),
-                                lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                _stream(stream)), "fcp_paged_attn")
+    status = lib().fcp_paged_attn(cache._ref, batch._ref, q.data_ptr(), shape[0], 1 if causal else 0, o.data_ptr(),
+                                  lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _here(cache.device, stream))
+    if status:
+        _check(status, "fcp_paged_attn")
 
 
 class PagedAttention:
