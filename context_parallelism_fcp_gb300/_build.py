@@ -22,7 +22,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libfcp.so")
 
 SOURCES = ["fcp_plan.cpp", "fcp_solver.cpp", "fcp_validate.cpp", "fcp_fwd.cu", "fcp_bwd.cu", "fcp_bwd_tile.cu", "fcp_merge.cu",
-           "fcp_cache.cu", "fcp_paged_few.cu"]
+           "fcp_cache.cu", "fcp_paged_few.cu", "fcp_paged_chunk.cu"]
 HEADERS = ["fcp_internal.h", "fcp_cuda_util.h", "fcp_sm100.cuh", "fcp_paged.h",
            "fcp_paged_sched.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

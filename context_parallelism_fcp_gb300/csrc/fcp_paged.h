@@ -21,6 +21,7 @@ namespace fcp {
 enum CacheError : int32_t {
   kErrCacheBatch = 0x50,  // a sequence's row offsets or length do not fit the batch
   kErrCachePage = 0x51,   // a block-table entry that is needed is outside [0, n_pages)
+  kErrPagedWait = 0x60,   // .. 0x6f: a bounded wait of the chunk kernel gave up
 };
 
 // What the kernels need of fcp_cache and fcp_cache_batch.

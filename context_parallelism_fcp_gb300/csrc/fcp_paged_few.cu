@@ -458,11 +458,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
   }
 }
 
-size_t few_workspace(int rows, int d) {
-  return static_cast<size_t>(2 * kMaxBlocks) * rows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
-         kMaxBlocks * sizeof(SplitGroup);
-}
-
 fcp_status sm_count(int* n) {
   int dev = 0;
   FCP_CUDA_TRY(cudaGetDevice(&dev), "paged attention device");
@@ -470,45 +465,33 @@ fcp_status sm_count(int* n) {
   return FCP_OK;
 }
 
-template <class P, int D>
-fcp_status launch_merge(const AttnArgs& a, int blocks, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, 16);
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<P, D>, a), "paged merge launch");
-  return FCP_OK;
-}
-
 template <int D, bool kE4M3, int MT>
-fcp_status launch_few(AttnArgs a, void* workspace, cudaStream_t s) {
+fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaStream_t s) {
   using C = FewCfg<D, kE4M3>;
   using P = FewRows<16 * MT>;
   constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * D * 4);
-  int n_sm = 0;
-  if (const fcp_status st = sm_count(&n_sm); st != FCP_OK) return st;
   const int blocks = std::min(2 * n_sm, kMaxBlocks);
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * kMaxBlocks) * P::kRows * D);
-  a.split = reinterpret_cast<SplitGroup*>(a.part_ml + static_cast<size_t>(2 * kMaxBlocks) * P::kRows);
+  set_workspace<P>(a, workspace, D, kMaxBlocks);
   FCP_CUDA_TRY(cudaFuncSetAttribute(few_kernel<D, kE4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
                "paged attention smem attribute");
   few_kernel<D, kE4M3, MT><<<blocks, kFewThreads, kSmem, s>>>(a);
   FCP_CUDA_TRY(cudaGetLastError(), "paged attention launch");
-  return launch_merge<P, D>(a, blocks, s);
+  const long long rows = static_cast<long long>(std::max(max_new, 1)) * a.group;
+  return launch_merge<P, D>(a, blocks, static_cast<int>(std::min<long long>(rows, 16)), s);
 }
 
 template <int D>
-fcp_status launch_attn(const AttnArgs& a, int dtype, int max_new, void* workspace, cudaStream_t s) {
-  const bool wide = static_cast<long long>(max_new) * a.group > 16;
+fcp_status launch_attn(const AttnArgs& a, int dtype, int hq, int max_new, void* workspace, cudaStream_t s) {
+  int n_sm = 0;
+  if (const fcp_status st = sm_count(&n_sm); st != FCP_OK) return st;
+  const long long rows = static_cast<long long>(max_new) * a.group;
+  if (rows > 32 && dtype == FCP_CACHE_BF16) return launch_paged_chunk(a, dtype, D, hq, workspace, n_sm, s);
+  const bool wide = rows > 16;
   if (dtype == FCP_CACHE_E4M3)
-    return wide ? launch_few<D, true, 2>(a, workspace, s) : launch_few<D, true, 1>(a, workspace, s);
-  return wide ? launch_few<D, false, 2>(a, workspace, s) : launch_few<D, false, 1>(a, workspace, s);
+    return wide ? launch_few<D, true, 2>(a, workspace, n_sm, max_new, s)
+                : launch_few<D, true, 1>(a, workspace, n_sm, max_new, s);
+  return wide ? launch_few<D, false, 2>(a, workspace, n_sm, max_new, s)
+              : launch_few<D, false, 1>(a, workspace, n_sm, max_new, s);
 }
 
 }  // namespace
@@ -518,7 +501,7 @@ using namespace fcp;
 
 extern "C" size_t fcp_paged_attn_workspace_bytes(int32_t head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
-  return few_workspace(32, head_dim);
+  return std::max(workspace_bytes(ChunkRows::kRows, head_dim, kMaxChunkBlocks), workspace_bytes(32, head_dim, kMaxBlocks));
 }
 
 extern "C" fcp_status fcp_paged_attn(const fcp_cache* cache, const fcp_cache_batch* batch, const void* q, int32_t hq,
@@ -539,6 +522,6 @@ extern "C" fcp_status fcp_paged_attn(const fcp_cache* cache, const fcp_cache_bat
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cache->head_dim == 128 ? launch_attn<128>(a, cache->dtype, batch->max_new, workspace, s)
-                                : launch_attn<64>(a, cache->dtype, batch->max_new, workspace, s);
+  return cache->head_dim == 128 ? launch_attn<128>(a, cache->dtype, hq, batch->max_new, workspace, s)
+                                : launch_attn<64>(a, cache->dtype, hq, batch->max_new, workspace, s);
 }

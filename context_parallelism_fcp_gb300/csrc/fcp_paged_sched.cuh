@@ -16,7 +16,8 @@
 namespace fcp {
 
 constexpr int kGranule = 128;    // keys
-constexpr int kMaxBlocks = 320;  // two blocks to each of up to 160 SMs
+constexpr int kMaxBlocks = 320;       // few rows: two blocks to each of up to 160 SMs
+constexpr int kMaxChunkBlocks = 160;  // chunks: one
 
 struct SplitGroup;
 
@@ -57,6 +58,37 @@ struct FewRows {
     tok = static_cast<int>(x / group);
     head = static_cast<int>(x - static_cast<long long>(tok) * group);
     return tok < s.n;
+  }
+};
+
+// Chunks: a tile is 2^log_tokens new tokens of `heads` query heads (128 rows, head by head), the
+// tiles of a KV head are ordered tokens first, heads within them, and a unit is two of them.
+struct ChunkRows {
+  static constexpr int kRows = 2 * kTileM;
+  struct Shape {
+    int log_tokens, heads, head_tiles, tiles;
+    __device__ __forceinline__ Shape(const SeqShape& s, int group) {
+      log_tokens = s.n > 64 ? 7 : (s.n > 32 ? 6 : (s.n > 16 ? 5 : 4));
+      heads = kTileM >> log_tokens;
+      head_tiles = (group + heads - 1) / heads;
+      tiles = head_tiles * ((s.n + (1 << log_tokens) - 1) >> log_tokens);
+    }
+  };
+  static __device__ __forceinline__ int units(const SeqShape& s, int group) { return (Shape(s, group).tiles + 1) >> 1; }
+  static __device__ __forceinline__ int tiles_of(const SeqShape& s, int group, int u) {
+    return min(2, Shape(s, group).tiles - 2 * u);
+  }
+  static __device__ __forceinline__ int end(const SeqShape& s, int group, int u, int causal) {
+    const Shape z(s, group);
+    const int x = min(2 * u + 1, z.tiles - 1);
+    return key_end(s, ((x / z.head_tiles + 1) << z.log_tokens) - 1, causal);
+  }
+  static __device__ __forceinline__ bool row(const SeqShape& s, int group, int u, int r, int& tok, int& head) {
+    const Shape z(s, group);
+    const int x = 2 * u + (r >> 7), rr = r & (kTileM - 1);
+    tok = ((x / z.head_tiles) << z.log_tokens) + (rr & ((1 << z.log_tokens) - 1));
+    head = (x % z.head_tiles) * z.heads + (rr >> z.log_tokens);
+    return x < z.tiles && tok < s.n && head < group;
   }
 };
 
@@ -275,5 +307,36 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Att
     __syncthreads();
   }
 }
+
+// Partial results, their statistics and the split groups' descriptors of a grid of up to
+// `blocks` blocks.
+inline size_t workspace_bytes(int rows, int d, int blocks) {
+  return static_cast<size_t>(2 * blocks) * rows * (static_cast<size_t>(d) * sizeof(float) + sizeof(float2)) +
+         blocks * sizeof(SplitGroup);
+}
+template <class P>
+inline void set_workspace(AttnArgs& a, void* workspace, int d, int blocks) {
+  const size_t rows = static_cast<size_t>(2 * blocks) * P::kRows;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * d);
+  a.split = reinterpret_cast<SplitGroup*>(a.part_ml + rows);
+}
+
+template <class P, int D>
+inline fcp_status launch_merge(const AttnArgs& a, int blocks, int slices, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, slices);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<P, D>, a), "paged merge launch");
+  return FCP_OK;
+}
+
+fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int n_sm, cudaStream_t s);
 
 }  // namespace fcp

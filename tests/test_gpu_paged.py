@@ -179,3 +179,31 @@ def test_attention_is_the_same_every_time(fcp, c):
     for _ in range(3):
         again = attend(fcp, b, t, cache, batch)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+# ---------------------------------------------------------------- attention, chunks
+CHUNK = [
+    Batch([40], [40]),
+    Batch([40], [40], hq=1, hkv=1, d=128),
+    Batch([17, 33, 65, 16], [17, 100, 65, 400], hq=8, hkv=1, d=128, pad=2),
+    Batch([128, 1, 0, 129], [128, 300, 77, 1000], hq=4, hkv=4, d=128, page=32),
+    Batch([200, 64], [1500, 64], hq=6, hkv=2, page=64),
+    Batch([300], [300], hq=5, hkv=1, d=128, page=128, causal=False),
+    Batch([90, 130], [60, 129], hq=3, hkv=1, d=128),                     # rows before position 0 see nothing
+    Batch([70, 5], [0, 700], causal=False),                              # a sequence with no cached rows
+    Batch([34, 1, 1, 1], [5000, 4000, 129, 128], hq=8, hkv=1, d=128, page=256),
+    Batch([1] * 40 + [35], [(i * 53) % 300 for i in range(40)] + [35], hq=2, hkv=1),
+    Batch([513], [2049], hq=2, hkv=1, page=512, std=3.0, pad=1),
+    Batch([3, 2], [900, 100], hq=4, hkv=2, d=128, max_new=500),          # a wrong max_new is only slow
+    Batch([35, 20], [300, 20], hq=300, hkv=2),                           # 150 heads to a KV head
+]
+CHUNK = [b.__class__(**{**b.__dict__, "cache": c, "seed": 50 + i}) for i, b in enumerate(CHUNK) for c in ("bf16", "e4m3")]
+
+
+@pytest.mark.parametrize("b", CHUNK, ids=str)
+def test_attention_of_chunks(fcp, b):
+    t = U.make(b)
+    cache, batch = U.handles(fcp, b, t)
+    o, lse, before = attend(fcp, b, t, cache, batch)
+    cache.check_device_error()
+    U.check_attention(b, t, o, lse, *before)
