@@ -89,7 +89,39 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-template <int D>
+// 16 codes and their row's scale byte as 16 bf16 channels: code * 2^(byte - 127). The code's bits
+// in bf16's fields are code * 2^-120, and 2^120 is taken into the scale where bf16 holds the
+// product of both; larger scales take two exact products.
+__device__ __forceinline__ void scaled16(const uint4 x, uint32_t byte, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t y = __byte_perm(w[i], 0, j ? 0x3424 : 0x1404);
+      r[2 * i + j] = (y & 0x80008000u) | ((y & 0x7f007f00u) >> 4);
+    }
+  auto times = [&](uint32_t f) {
+    f |= f << 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 y =
+          __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]), *reinterpret_cast<const __nv_bfloat162*>(&f));
+      r[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+  };
+  if (byte <= 134u) {
+    times((byte + 120u) << 7);
+  } else {
+    times(254u << 7);
+    times(byte == 255u ? 0x7fc0u : (byte - 7u) << 7);
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+template <int D, bool kE4M3>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const AttnArgs a) {
   using C = Cfg<D>;
@@ -177,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ loaders
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoader));
     const int tid = threadIdx.x - 12 * 32;
-    constexpr int kLanes = D / 8;              // threads to a row, 16 bytes each
+    constexpr int kLanes = kE4M3 ? D / 16 : D / 8;  // threads to a row, 16 bytes of it each
     constexpr int kRowsAtOnce = 128 / kLanes;
     constexpr int kPasses = kTileN / kRowsAtOnce;
     const int r0 = tid / kLanes, c = tid % kLanes;
-    // piece c of row r of a tile: 128-byte rows of a 64-channel panel, XOR-swizzled by r & 7
+    // 16-byte piece p of row r of a tile: 128-byte rows of 64-channel panels, XOR-swizzled by r & 7
     // (r = r0 + a multiple of 8, so the swizzle is the thread's own)
-    const uint32_t off = (c >> 3) * kPanelBytes + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4);
+    auto piece = [&](int p) -> uint32_t { return (p >> 3) * kPanelBytes + r0 * 128 + (((p & 7) ^ (r0 & 7)) << 4); };
     const int page_mask = (1 << a.c.page_shift) - 1;
     bool ok = true;
     int J = 0;
@@ -198,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit t = next_unit(v, kErrPagedWait + 1);
       if (t.valid <= 0) break;
       const int* table = a.c.table + static_cast<long long>(t.i) * a.c.max_pages;
-      // lane l < 8 looks up the page of the tile's keys [16 l, 16 l + 16)
+      // lane l < 8 looks up the page of the tile's keys [16 l, 16 l + 16); -1: nothing to read
       auto lookup = [&](int kt) -> int {
         const int key = kt * kTileN + 16 * (lane & 7);
-        if (kt >= t.kt1 || key >= t.len) return 0;
+        if (kt >= t.kt1 || key >= t.len) return -1;
         const int pg = __ldg(table + (key >> a.c.page_shift));
         if (pg < 0 || pg >= a.c.n_pages) {
           atomicCAS(err, 0, kErrCachePage);
@@ -210,31 +242,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         return pg;
       };
       int page_next = lookup(t.kt0);
-      for (int kt = t.kt0; kt < t.kt1 && ok; ++kt, ++J) {
-        const int page = page_next;
-        page_next = lookup(kt + 1);
-        const int s = J & 1;
-        const uint32_t ph = (J >> 1) & 1;
+      // pass x of key tile kt: its row of the cache; false for rows that become zeros
+      auto row_of = [&](int page, int kt, int x, long long& row) -> bool {
+        const int pg = __shfl_sync(0xffffffffu, page, (x * kRowsAtOnce + (kRowsAtOnce > 16 ? r0 & 16 : 0)) >> 4);
+        const int key = kt * kTileN + r0 + x * kRowsAtOnce;
+        row = page_row(a.c, pg, t.h) + (key & page_mask);
+        return key < t.len && pg >= 0;
+      };
+      if constexpr (!kE4M3) {
+        const uint32_t off = piece(c);
+        for (int kt = t.kt0; kt < t.kt1 && ok; ++kt, ++J) {
+          const int page = page_next;
+          page_next = lookup(kt + 1);
+          const int s = J & 1;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = ok && mbar_wait(bar((kv ? B_VEMPTY : B_KEMPTY) + s), ph ^ 1, abort_flag, err, kErrPagedWait + 2);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint8_t* pages = kv ? a.c.v_pages : a.c.k_pages;
-          const uint32_t dst = sb + (kv ? C::kV : C::kK) + s * C::kTileBytes + off;
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = ok && mbar_wait(bar((kv ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t* pages = kv ? a.c.v_pages : a.c.k_pages;
+            const uint32_t dst = sb + (kv ? C::kV : C::kK) + s * C::kTileBytes + off;
 #pragma unroll
-          for (int x = 0; x < kPasses; ++x) {
-            const int r = r0 + x * kRowsAtOnce;
-            const int pg = __shfl_sync(0xffffffffu, page, (x * kRowsAtOnce) >> 4);
-            const int key = kt * kTileN + r;
-            const bool on = key < t.len && pg >= 0;
-            const long long row = page_row(a.c, pg, t.h) + (key & page_mask);
-            cp_async16(dst + x * kRowsAtOnce * 128, pages + (on ? row * (2 * D) + c * 16 : 0), on);
+            for (int x = 0; x < kPasses; ++x) {
+              long long row;
+              const bool on = row_of(page, kt, x, row);
+              cp_async16(dst + x * kRowsAtOnce * 128, pages + (on ? row * (2 * D) + c * 16 : 0), on);
+            }
+            cp_commit();
+            cp_wait<1>();  // the copies before these have arrived: theirs is the tile to hand over
+            signal();
+            pending = (kv ? B_VFULL : B_KFULL) + s;
           }
-          cp_commit();
-          cp_wait<1>();  // the copies before these have arrived: theirs is the tile to hand over
-          signal();
-          pending = (kv ? B_VFULL : B_KFULL) + s;
+        }
+      } else {
+        // The codes of a half step (K or V of a tile) are loaded while the half step before is
+        // turned into bf16: as soon as a register is converted, its next load goes out.
+        uint4 raw[kPasses];
+        uint32_t byte[kPasses];
+        auto load = [&](int page, int kt, int kv, int x) {
+          long long row;
+          const bool on = row_of(page, kt, x, row);
+          raw[x] = make_uint4(0u, 0u, 0u, 0u);
+          byte[x] = 127u;
+          if (on) {
+            raw[x] = __ldg(reinterpret_cast<const uint4*>((kv ? a.c.v_pages : a.c.k_pages) + row * D) + c);
+            byte[x] = __ldg((kv ? a.c.v_scales : a.c.k_scales) + row);
+          }
+        };
+        // lanes of the row's other panel store their two pieces in the other order, so that the
+        // eight lanes of a row always hit different banks
+        const uint32_t swap = (c >> 2) & 1;
+        const uint32_t off0 = piece(2 * c + swap), off1 = piece(2 * c + 1 - swap);
+#pragma unroll
+        for (int x = 0; x < kPasses; ++x) load(page_next, t.kt0, 0, x);
+        for (int kt = t.kt0; kt < t.kt1 && ok; ++kt, ++J) {
+          const int page = page_next;
+          page_next = lookup(kt + 1);
+          const int s = J & 1;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = ok && mbar_wait(bar((kv ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t* dst = smem + (kv ? C::kV : C::kK) + s * C::kTileBytes;
+#pragma unroll
+            for (int x = 0; x < kPasses; ++x) {
+              const uint4 y = raw[x];
+              const uint32_t f = byte[x];
+              load(kv ? page_next : page, kt + kv, 1 - kv, x);
+              uint4 lo, hi;
+              scaled16(y, f, lo, hi);
+              *reinterpret_cast<uint4*>(dst + off0 + x * kRowsAtOnce * 128) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(dst + off1 + x * kRowsAtOnce * 128) = swap ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive_warp(bar((kv ? B_VFULL : B_KFULL) + s));
+          }
         }
       }
     }
@@ -602,16 +685,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kE4M3>
 fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s) {
   using C = Cfg<D>;
   CUtensorMap mq;
   if (const fcp_status st = make_bf16_map(&mq, a.q, hq, a.c.total_new, D, kQBox); st != FCP_OK) return st;
   const int blocks = std::min(n_sm, kMaxChunkBlocks);
   set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
-  FCP_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes),
+  FCP_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes),
                "paged chunk smem attribute");
-  chunk_kernel<D><<<blocks, kThreads, C::kSmemBytes, s>>>(mq, a);
+  chunk_kernel<D, kE4M3><<<blocks, kThreads, C::kSmemBytes, s>>>(mq, a);
   FCP_CUDA_TRY(cudaGetLastError(), "paged chunk launch");
   return launch_merge<ChunkRows, D>(a, blocks, 32, s);
 }
@@ -619,8 +702,9 @@ fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s)
 }  // namespace
 
 fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int n_sm, cudaStream_t s) {
-  if (dtype != FCP_CACHE_BF16) return FCP_ERR_UNSUPPORTED;
-  return d == 128 ? launch<128>(a, workspace, n_sm, hq, s) : launch<64>(a, workspace, n_sm, hq, s);
+  if (dtype == FCP_CACHE_E4M3)
+    return d == 128 ? launch<128, true>(a, workspace, n_sm, hq, s) : launch<64, true>(a, workspace, n_sm, hq, s);
+  return d == 128 ? launch<128, false>(a, workspace, n_sm, hq, s) : launch<64, false>(a, workspace, n_sm, hq, s);
 }
 
 }  // namespace fcp

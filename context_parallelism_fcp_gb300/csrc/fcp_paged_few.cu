@@ -485,7 +485,7 @@ fcp_status launch_attn(const AttnArgs& a, int dtype, int hq, int max_new, void* 
   int n_sm = 0;
   if (const fcp_status st = sm_count(&n_sm); st != FCP_OK) return st;
   const long long rows = static_cast<long long>(max_new) * a.group;
-  if (rows > 32 && dtype == FCP_CACHE_BF16) return launch_paged_chunk(a, dtype, D, hq, workspace, n_sm, s);
+  if (rows > 32) return launch_paged_chunk(a, dtype, D, hq, workspace, n_sm, s);
   const bool wide = rows > 16;
   if (dtype == FCP_CACHE_E4M3)
     return wide ? launch_few<D, true, 2>(a, workspace, n_sm, max_new, s)
