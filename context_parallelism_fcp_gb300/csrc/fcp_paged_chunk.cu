@@ -8,16 +8,18 @@
 //
 // As in the forward over a work list, S_t = Q_t K^T and O_t += P_t V run on the tensor core
 // with accumulators in tensor memory while the other tile's softmax runs; what differs is where
-// keys come from. A key tile is 128 positions, gathered from their pages by four loader warps
-// into the 128-byte-swizzled layout that the matrix instructions read: as asynchronous copies
-// for bf16, and for e4m3 through registers, where each row is scaled by its power of two. That
-// product is exact, so the kernel computes the attention over what reading the cache gives, and
-// the tensor core runs the same bf16 instructions for both. Rows past the sequence become zeros,
-// since a zero weight times NaN is NaN.
+// keys come from. A key tile is 128 positions, gathered from their pages into the
+// 128-byte-swizzled layout that the matrix instructions read: a bf16 cache by TMA, one box for
+// each page and 64 channels, an e4m3 cache by six warps that turn codes into scaled bf16 on
+// their way to shared memory. That product with a power of two is exact, so the kernel computes
+// the attention over what reading the cache gives, and the tensor core runs the same bf16
+// instructions for both. Rows of V past the sequence become zeros, since a zero weight times
+// whatever such a row holds may be NaN.
 //
-// 16 warps: 0-3 and 4-7 softmax of tile 0 and 1 (thread = row = TMEM lane), 8 the walk along
-// the block's share of the work and Q's TMA loads, 9 MMA, 12-15 loaders. TMEM columns: S_t at
-// [128 t, 128 t + 128), overwritten by P_t as bf16; O_t at [256 + 128 t, 256 + 128 t + D).
+// Warps 0-3 and 4-7: softmax of tile 0 and 1 (thread = row = TMEM lane); 8: the walk along the
+// block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 only): loaders.
+// TMEM columns: S_t at [128 t, 128 t + 128), overwritten by P_t as bf16; O_t at [256 + 128 t,
+// 256 + 128 t + D).
 #include <algorithm>
 #include <cmath>
 
@@ -28,13 +30,16 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreads = 512;
+constexpr int kLoaders = 6;  // warps
+template <bool kE4M3>
+constexpr int kThreads = 32 * (10 + (kE4M3 ? kLoaders : 0));
 constexpr int kPanelBytes = kTileM * 128;  // 128 rows x 64 bf16 channels
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr int kQBox = 16;                   // tokens of one TMA load of Q
-// registers a thread: the launch gives 128; softmax warps take what the others leave
-constexpr int kRegsSoftmax = 176, kRegsControl = 64, kRegsLoader = 96;
-static_assert(2 * kRegsSoftmax + kRegsControl + kRegsLoader <= 4 * 128, "the split fits the launch's registers");
+// Registers a thread with the loader warps: the launch gives 128, and the softmax warps take
+// what the others leave (they hold a row of 128 scores).
+constexpr int kRegsSoftmax = 176, kRegsOther = 80;
+static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * 128, "the split fits the launch's registers");
 
 enum : int {
   B_QFULL = 0,
@@ -49,7 +54,7 @@ enum : int {
   B_OFREE = 18,  // per tile: the epilogue has read O_t out of TMEM
   B_DRAIN = 20,
   B_TFULL = 21,   // 2 slots: the next unit is published
-  B_TEMPTY = 23,  // 2 slots: 13 warps (MMA, softmax, loaders) have read it
+  B_TEMPTY = 23,  // 2 slots: the MMA, softmax and loader warps have read it
   B_COUNT = 25
 };
 
@@ -79,15 +84,6 @@ struct Cfg {
   static constexpr uint32_t kIdescS = idesc_bf16(kTileM, kTileN, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16(kTileM, D, false, true);
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int n>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
-}
 
 // 16 codes and their row's scale byte as 16 bf16 channels: code * 2^(byte - 127). The code's bits
 // in bf16's fields are code * 2^-120, and 2^120 is taken into the scale where bf16 holds the
@@ -122,8 +118,10 @@ __device__ __forceinline__ void scaled16(const uint4 x, uint32_t byte, uint4& lo
 }
 
 template <int D, bool kE4M3>
-__global__ void __launch_bounds__(kThreads, 1)
-    chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads<kE4M3>, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+  constexpr int kThreads = fcp::kThreads<kE4M3>;
   using C = Cfg<D>;
   using P = ChunkRows;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -179,9 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B_QFULL), 1);
     mbar_init(bar(B_QEMPTY), 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_KFULL + s), 4);  // one arrival per loader warp
+      mbar_init(bar(B_KFULL + s), kE4M3 ? 8 : 1);  // one arrival per 16 rows, or the copies' bytes
       mbar_init(bar(B_KEMPTY + s), 1);
-      mbar_init(bar(B_VFULL + s), 4);
+      mbar_init(bar(B_VFULL + s), kE4M3 ? 8 : 1);
       mbar_init(bar(B_VEMPTY + s), 1);
       mbar_init(bar(B_SFULL + s), 1);
       mbar_init(bar(B_PFULL + 2 * s), 4);  // one arrival per softmax warp of the tile
@@ -189,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_ODONE + s), 1);
       mbar_init(bar(B_OFREE + s), 4);
       mbar_init(bar(B_TFULL + s), 1);
-      mbar_init(bar(B_TEMPTY + s), 13);
+      mbar_init(bar(B_TEMPTY + s), 9 + (kE4M3 ? kLoaders : 0));
     }
     mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0;
@@ -205,126 +203,91 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 12) {
-    // ------------------------------------------------------------ loaders
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoader));
-    const int tid = threadIdx.x - 12 * 32;
-    constexpr int kLanes = kE4M3 ? D / 16 : D / 8;  // threads to a row, 16 bytes of it each
-    constexpr int kRowsAtOnce = 128 / kLanes;
-    constexpr int kPasses = kTileN / kRowsAtOnce;
-    const int r0 = tid / kLanes, c = tid % kLanes;
-    // 16-byte piece p of row r of a tile: 128-byte rows of 64-channel panels, XOR-swizzled by r & 7
-    // (r = r0 + a multiple of 8, so the swizzle is the thread's own)
-    auto piece = [&](int p) -> uint32_t { return (p >> 3) * kPanelBytes + r0 * 128 + (((p & 7) ^ (r0 & 7)) << 4); };
-    const int page_mask = (1 << a.c.page_shift) - 1;
-    bool ok = true;
-    int J = 0;
-    int pending = -1;  // barrier of the copies that are in flight and not signalled
-    auto signal = [&]() {
-      if (pending >= 0) {
-        fence_proxy_async_smem();
-        mbar_arrive_warp(bar(pending));
-      }
-    };
-    for (int v = 0; ok; ++v) {
-      const Unit t = next_unit(v, kErrPagedWait + 1);
-      if (t.valid <= 0) break;
-      const int* table = a.c.table + static_cast<long long>(t.i) * a.c.max_pages;
-      // lane l < 8 looks up the page of the tile's keys [16 l, 16 l + 16); -1: nothing to read
-      auto lookup = [&](int kt) -> int {
-        const int key = kt * kTileN + 16 * (lane & 7);
-        if (kt >= t.kt1 || key >= t.len) return -1;
-        const int pg = __ldg(table + (key >> a.c.page_shift));
-        if (pg < 0 || pg >= a.c.n_pages) {
-          atomicCAS(err, 0, kErrCachePage);
-          return -1;
-        }
-        return pg;
-      };
-      int page_next = lookup(t.kt0);
-      // pass x of key tile kt: its row of the cache; false for rows that become zeros
-      auto row_of = [&](int page, int kt, int x, long long& row) -> bool {
-        const int pg = __shfl_sync(0xffffffffu, page, (x * kRowsAtOnce + (kRowsAtOnce > 16 ? r0 & 16 : 0)) >> 4);
-        const int key = kt * kTileN + r0 + x * kRowsAtOnce;
-        row = page_row(a.c, pg, t.h) + (key & page_mask);
-        return key < t.len && pg >= 0;
-      };
-      if constexpr (!kE4M3) {
-        const uint32_t off = piece(c);
-        for (int kt = t.kt0; kt < t.kt1 && ok; ++kt, ++J) {
-          const int page = page_next;
-          page_next = lookup(kt + 1);
-          const int s = J & 1;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = ok && mbar_wait(bar((kv ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint8_t* pages = kv ? a.c.v_pages : a.c.k_pages;
-            const uint32_t dst = sb + (kv ? C::kV : C::kK) + s * C::kTileBytes + off;
-#pragma unroll
-            for (int x = 0; x < kPasses; ++x) {
-              long long row;
-              const bool on = row_of(page, kt, x, row);
-              cp_async16(dst + x * kRowsAtOnce * 128, pages + (on ? row * (2 * D) + c * 16 : 0), on);
-            }
-            cp_commit();
-            cp_wait<1>();  // the copies before these have arrived: theirs is the tile to hand over
-            signal();
-            pending = (kv ? B_VFULL : B_KFULL) + s;
-          }
-        }
-      } else {
-        // The codes of a half step (K or V of a tile) are loaded while the half step before is
-        // turned into bf16: as soon as a register is converted, its next load goes out.
+  if (warp >= 8) {
+    if constexpr (kE4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp >= 10) {
+      // ---------------------------------------------------------- loaders (e4m3)
+      // The 16-row groups of K of a tile, then of V, then of the next tile's K, go round the loader
+      // warps; a group lies in one page. Lane l turns codes [16 (l % kLanes), + 16) of rows l /
+      // kLanes + kRowsAtOnce x into 32 bytes of bf16. A warp's next group is loaded before its
+      // current one is converted.
+      constexpr int kLanes = D / 16;
+      constexpr int kRowsAtOnce = 32 / kLanes;
+      constexpr int kPasses = 16 / kRowsAtOnce;
+      const int r0 = lane / kLanes, c = lane % kLanes;
+      const int page_mask = (1 << a.c.page_shift) - 1;
+      bool ok = true;
+      int J0 = 0;       // key tiles before this unit
+      int skip = warp - 10;  // groups of this unit that come before the warp's first
+      for (int v = 0; ok; ++v) {
+        const Unit t = next_unit(v, kErrPagedWait + 1);
+        if (t.valid <= 0) break;
+        const int* table = a.c.table + static_cast<long long>(t.i) * a.c.max_pages;
+        const int n_groups = (t.kt1 - t.kt0) * 16;
         uint4 raw[kPasses];
         uint32_t byte[kPasses];
-        auto load = [&](int page, int kt, int kv, int x) {
-          long long row;
-          const bool on = row_of(page, kt, x, row);
-          raw[x] = make_uint4(0u, 0u, 0u, 0u);
-          byte[x] = 127u;
-          if (on) {
-            raw[x] = __ldg(reinterpret_cast<const uint4*>((kv ? a.c.v_pages : a.c.k_pages) + row * D) + c);
-            byte[x] = __ldg((kv ? a.c.v_scales : a.c.k_scales) + row);
+        auto load = [&](int gi) {
+          const int key0 = (t.kt0 + (gi >> 4)) * kTileN + 16 * (gi & 7);
+          int page = -1;
+          if (gi < n_groups && key0 < t.len) {
+            page = __ldg(table + (key0 >> a.c.page_shift));
+            if (page < 0 || page >= a.c.n_pages) {
+              atomicCAS(err, 0, kErrCachePage);
+              page = -1;
+            }
+          }
+          const bool is_v = (gi & 8) != 0;
+          const long long row0 = page >= 0 ? page_row(a.c, page, t.h) + (key0 & page_mask) : 0;
+          const uint8_t* src = (is_v ? a.c.v_pages : a.c.k_pages) + row0 * D + c * 16;
+          const uint8_t* sc = (is_v ? a.c.v_scales : a.c.k_scales) + row0;
+#pragma unroll
+          for (int x = 0; x < kPasses; ++x) {
+            const int r = r0 + x * kRowsAtOnce;
+            const bool on = page >= 0 && key0 + r < t.len;
+            raw[x] = make_uint4(0u, 0u, 0u, 0u);
+            byte[x] = 127u;
+            if (on) {
+              raw[x] = __ldg(reinterpret_cast<const uint4*>(src + r * D));
+              byte[x] = __ldg(sc + r);
+            }
           }
         };
-        // lanes of the row's other panel store their two pieces in the other order, so that the
-        // eight lanes of a row always hit different banks
-        const uint32_t swap = (c >> 2) & 1;
-        const uint32_t off0 = piece(2 * c + swap), off1 = piece(2 * c + 1 - swap);
+        int gi = skip;
+        load(gi);
+        for (; gi < n_groups; gi += kLoaders) {
+          uint4 cur[kPasses];
+          uint32_t f[kPasses];
 #pragma unroll
-        for (int x = 0; x < kPasses; ++x) load(page_next, t.kt0, 0, x);
-        for (int kt = t.kt0; kt < t.kt1 && ok; ++kt, ++J) {
-          const int page = page_next;
-          page_next = lookup(kt + 1);
-          const int s = J & 1;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = ok && mbar_wait(bar((kv ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            uint8_t* dst = smem + (kv ? C::kV : C::kK) + s * C::kTileBytes;
-#pragma unroll
-            for (int x = 0; x < kPasses; ++x) {
-              const uint4 y = raw[x];
-              const uint32_t f = byte[x];
-              load(kv ? page_next : page, kt + kv, 1 - kv, x);
-              uint4 lo, hi;
-              scaled16(y, f, lo, hi);
-              *reinterpret_cast<uint4*>(dst + off0 + x * kRowsAtOnce * 128) = swap ? hi : lo;
-              *reinterpret_cast<uint4*>(dst + off1 + x * kRowsAtOnce * 128) = swap ? lo : hi;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive_warp(bar((kv ? B_VFULL : B_KFULL) + s));
+          for (int x = 0; x < kPasses; ++x) {
+            cur[x] = raw[x];
+            f[x] = byte[x];
           }
+          load(gi + kLoaders);
+          const int J = J0 + (gi >> 4), s = J & 1;
+          const bool is_v = (gi & 8) != 0;
+          ok = mbar_wait(bar((is_v ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint8_t* dst = smem + (is_v ? C::kV : C::kK) + s * C::kTileBytes + (c >> 2) * kPanelBytes + 16 * (gi & 7) * 128;
+          // lanes of the row's other panel store their two pieces in the other order, so that the
+          // eight lanes that store together always hit different banks
+          const int swap = (c >> 2) & 1;
+#pragma unroll
+          for (int x = 0; x < kPasses; ++x) {
+            const int r = r0 + x * kRowsAtOnce;
+            uint4 lo, hi;
+            scaled16(cur[x], f[x], lo, hi);
+            const int p = (2 * c) & 7;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((p + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((p + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive_warp(bar((is_v ? B_VFULL : B_KFULL) + s));
         }
+        skip = gi - n_groups;
+        J0 += t.kt1 - t.kt0;
       }
-    }
-    cp_wait<0>();
-    if (ok) signal();
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    } else
     if (warp == 8) {
       // ---------------------------------------------------------- walk and Q producer
       if (lane == 0) {
@@ -332,17 +295,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
         Walk<P> w;
         bool more = seek<P, kThreads>(a, line, w0, w);
-        int last_q = -1;  // round of the last Q load
+        int J = 0;                                  // key tiles loaded
+        int last_q = -1, last_kj = -1, last_vj = -1;  // round of the last Q load, tiles of the last K, V loads
+        if constexpr (!kE4M3) {
+          tma_prefetch_desc(&tmK);
+          tma_prefetch_desc(&tmV);
+        }
         for (int v = 0;; ++v) {
           const int k = v & 1;
           if (!mbar_wait(bar(B_TEMPTY + k), ((v >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 3)) break;
           if (v > 0) w.next(a);
-          more = more && w.i < a.c.n_seqs && w.f0 < w1;
+          int ga = 0, gb = 0;
+          while ((more = more && w.i < a.c.n_seqs && w.f0 < w1)) {
+            w.part(w0, w1, ga, gb);
+            if (gb > ga) break;
+            w.next(a);  // the share has the group's overhead only
+          }
           volatile Unit* dst = unit_slot + k;
           dst->valid = more ? 1 : 0;
           if (more) {
-            const int ga = static_cast<int>(max(w0 - w.f0, 0ll));
-            const int gb = static_cast<int>(min(w1 - w.f0, static_cast<long long>(w.g)));
             dst->i = w.i;
             dst->a = w.s.a;
             dst->n = w.s.n;
@@ -352,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst->kt0 = ga;
             dst->kt1 = gb;
             dst->slot = piece_slot(b, ga, gb, w.g);
-            if (ga == 0 && gb < w.g) a.split[b] = SplitGroup{sh.owner(w.f0 + w.g - 1), w.s.a, w.s.n, w.h, w.u, {}};
+            if (ga == 0 && gb < w.g) a.split[b] = SplitGroup{sh.owner(w.behind() - 1), w.s.a, w.s.n, w.h, w.u, {}};
           }
           mbar_arrive(bar(B_TFULL + k));
           if (!more) break;
@@ -380,9 +351,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (pass == 0) mbar_arrive_expect_tx(bar(B_QFULL), boxes * kQBox * 128 * C::kPanels);
           }
           last_q = v;
+          if constexpr (!kE4M3) {
+            // a tile's pages: `boxes_kt` boxes of `rows` keys; the next tile's are looked up while
+            // this one's loads go out. Keys past the sequence and pages outside the cache take a box
+            // behind the last page, which reads as zeros.
+            const int rows = min(1 << a.c.page_shift, kTileN), boxes_kt = kTileN / rows;
+            const int* table = a.c.table + static_cast<long long>(w.i) * a.c.max_pages;
+            int page[kTileN / 16];
+            auto lookup = [&](int kt) {
+#pragma unroll
+              for (int x = 0; x < kTileN / 16; ++x) {
+                const int key = kt * kTileN + x * rows;
+                page[x] = x < boxes_kt && kt < gb && key < w.s.len ? __ldg(table + (key >> a.c.page_shift)) : -1;
+              }
+            };
+            lookup(ga);
+            bool ok = true;
+            for (int kt = ga; kt < gb && ok; ++kt, ++J) {
+              const int s = J & 1;
+              const uint32_t ph = (J >> 1) & 1;
+              int outer[kTileN / 16];
+#pragma unroll
+              for (int x = 0; x < kTileN / 16; ++x) {
+                if (page[x] >= a.c.n_pages || (page[x] < 0 && x < boxes_kt && kt * kTileN + x * rows < w.s.len)) {
+                  atomicCAS(err, 0, kErrCachePage);
+                  page[x] = -1;
+                }
+                outer[x] = page[x] < 0 ? max(a.c.n_pages * a.c.hkv, 1) : page[x] * a.c.hkv + w.h;
+              }
+              lookup(kt + 1);
+              const int in_page = (kt * kTileN) & ((1 << a.c.page_shift) - 1);
+#pragma unroll
+              for (int kv = 0; kv < 2; ++kv) {
+                const int full = (kv ? B_VFULL : B_KFULL) + s;
+                ok = ok && mbar_wait(bar((kv ? B_VEMPTY : B_KEMPTY) + s), ph ^ 1, abort_flag, err, kErrPagedWait + 2);
+                if (!ok) break;
+                mbar_arrive_expect_tx(bar(full), C::kTileBytes);
+                const uint32_t to = sb + (kv ? C::kV : C::kK) + s * C::kTileBytes;
+#pragma unroll
+                for (int x = 0; x < kTileN / 16; ++x)
+                  if (x < boxes_kt)
+#pragma unroll
+                    for (int p = 0; p < C::kPanels; ++p)
+                      tma_load_3d(to + p * kPanelBytes + x * rows * 128, kv ? &tmV : &tmK, bar(full), p * 64, in_page,
+                                  outer[x]);
+                if (kv) last_vj = J; else last_kj = J;
+              }
+            }
+            if (!ok) break;
+          }
         }
-        // an aborted block waits (bounded) for the loads that land in its shared memory
-        if (*abort_flag && last_q >= 0 && !mbar_wait_quiesce(bar(B_QFULL), last_q & 1, kWaitLimitNs)) *unquiesced = 1;
+        if (*abort_flag) {
+          // an aborted block waits (bounded) for the loads that land in its shared memory; a stage is
+          // loaded again only when its tile was consumed, so only the last two tiles' may be in flight
+          bool done = last_q < 0 || mbar_wait_quiesce(bar(B_QFULL), last_q & 1, kWaitLimitNs);
+          for (int j = max(last_kj - 1, 0); j <= last_kj; ++j)
+            done = mbar_wait_quiesce(bar(B_KFULL + (j & 1)), (j >> 1) & 1, kWaitLimitNs) && done;
+          for (int j = max(last_vj - 1, 0); j <= last_vj; ++j)
+            done = mbar_wait_quiesce(bar(B_VFULL + (j & 1)), (j >> 1) & 1, kWaitLimitNs) && done;
+          if (!done) *unquiesced = 1;
+        }
       }
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer
@@ -405,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O_t += P_t V of the group's last issued S, in two halves of 64 keys
       auto issue_pv = [&](int t, int s, bool acc) -> bool {
         const uint32_t vbase = sb + C::kV + s * C::kTileBytes;
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!wwait(bar(B_PFULL + 2 * t + half), (jt[t] - 1) & 1, kErrPagedWait + 5)) return false;
           tc_fence_after();
@@ -430,7 +459,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // previous unit's epilogue must have read out
         auto pv = [&](int t, int jl) -> bool {
           const int ps = (J - 1) & 1;
-          if (t == 0 && !wwait(bar(B_VFULL + ps), ((J - 1) >> 1) & 1, kErrPagedWait + 8)) return false;
+          if (t == 0) {
+            if (!wwait(bar(B_VFULL + ps), ((J - 1) >> 1) & 1, kErrPagedWait + 8)) return false;
+            if constexpr (!kE4M3) {
+              // rows of the tile past the sequence, in its last page, become zeros
+              const int held = T.len - (T.kt0 + jl - 1) * kTileN;
+              if (held < kTileN) {
+                for (int x = max(held, 0) * (D / 8) + lane; x < kTileN * (D / 8); x += 32) {
+                  const int r = x / (D / 8), p = x % (D / 8);
+                  *reinterpret_cast<uint4*>(smem + C::kV + ps * C::kTileBytes + (p >> 3) * kPanelBytes + r * 128 +
+                                            (p & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
+            }
+          }
           if (jl == 1 && ut[t] > 0 && !wwait(bar(B_OFREE + t), (ut[t] - 1) & 1, kErrPagedWait + 9)) return false;
           tc_fence_after();
           if (!issue_pv(t, ps, jl > 1)) return false;
@@ -443,8 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = J & 1;
           if (!wwait(bar(B_KFULL + s), (J >> 1) & 1, kErrPagedWait + 10)) { ok = false; break; }
           tc_fence_after();
-          for (int t = 0; t < nt; ++t) {
-            if (jl > 0 && !pv(t, jl)) { ok = false; break; }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || t >= nt) break;
+            if (jl > 0) ok = pv(t, jl);
+            if (!ok) break;
             issue_s(t, s);
             tc_commit_w(bar(B_SFULL + t));
             ++jt[t];
@@ -454,8 +501,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         // every S of this unit has been issued: Q is free once they complete
         tc_commit_w(bar(B_QEMPTY));
-        for (int t = 0; t < nt && ok; ++t) ok = pv(t, jl);
-        for (int t = 0; t < nt; ++t) ++ut[t];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && t < nt) {
+            ok = pv(t, jl);
+            ++ut[t];
+          }
       }
       // every issued MMA has completed once the drain barrier fires; wait for it also after an
       // abort, so that no MMA still reads shared memory or writes tensor memory when they are
@@ -469,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax (warps 0-7)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    if constexpr (kE4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -688,13 +739,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool kE4M3>
 fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s) {
   using C = Cfg<D>;
-  CUtensorMap mq;
+  CUtensorMap mq, mk = {}, mv = {};
   if (const fcp_status st = make_bf16_map(&mq, a.q, hq, a.c.total_new, D, kQBox); st != FCP_OK) return st;
+  if constexpr (!kE4M3) {
+    // pages and heads are the maps' outer dimension; a box is a page's rows, at most a tile
+    const long long outer = static_cast<long long>(a.c.n_pages) * a.c.hkv;
+    if (outer + a.c.hkv > INT32_MAX) return FCP_ERR_UNSUPPORTED;
+    const int page = 1 << a.c.page_shift, n = static_cast<int>(std::max(outer, 1ll));
+    fcp_status st;
+    if ((st = make_bf16_map(&mk, a.c.k_pages, n, page, D, std::min(page, kTileN))) != FCP_OK) return st;
+    if ((st = make_bf16_map(&mv, a.c.v_pages, n, page, D, std::min(page, kTileN))) != FCP_OK) return st;
+  }
   const int blocks = std::min(n_sm, kMaxChunkBlocks);
   set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
   FCP_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes),
                "paged chunk smem attribute");
-  chunk_kernel<D, kE4M3><<<blocks, kThreads, C::kSmemBytes, s>>>(mq, a);
+  chunk_kernel<D, kE4M3><<<blocks, kThreads<kE4M3>, C::kSmemBytes, s>>>(mq, mk, mv, a);
   FCP_CUDA_TRY(cudaGetLastError(), "paged chunk launch");
   return launch_merge<ChunkRows, D>(a, blocks, 32, s);
 }

@@ -122,7 +122,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
     if (threadIdx.x == 0) {
       if (!first) w.next(a);
       Piece p;
-      p.valid = walking && w.i < a.c.n_seqs && w.f0 < w1;
+      p.ga = p.gb = 0;
+      while ((p.valid = walking && w.i < a.c.n_seqs && w.f0 < w1)) {
+        w.part(w0, w1, p.ga, p.gb);
+        if (p.gb > p.ga) break;
+        w.next(a);  // the share has the group's overhead only
+      }
       if (p.valid) {
         p.i = w.i;
         p.h = w.h;
@@ -131,10 +136,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
         p.n = w.s.n;
         p.len = w.s.len;
         p.end = w.end;
-        p.ga = static_cast<int>(max(w0 - w.f0, 0ll));
-        p.gb = static_cast<int>(min(w1 - w.f0, static_cast<long long>(w.g)));
         p.slot = piece_slot(b, p.ga, p.gb, w.g);
-        if (p.ga == 0 && p.gb < w.g) a.split[b] = SplitGroup{sh.owner(w.f0 + w.g - 1), w.s.a, w.s.n, w.h, w.u, {}};
+        if (p.ga == 0 && p.gb < w.g) a.split[b] = SplitGroup{sh.owner(w.behind() - 1), w.s.a, w.s.n, w.h, w.u, {}};
       }
       shared_piece = p;
     }

@@ -2,11 +2,12 @@
 //
 // The work is a list of groups in the order sequence, KV head, unit: a unit is the largest set
 // of (new token, query head) rows that one block handles together, and a group reads the keys
-// [0, end) that any row of its unit sees, in granules of 128. Laid end to end, the groups'
-// granules form one line, and block b of B takes the b-th of B equal shares of it. So the load
-// is even whatever the lengths are, no block ever holds more than two groups that it does not
-// finish (its first and its last), and the space for partial results does not depend on the
-// batch. Every block derives its share from the lengths in device memory, so a captured graph
+// [0, end) that any row of its unit sees, in granules of 128. Laid end to end, the groups form
+// one line, each as long as its granules and the policy's kOverhead in front of them (what
+// loading its rows and storing their results costs, in granules), and block b of B takes the
+// b-th of B equal shares of it. So the load is even whatever the lengths are, no block ever
+// holds more than two groups that it does not finish (its first and its last), and the space
+// for partial results does not depend on the batch. Every block derives its share from the lengths in device memory, so a captured graph
 // follows them.
 #pragma once
 
@@ -46,6 +47,7 @@ __device__ __forceinline__ int granules_of(int end) { return max(1, (end + kGran
 template <int kRowsPerUnit>
 struct FewRows {
   static constexpr int kRows = kRowsPerUnit;
+  static constexpr int kOverhead = 1;
   static __device__ __forceinline__ int units(const SeqShape& s, int group) {
     return static_cast<int>((static_cast<long long>(s.n) * group + kRows - 1) / kRows);
   }
@@ -65,6 +67,7 @@ struct FewRows {
 // tiles of a KV head are ordered tokens first, heads within them, and a unit is two of them.
 struct ChunkRows {
   static constexpr int kRows = 2 * kTileM;
+  static constexpr int kOverhead = 3;
   struct Shape {
     int log_tokens, heads, head_tiles, tiles;
     __device__ __forceinline__ Shape(const SeqShape& s, int group) {
@@ -97,14 +100,20 @@ template <class P>
 struct Walk {
   int i, h, u, n_units, end, g;   // sequence, KV head, unit, units a head, keys, granules
   SeqShape s;
-  long long f0;                   // the group's first granule on the line
+  long long f0;                   // where the group begins on the line
 
   __device__ __forceinline__ void enter(const AttnArgs& a) {
     end = P::end(s, a.group, u, a.causal);
     g = granules_of(end);
   }
+  __device__ __forceinline__ long long behind() const { return f0 + P::kOverhead + g; }
+  // Granules [ga, gb) of the group that the part [w0, w1) of the line holds.
+  __device__ __forceinline__ void part(long long w0, long long w1, int& ga, int& gb) const {
+    ga = static_cast<int>(max(w0 - f0 - P::kOverhead, 0ll));
+    gb = static_cast<int>(min(max(w1 - f0 - P::kOverhead, 0ll), static_cast<long long>(g)));
+  }
   __device__ __forceinline__ void next(const AttnArgs& a) {
-    f0 += g;
+    f0 = behind();
     if (++u == n_units) {
       u = 0;
       if (++h == a.c.hkv) {
@@ -121,10 +130,10 @@ struct Walk {
 };
 
 template <class P>
-__device__ __forceinline__ long long head_granules(const AttnArgs& a, const SeqShape& s) {
+__device__ __forceinline__ long long head_length(const AttnArgs& a, const SeqShape& s) {
   long long sum = 0;
   const int n = P::units(s, a.group);
-  for (int u = 0; u < n; ++u) sum += granules_of(P::end(s, a.group, u, a.causal));
+  for (int u = 0; u < n; ++u) sum += P::kOverhead + granules_of(P::end(s, a.group, u, a.causal));
   return sum;
 }
 
@@ -143,7 +152,7 @@ __device__ __forceinline__ void build_line(const AttnArgs& a, Line<kThreads>& li
   long long mine = 0;
   for (int i = threadIdx.x * per; i < min((static_cast<int>(threadIdx.x) + 1) * per, a.c.n_seqs); ++i) {
     const SeqShape s = seq_shape(a.c, i, report);
-    if (s.n > 0) mine += head_granules<P>(a, s) * a.c.hkv;
+    if (s.n > 0) mine += head_length<P>(a, s) * a.c.hkv;
   }
   long long x = mine;
 #pragma unroll
@@ -162,7 +171,7 @@ __device__ __forceinline__ void build_line(const AttnArgs& a, Line<kThreads>& li
   __syncthreads();
 }
 
-// Place `w` on the group that holds granule f of the line (f < the line's length). False only
+// Place `w` on the group that holds place f of the line (f < the line's length). False only
 // if the lengths no longer are what the line was built from.
 template <class P, int kThreads>
 __device__ __forceinline__ bool seek(const AttnArgs& a, const Line<kThreads>& line, long long f, Walk<P>& w) {
@@ -177,7 +186,7 @@ __device__ __forceinline__ bool seek(const AttnArgs& a, const Line<kThreads>& li
   while (true) {
     if (w.i >= a.c.n_seqs) return false;
     w.s = seq_shape(a.c, w.i, false);
-    per_head = w.s.n > 0 ? head_granules<P>(a, w.s) : 0;
+    per_head = w.s.n > 0 ? head_length<P>(a, w.s) : 0;
     if (f < w.f0 + per_head * a.c.hkv) break;
     w.f0 += per_head * a.c.hkv;
     ++w.i;
@@ -187,16 +196,16 @@ __device__ __forceinline__ bool seek(const AttnArgs& a, const Line<kThreads>& li
   w.n_units = P::units(w.s, a.group);
   w.u = 0;
   w.enter(a);
-  while (f >= w.f0 + w.g) {
-    w.f0 += w.g;
+  while (f >= w.behind()) {
+    w.f0 = w.behind();
     ++w.u;
     w.enter(a);
   }
   return true;
 }
 
-// The blocks' shares of a line of `total` granules: block b < blocks takes [begin(b), begin(b +
-// 1)), at least one granule (blocks is less than the grid where there are fewer granules).
+// The blocks' shares of a line of length `total`: block b < blocks takes [begin(b), begin(b + 1)),
+// which is not empty (blocks is less than the grid where the line is shorter).
 struct Shares {
   long long base;
   int rem, blocks;
@@ -206,7 +215,7 @@ struct Shares {
     rem = static_cast<int>(total - base * blocks);
   }
   __device__ __forceinline__ long long begin(int b) const { return base * b + rem * b / blocks; }
-  // The block that takes granule f.
+  // The block that takes place f.
   __device__ __forceinline__ int owner(long long f) const {
     int b = static_cast<int>(f / (base + 1));
     while (begin(b + 1) <= f) ++b;
