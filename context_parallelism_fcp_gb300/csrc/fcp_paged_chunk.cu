@@ -289,21 +289,28 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       }
     } else
     if (warp == 8) {
-      // ---------------------------------------------------------- walk and Q producer
+      // ---------------------------------------------------------- walk, Q and (bf16) K, V loads
+      // Lane 0 walks along the block's share and publishes each unit; then the lanes issue its
+      // loads side by side: box j of Q, or page j of a key tile, is lane j's.
       if (lane == 0) {
         tma_prefetch_desc(&tmQ);
-        const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
-        Walk<P> w;
-        bool more = seek<P, kThreads>(a, line, w0, w);
-        int J = 0;                                  // key tiles loaded
-        int last_q = -1, last_kj = -1, last_vj = -1;  // round of the last Q load, tiles of the last K, V loads
         if constexpr (!kE4M3) {
           tma_prefetch_desc(&tmK);
           tma_prefetch_desc(&tmV);
         }
-        for (int v = 0;; ++v) {
-          const int k = v & 1;
-          if (!mbar_wait(bar(B_TEMPTY + k), ((v >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 3)) break;
+      }
+      const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
+      Walk<P> w;
+      bool more = lane == 0 && seek<P, kThreads>(a, line, w0, w);
+      bool ok = true;
+      int J = 0;                                    // key tiles loaded
+      int last_q = -1, last_kj = -1, last_vj = -1;  // round of the last Q load, tiles of the last K, V loads
+      for (int v = 0; ok; ++v) {
+        const int k = v & 1;
+        ok = mbar_wait(bar(B_TEMPTY + k), ((v >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 3);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
           if (v > 0) w.next(a);
           int ga = 0, gb = 0;
           while ((more = more && w.i < a.c.n_seqs && w.f0 < w1)) {
@@ -326,91 +333,82 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             if (ga == 0 && gb < w.g) a.split[b] = SplitGroup{sh.owner(w.behind() - 1), w.s.a, w.s.n, w.h, w.u, {}};
           }
           mbar_arrive(bar(B_TFULL + k));
-          if (!more) break;
-          if (!mbar_wait(bar(B_QEMPTY), (v & 1) ^ 1, abort_flag, err, kErrPagedWait + 4)) break;
-          // Q: boxes of 16 tokens of one head; the rest of the tiles is never read for a stored row
-          const ChunkRows::Shape z(w.s, a.group);
-          const int x1 = min(2 * w.u + 2, z.tiles);
-          for (int pass = 0; pass < 2; ++pass) {
-            int boxes = 0;
-            for (int x = 2 * w.u; x < x1; ++x) {
-              const int tok0 = (x / z.head_tiles) << z.log_tokens, head0 = (x % z.head_tiles) * z.heads;
-              const int heads = min(z.heads, a.group - head0);
-              const int toks = min((1 << z.log_tokens), w.s.n - tok0);
-              if (pass == 0) {
-                boxes += heads * ((toks + kQBox - 1) / kQBox);
-                continue;
+        }
+        __syncwarp();
+        const volatile Unit* src = unit_slot + k;  // stays until this unit's consumers have read it
+        if (!src->valid) break;
+        const SeqShape seq{src->a, src->n, src->len};
+        const int h = src->h, kt0 = src->kt0, kt1 = src->kt1, x0 = 2 * src->u;
+        const int* table = a.c.table + static_cast<long long>(src->i) * a.c.max_pages;
+        ok = mbar_wait(bar(B_QEMPTY), (v & 1) ^ 1, abort_flag, err, kErrPagedWait + 4);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        {
+          // Q: boxes of 16 tokens of one head, eight to a tile; rows of boxes without a new token are
+          // never read for a stored row
+          const ChunkRows::Shape z(seq, a.group);
+          const int x = x0 + (lane >> 4), box = lane & 7, p = (lane >> 3) & 1;
+          const int tt = x / z.head_tiles;
+          const int per_head = 1 << (z.log_tokens - 4);  // boxes of one head
+          const int tok = (tt << z.log_tokens) + (box & (per_head - 1)) * kQBox;
+          const int head = (x - tt * z.head_tiles) * z.heads + box / per_head;
+          const bool mine = p < C::kPanels && x < z.tiles && tok < seq.n && head < a.group;
+          const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+          if (lane == 0) mbar_arrive_expect_tx(bar(B_QFULL), boxes * kQBox * 128);
+          __syncwarp();
+          if (mine)
+            tma_load_3d(sb + C::kQ + (x & 1) * C::kTileBytes + p * kPanelBytes + box * kQBox * 128, &tmQ, bar(B_QFULL),
+                        p * 64, seq.a + tok, h * a.group + head);
+        }
+        last_q = v;
+        if constexpr (!kE4M3) {
+          // A tile's pages, one to a lane; the next tile's are looked up while this one's loads go
+          // out. Keys past the sequence and pages outside the cache take a box behind the last page,
+          // which reads as zeros.
+          const int rows = min(1 << a.c.page_shift, kTileN), n_boxes = kTileN / rows;
+          auto lookup = [&](int kt) -> int {
+            const int key = kt * kTileN + lane * rows;
+            if (lane >= n_boxes || kt >= kt1 || key >= seq.len) return -1;
+            const int page = __ldg(table + (key >> a.c.page_shift));
+            if (page >= 0 && page < a.c.n_pages) return page;
+            atomicCAS(err, 0, kErrCachePage);
+            return -1;
+          };
+          int page_next = lookup(kt0);
+          for (int kt = kt0; kt < kt1 && ok; ++kt, ++J) {
+            const int s = J & 1;
+            const uint32_t ph = (J >> 1) & 1;
+            const int outer = page_next < 0 ? max(a.c.n_pages * a.c.hkv, 1) : page_next * a.c.hkv + h;
+            page_next = lookup(kt + 1);
+            const int in_page = (kt * kTileN) & ((1 << a.c.page_shift) - 1);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              ok = ok && mbar_wait(bar((kv ? B_VEMPTY : B_KEMPTY) + s), ph ^ 1, abort_flag, err, kErrPagedWait + 2);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              const uint32_t full = bar((kv ? B_VFULL : B_KFULL) + s);
+              if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
+              __syncwarp();
+              if (lane < n_boxes) {
+                const uint32_t to = sb + (kv ? C::kV : C::kK) + s * C::kTileBytes + lane * rows * 128;
+#pragma unroll
+                for (int p = 0; p < C::kPanels; ++p)
+                  tma_load_3d(to + p * kPanelBytes, kv ? &tmV : &tmK, full, p * 64, in_page, outer);
               }
-              for (int hh = 0; hh < heads; ++hh)
-                for (int tok = 0; tok < toks; tok += kQBox)
-                  for (int p = 0; p < C::kPanels; ++p)
-                    tma_load_3d(sb + C::kQ + (x & 1) * C::kTileBytes + p * kPanelBytes +
-                                    ((hh << z.log_tokens) + tok) * 128,
-                                &tmQ, bar(B_QFULL), p * 64, w.s.a + tok0 + tok, w.h * a.group + head0 + hh);
+              if (kv) last_vj = J; else last_kj = J;
             }
-            if (pass == 0) mbar_arrive_expect_tx(bar(B_QFULL), boxes * kQBox * 128 * C::kPanels);
-          }
-          last_q = v;
-          if constexpr (!kE4M3) {
-            // a tile's pages: `boxes_kt` boxes of `rows` keys; the next tile's are looked up while
-            // this one's loads go out. Keys past the sequence and pages outside the cache take a box
-            // behind the last page, which reads as zeros.
-            const int rows = min(1 << a.c.page_shift, kTileN), boxes_kt = kTileN / rows;
-            const int* table = a.c.table + static_cast<long long>(w.i) * a.c.max_pages;
-            int page[kTileN / 16];
-            auto lookup = [&](int kt) {
-#pragma unroll
-              for (int x = 0; x < kTileN / 16; ++x) {
-                const int key = kt * kTileN + x * rows;
-                page[x] = x < boxes_kt && kt < gb && key < w.s.len ? __ldg(table + (key >> a.c.page_shift)) : -1;
-              }
-            };
-            lookup(ga);
-            bool ok = true;
-            for (int kt = ga; kt < gb && ok; ++kt, ++J) {
-              const int s = J & 1;
-              const uint32_t ph = (J >> 1) & 1;
-              int outer[kTileN / 16];
-#pragma unroll
-              for (int x = 0; x < kTileN / 16; ++x) {
-                if (page[x] >= a.c.n_pages || (page[x] < 0 && x < boxes_kt && kt * kTileN + x * rows < w.s.len)) {
-                  atomicCAS(err, 0, kErrCachePage);
-                  page[x] = -1;
-                }
-                outer[x] = page[x] < 0 ? max(a.c.n_pages * a.c.hkv, 1) : page[x] * a.c.hkv + w.h;
-              }
-              lookup(kt + 1);
-              const int in_page = (kt * kTileN) & ((1 << a.c.page_shift) - 1);
-#pragma unroll
-              for (int kv = 0; kv < 2; ++kv) {
-                const int full = (kv ? B_VFULL : B_KFULL) + s;
-                ok = ok && mbar_wait(bar((kv ? B_VEMPTY : B_KEMPTY) + s), ph ^ 1, abort_flag, err, kErrPagedWait + 2);
-                if (!ok) break;
-                mbar_arrive_expect_tx(bar(full), C::kTileBytes);
-                const uint32_t to = sb + (kv ? C::kV : C::kK) + s * C::kTileBytes;
-#pragma unroll
-                for (int x = 0; x < kTileN / 16; ++x)
-                  if (x < boxes_kt)
-#pragma unroll
-                    for (int p = 0; p < C::kPanels; ++p)
-                      tma_load_3d(to + p * kPanelBytes + x * rows * 128, kv ? &tmV : &tmK, bar(full), p * 64, in_page,
-                                  outer[x]);
-                if (kv) last_vj = J; else last_kj = J;
-              }
-            }
-            if (!ok) break;
           }
         }
-        if (*abort_flag) {
-          // an aborted block waits (bounded) for the loads that land in its shared memory; a stage is
-          // loaded again only when its tile was consumed, so only the last two tiles' may be in flight
-          bool done = last_q < 0 || mbar_wait_quiesce(bar(B_QFULL), last_q & 1, kWaitLimitNs);
-          for (int j = max(last_kj - 1, 0); j <= last_kj; ++j)
-            done = mbar_wait_quiesce(bar(B_KFULL + (j & 1)), (j >> 1) & 1, kWaitLimitNs) && done;
-          for (int j = max(last_vj - 1, 0); j <= last_vj; ++j)
-            done = mbar_wait_quiesce(bar(B_VFULL + (j & 1)), (j >> 1) & 1, kWaitLimitNs) && done;
-          if (!done) *unquiesced = 1;
-        }
+      }
+      if (lane == 0 && *abort_flag) {
+        // an aborted block waits (bounded) for the loads that land in its shared memory; a stage is
+        // loaded again only when its tile was consumed, so only the last two tiles' may be in flight
+        bool done = last_q < 0 || mbar_wait_quiesce(bar(B_QFULL), last_q & 1, kWaitLimitNs);
+        for (int j = max(last_kj - 1, 0); j <= last_kj; ++j)
+          done = mbar_wait_quiesce(bar(B_KFULL + (j & 1)), (j >> 1) & 1, kWaitLimitNs) && done;
+        for (int j = max(last_vj - 1, 0); j <= last_vj; ++j)
+          done = mbar_wait_quiesce(bar(B_VFULL + (j & 1)), (j >> 1) & 1, kWaitLimitNs) && done;
+        if (!done) *unquiesced = 1;
       }
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer

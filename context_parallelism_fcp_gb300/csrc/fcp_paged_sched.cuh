@@ -54,6 +54,21 @@ struct FewRows {
   static __device__ __forceinline__ int end(const SeqShape& s, int group, int u, int causal) {
     return key_end(s, static_cast<int>(((u + 1ll) * kRows - 1) / group), causal);
   }
+  static __device__ __forceinline__ long long head_length(const SeqShape& s, int group, int causal) {
+    long long sum = 0;
+    const int n = units(s, group);
+    for (int u = 0; u < n; ++u) sum += kOverhead + granules_of(end(s, group, u, causal));
+    return sum;
+  }
+  // The unit of a head that holds place f >= f0 of the line, where the head begins at f0; f0
+  // becomes where the unit begins.
+  static __device__ __forceinline__ int find(const SeqShape& s, int group, int causal, long long f, long long& f0) {
+    for (int u = 0;; ++u) {
+      const long long next = f0 + kOverhead + granules_of(end(s, group, u, causal));
+      if (f < next) return u;
+      f0 = next;
+    }
+  }
   // (token, head of the group) of row r of unit u; false behind the last
   static __device__ __forceinline__ bool row(const SeqShape& s, int group, int u, int r, int& tok, int& head) {
     const long long x = static_cast<long long>(u) * kRows + r;
@@ -69,14 +84,47 @@ struct ChunkRows {
   static constexpr int kRows = 2 * kTileM;
   static constexpr int kOverhead = 3;
   struct Shape {
-    int log_tokens, heads, head_tiles, tiles;
+    int log_tokens, heads, head_tiles, token_tiles, tiles;
     __device__ __forceinline__ Shape(const SeqShape& s, int group) {
       log_tokens = s.n > 64 ? 7 : (s.n > 32 ? 6 : (s.n > 16 ? 5 : 4));
       heads = kTileM >> log_tokens;
-      head_tiles = (group + heads - 1) / heads;
-      tiles = head_tiles * ((s.n + (1 << log_tokens) - 1) >> log_tokens);
+      head_tiles = (group + heads - 1) >> (7 - log_tokens);
+      token_tiles = (s.n + (1 << log_tokens) - 1) >> log_tokens;
+      tiles = head_tiles * token_tiles;
+    }
+    // First unit whose last tile is of token tile tt or a later one.
+    __device__ __forceinline__ int first_unit(int tt) const {
+      return tt >= token_tiles ? (tiles + 1) >> 1 : (tt * head_tiles) >> 1;
+    }
+    // Length on the line of a unit whose last tile is of token tile tt.
+    __device__ __forceinline__ int length(const SeqShape& s, int tt, int causal) const {
+      return kOverhead + granules_of(key_end(s, ((tt + 1) << log_tokens) - 1, causal));
     }
   };
+  static __device__ __forceinline__ long long head_length(const SeqShape& s, int group, int causal) {
+    const Shape z(s, group);
+    long long sum = 0;
+    for (int tt = 0, u = 0; tt < z.token_tiles; ++tt) {
+      const int next = z.first_unit(tt + 1);
+      sum += static_cast<long long>(next - u) * z.length(s, tt, causal);
+      u = next;
+    }
+    return sum;
+  }
+  static __device__ __forceinline__ int find(const SeqShape& s, int group, int causal, long long f, long long& f0) {
+    const Shape z(s, group);
+    for (int tt = 0, u = 0;; ++tt) {
+      const int next = z.first_unit(tt + 1), len = z.length(s, tt, causal);
+      const long long behind = f0 + static_cast<long long>(next - u) * len;
+      if (f < behind) {
+        const int x = static_cast<int>((f - f0) / len);
+        f0 += static_cast<long long>(x) * len;
+        return u + x;
+      }
+      f0 = behind;
+      u = next;
+    }
+  }
   static __device__ __forceinline__ int units(const SeqShape& s, int group) { return (Shape(s, group).tiles + 1) >> 1; }
   static __device__ __forceinline__ int tiles_of(const SeqShape& s, int group, int u) {
     return min(2, Shape(s, group).tiles - 2 * u);
@@ -129,14 +177,6 @@ struct Walk {
   }
 };
 
-template <class P>
-__device__ __forceinline__ long long head_length(const AttnArgs& a, const SeqShape& s) {
-  long long sum = 0;
-  const int n = P::units(s, a.group);
-  for (int u = 0; u < n; ++u) sum += P::kOverhead + granules_of(P::end(s, a.group, u, a.causal));
-  return sum;
-}
-
 // Shared memory of the line's prefix sums: thread t's sequences begin at prefix[t].
 template <int kThreads>
 struct Line {
@@ -152,7 +192,7 @@ __device__ __forceinline__ void build_line(const AttnArgs& a, Line<kThreads>& li
   long long mine = 0;
   for (int i = threadIdx.x * per; i < min((static_cast<int>(threadIdx.x) + 1) * per, a.c.n_seqs); ++i) {
     const SeqShape s = seq_shape(a.c, i, report);
-    if (s.n > 0) mine += head_length<P>(a, s) * a.c.hkv;
+    if (s.n > 0) mine += P::head_length(s, a.group, a.causal) * a.c.hkv;
   }
   long long x = mine;
 #pragma unroll
@@ -186,7 +226,7 @@ __device__ __forceinline__ bool seek(const AttnArgs& a, const Line<kThreads>& li
   while (true) {
     if (w.i >= a.c.n_seqs) return false;
     w.s = seq_shape(a.c, w.i, false);
-    per_head = w.s.n > 0 ? head_length<P>(a, w.s) : 0;
+    per_head = w.s.n > 0 ? P::head_length(w.s, a.group, a.causal) : 0;
     if (f < w.f0 + per_head * a.c.hkv) break;
     w.f0 += per_head * a.c.hkv;
     ++w.i;
@@ -194,13 +234,8 @@ __device__ __forceinline__ bool seek(const AttnArgs& a, const Line<kThreads>& li
   w.h = static_cast<int>((f - w.f0) / per_head);
   w.f0 += w.h * per_head;
   w.n_units = P::units(w.s, a.group);
-  w.u = 0;
+  w.u = P::find(w.s, a.group, a.causal, f, w.f0);
   w.enter(a);
-  while (f >= w.behind()) {
-    w.f0 = w.behind();
-    ++w.u;
-    w.enter(a);
-  }
   return true;
 }
 
