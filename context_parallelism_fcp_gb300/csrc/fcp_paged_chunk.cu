@@ -35,7 +35,7 @@ template <bool kE4M3>
 constexpr int kThreads = 32 * (10 + (kE4M3 ? kLoaders : 0));
 constexpr int kPanelBytes = kTileM * 128;  // 128 rows x 64 bf16 channels
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-constexpr int kQBox = 16;                   // tokens of one TMA load of Q
+constexpr int kQBox = 16;                   // tokens of a TMA load of Q for tiles of several heads
 // Registers a thread with the loader warps: the launch gives 128, and the softmax warps take
 // what the others leave (they hold a row of 128 scores).
 constexpr int kRegsSoftmax = 176, kRegsOther = 80;
@@ -74,8 +74,8 @@ struct Cfg {
   static constexpr int kK = 2 * kTileBytes;        // 2 stages
   static constexpr int kV = 4 * kTileBytes;        // 2 stages
   static constexpr int kBar = 6 * kTileBytes;
-  static constexpr int kStage = kBar + kBarArea;   // epilogue: [32 rows][32 float32] per softmax warp
-  static constexpr int kStageBytes = 8 * 32 * 32 * 4;
+  static constexpr int kStage = kBar + kBarArea;   // epilogue: 32 rows x 128 bytes per softmax warp
+  static constexpr int kStageBytes = 8 * 32 * 128;
   static constexpr int kEnd = kStage + kStageBytes;
   // at least half the SM's shared memory, so one block per SM holds all 512 TMEM columns
   static constexpr int kSmemBytes = kEnd > 118 * 1024 ? kEnd : 118 * 1024;
@@ -107,19 +107,16 @@ __device__ __forceinline__ void scaled16(const uint4 x, uint32_t byte, uint4& lo
       r[i] = *reinterpret_cast<const uint32_t*>(&y);
     }
   };
-  if (byte <= 134u) {
-    times((byte + 120u) << 7);
-  } else {
-    times(254u << 7);
-    times(byte == 255u ? 0x7fc0u : (byte - 7u) << 7);
-  }
+  times((min(byte, 134u) + 120u) << 7);
+  if (byte > 134u) times(byte == 255u ? 0x7fc0u : (byte - 7u) << 7);
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
 template <int D, bool kE4M3>
 __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
-    chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+    chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ16,
+                 const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
   constexpr int kThreads = fcp::kThreads<kE4M3>;
   using C = Cfg<D>;
@@ -224,36 +221,37 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         if (t.valid <= 0) break;
         const int* table = a.c.table + static_cast<long long>(t.i) * a.c.max_pages;
         const int n_groups = (t.kt1 - t.kt0) * 16;
+        auto lookup = [&](int gi) -> int {  // the page of group gi; -1: its rows become zeros
+          const int key0 = (t.kt0 + (gi >> 4)) * kTileN + 16 * (gi & 7);
+          if (gi >= n_groups || key0 >= t.len) return -1;
+          const int page = __ldg(table + (key0 >> a.c.page_shift));
+          if (page >= 0 && page < a.c.n_pages) return page;
+          atomicCAS(err, 0, kErrCachePage);
+          return -1;
+        };
         uint4 raw[kPasses];
         uint32_t byte[kPasses];
-        auto load = [&](int gi) {
+        auto load = [&](int gi, int page) {
           const int key0 = (t.kt0 + (gi >> 4)) * kTileN + 16 * (gi & 7);
-          int page = -1;
-          if (gi < n_groups && key0 < t.len) {
-            page = __ldg(table + (key0 >> a.c.page_shift));
-            if (page < 0 || page >= a.c.n_pages) {
-              atomicCAS(err, 0, kErrCachePage);
-              page = -1;
-            }
-          }
           const bool is_v = (gi & 8) != 0;
-          const long long row0 = page >= 0 ? page_row(a.c, page, t.h) + (key0 & page_mask) : 0;
+          const long long row0 = (page >= 0 ? page_row(a.c, page, t.h) + (key0 & page_mask) : 0) + r0;
           const uint8_t* src = (is_v ? a.c.v_pages : a.c.k_pages) + row0 * D + c * 16;
           const uint8_t* sc = (is_v ? a.c.v_scales : a.c.k_scales) + row0;
+          const int held = page >= 0 ? t.len - key0 - r0 : 0;  // rows below held are there
 #pragma unroll
           for (int x = 0; x < kPasses; ++x) {
-            const int r = r0 + x * kRowsAtOnce;
-            const bool on = page >= 0 && key0 + r < t.len;
             raw[x] = make_uint4(0u, 0u, 0u, 0u);
             byte[x] = 127u;
-            if (on) {
-              raw[x] = __ldg(reinterpret_cast<const uint4*>(src + r * D));
-              byte[x] = __ldg(sc + r);
+            if (x * kRowsAtOnce < held) {
+              raw[x] = __ldg(reinterpret_cast<const uint4*>(src + x * kRowsAtOnce * D));
+              byte[x] = __ldg(sc + x * kRowsAtOnce);
             }
           }
         };
         int gi = skip;
-        load(gi);
+        int page_next = lookup(gi);
+        load(gi, page_next);
+        page_next = lookup(gi + kLoaders);
         for (; gi < n_groups; gi += kLoaders) {
           uint4 cur[kPasses];
           uint32_t f[kPasses];
@@ -262,7 +260,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             cur[x] = raw[x];
             f[x] = byte[x];
           }
-          load(gi + kLoaders);
+          load(gi + kLoaders, page_next);
+          page_next = lookup(gi + 2 * kLoaders);
           const int J = J0 + (gi >> 4), s = J & 1;
           const bool is_v = (gi & 8) != 0;
           ok = mbar_wait(bar((is_v ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
@@ -294,6 +293,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       // loads side by side: box j of Q, or page j of a key tile, is lane j's.
       if (lane == 0) {
         tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmQ16);
         if constexpr (!kE4M3) {
           tma_prefetch_desc(&tmK);
           tma_prefetch_desc(&tmV);
@@ -344,21 +344,22 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         {
-          // Q: boxes of 16 tokens of one head, eight to a tile; rows of boxes without a new token are
-          // never read for a stored row
+          // Q: a tile of 128 tokens of one head is one box, others are boxes of 16 tokens of one
+          // head; rows of boxes without a new token are never read for a stored row
           const ChunkRows::Shape z(seq, a.group);
+          const bool whole = z.log_tokens == 7;
           const int x = x0 + (lane >> 4), box = lane & 7, p = (lane >> 3) & 1;
-          const int tt = x / z.head_tiles;
-          const int per_head = 1 << (z.log_tokens - 4);  // boxes of one head
-          const int tok = (tt << z.log_tokens) + (box & (per_head - 1)) * kQBox;
-          const int head = (x - tt * z.head_tiles) * z.heads + box / per_head;
-          const bool mine = p < C::kPanels && x < z.tiles && tok < seq.n && head < a.group;
+          const int tt = z.head_tiles == 1 ? x : x / z.head_tiles;
+          const int log_boxes = z.log_tokens - 4;  // boxes of one head
+          const int tok = (tt << z.log_tokens) + (box & ((1 << log_boxes) - 1)) * kQBox;
+          const int head = (x - tt * z.head_tiles) * z.heads + (box >> log_boxes);
+          const bool mine = p < C::kPanels && x < z.tiles && tok < seq.n && head < a.group && !(whole && box > 0);
           const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-          if (lane == 0) mbar_arrive_expect_tx(bar(B_QFULL), boxes * kQBox * 128);
+          if (lane == 0) mbar_arrive_expect_tx(bar(B_QFULL), boxes * (whole ? kTileM : kQBox) * 128);
           __syncwarp();
           if (mine)
-            tma_load_3d(sb + C::kQ + (x & 1) * C::kTileBytes + p * kPanelBytes + box * kQBox * 128, &tmQ, bar(B_QFULL),
-                        p * 64, seq.a + tok, h * a.group + head);
+            tma_load_3d(sb + C::kQ + (x & 1) * C::kTileBytes + p * kPanelBytes + box * kQBox * 128, whole ? &tmQ : &tmQ16,
+                        bar(B_QFULL), p * 64, seq.a + tok, h * a.group + head);
         }
         last_q = v;
         if constexpr (!kE4M3) {
@@ -555,26 +556,22 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         tc_fence_after();
         uint32_t sv[128];
         tmem_ld128(s_addr, sv);
-        // tiles with every column visible to every row of the warp take the short path
-        const bool full = __all_sync(0xffffffffu, lim >= kTileN);
-        float mx;
-        if (full) {
-          float mc[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            mc[c] = __uint_as_float(sv[32 * c]);
-#pragma unroll
-            for (int e = 0; e < 15; ++e)
-              mc[c] = max3f(mc[c], __uint_as_float(sv[32 * c + 1 + 2 * e]), __uint_as_float(sv[32 * c + 2 + 2 * e]));
-            mc[c] = fmaxf(mc[c], __uint_as_float(sv[32 * c + 31]));
-          }
-          mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-        } else {
-          mx = -INFINITY;
+        // columns that a row does not see become -inf, whose exp2 is 0 (most tiles have none)
+        if (!__all_sync(0xffffffffu, lim >= kTileN)) {
 #pragma unroll
           for (int e = 0; e < 128; ++e)
-            if (e < lim) mx = fmaxf(mx, __uint_as_float(sv[e]));
+            if (e >= lim) sv[e] = 0xff800000u;
         }
+        float mc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mc[c] = __uint_as_float(sv[32 * c]);
+#pragma unroll
+          for (int e = 0; e < 15; ++e)
+            mc[c] = max3f(mc[c], __uint_as_float(sv[32 * c + 1 + 2 * e]), __uint_as_float(sv[32 * c + 2 + 2 * e]));
+          mc[c] = fmaxf(mc[c], __uint_as_float(sv[32 * c + 31]));
+        }
+        const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
         const float m_new = fmaxf(m_used, mx * a.scale_log2);
         float alpha = 1.f;
         const bool grow = m_new > m_used + kRescaleThreshold;
@@ -588,38 +585,22 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         float rowsum = 0.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (full) {
-            float2 acc2 = make_float2(0.f, 0.f);
+          float2 acc2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 2 * half; c < 2 * half + 2; ++c) {
-              uint32_t pk[16];
+          for (int c = 2 * half; c < 2 * half + 2; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int i0 = 32 * c + 2 * e;
-                const float2 y = ffma2(__uint_as_float(sv[i0]), __uint_as_float(sv[i0 + 1]), a.scale_log2, a.scale_log2,
-                                       -mb, -mb);
-                const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
-                acc2 = fadd2(acc2.x, acc2.y, p0, p1);
-                pk[e] = pack_bf16(p0, p1);
-              }
-              tmem_st16(s_addr + c * 16, pk);
+            for (int e = 0; e < 16; ++e) {
+              const int i0 = 32 * c + 2 * e;
+              const float2 y = ffma2(__uint_as_float(sv[i0]), __uint_as_float(sv[i0 + 1]), a.scale_log2, a.scale_log2,
+                                     -mb, -mb);
+              const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+              acc2 = fadd2(acc2.x, acc2.y, p0, p1);
+              pk[e] = pack_bf16(p0, p1);
             }
-            rowsum += acc2.x + acc2.y;
-          } else {
-#pragma unroll
-            for (int c = 2 * half; c < 2 * half + 2; ++c) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int c0 = c * 32 + 2 * e;
-                const float p0 = (c0 < lim) ? fast_exp2(fmaf(__uint_as_float(sv[c0]), a.scale_log2, -mb)) : 0.f;
-                const float p1 = (c0 + 1 < lim) ? fast_exp2(fmaf(__uint_as_float(sv[c0 + 1]), a.scale_log2, -mb)) : 0.f;
-                rowsum += p0 + p1;
-                pk[e] = pack_bf16(p0, p1);
-              }
-              tmem_st16(s_addr + c * 16, pk);
-            }
+            tmem_st16(s_addr + c * 16, pk);
           }
+          rowsum += acc2.x + acc2.y;
           if (half == 0) {
             // rows whose maximum grew are rescaled once PV of the key tile before is complete
             // (warp-uniform TMEM access)
@@ -658,15 +639,12 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         continue;
       }
       const float inv = T.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-      // Each 32-column slice of the warp's rows goes through a shared [32][32] float32 block
-      // (16-byte slots XOR-swizzled by row), so that stores write whole row segments
-      float4* stg = reinterpret_cast<float4*>(smem + C::kStage + warp * 4096);
-      auto place = [&](int rr, int& tk, int& hd) -> bool {  // row rr of the tile
-        tk = tok0 + (rr & ((1 << z.log_tokens) - 1));
-        hd = head0 + (rr >> z.log_tokens);
-        return tk < T.n && hd < a.group;
-      };
-#pragma unroll
+      // The warp's rows go through a shared block of 32 rows x 128 bytes (16-byte slots XOR-swizzled
+      // by row), 64 bf16 or 32 float32 channels at a time, so that stores write whole row segments:
+      // lane l writes slot l % 8 of rows l / 8 + 4 i
+      uint8_t* stg = smem + C::kStage + warp * 4096;
+      const int wrow = (warp & 3) * 32, sub = lane >> 3, e8 = lane & 7;
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t ov[32];
         tmem_ld32(o_addr + c * 32, ov);
@@ -674,40 +652,36 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           tc_fence_before();
           mbar_arrive_warp(bar(B_OFREE + t));
         }
-        if (c > 0) __syncwarp();  // the previous slice has been read out of the block
+        const bool wide = T.slot >= 0;  // 32 float32 channels fill the rows, 32 bf16 ones half of them
+        if (wide || (c & 1) == 0) __syncwarp();  // the block has been read out
+        if (wide) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          stg[lane * 8 + (e ^ (lane & 7))] =
-              make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
-                          __uint_as_float(ov[4 * e + 2]) * inv, __uint_as_float(ov[4 * e + 3]) * inv);
-        __syncwarp();
-        const int wrow = (warp & 3) * 32;
-        if (T.slot >= 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3), e = lane & 7;
-            int tk, hd;
-            if (place(wrow + rr, tk, hd)) {
-              const long long at = static_cast<long long>(T.slot) * P::kRows + t * kTileM + wrow + rr;
-              reinterpret_cast<float4*>(a.part_o + at * D)[c * 8 + e] = stg[rr * 8 + (e ^ (rr & 7))];
-            }
-          }
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(stg + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2), e = lane & 3;
-            int tk, hd;
-            if (place(wrow + rr, tk, hd)) {
-              const float4 y0 = stg[rr * 8 + ((2 * e) ^ (rr & 7))], y1 = stg[rr * 8 + ((2 * e + 1) ^ (rr & 7))];
-              const long long at = static_cast<long long>(T.h * a.group + hd) * a.c.total_new + T.a + tk;
-              uint4 pk;
-              pk.x = pack_bf16(y0.x, y0.y);
-              pk.y = pack_bf16(y0.z, y0.w);
-              pk.z = pack_bf16(y1.x, y1.y);
-              pk.w = pack_bf16(y1.z, y1.w);
-              reinterpret_cast<uint4*>(a.o + at * D + c * 32)[e] = pk;
-            }
+          for (int e = 0; e < 4; ++e) {
+            uint4 pk;
+            pk.x = pack_bf16(__uint_as_float(ov[8 * e]) * inv, __uint_as_float(ov[8 * e + 1]) * inv);
+            pk.y = pack_bf16(__uint_as_float(ov[8 * e + 2]) * inv, __uint_as_float(ov[8 * e + 3]) * inv);
+            pk.z = pack_bf16(__uint_as_float(ov[8 * e + 4]) * inv, __uint_as_float(ov[8 * e + 5]) * inv);
+            pk.w = pack_bf16(__uint_as_float(ov[8 * e + 6]) * inv, __uint_as_float(ov[8 * e + 7]) * inv);
+            *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) = pk;
           }
+          if ((c & 1) == 0) continue;
+        }
+        __syncwarp();
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + sub, rt = wrow + rr;  // row of the warp, of the tile
+          const int tk = tok0 + (rt & ((1 << z.log_tokens) - 1)), hd = head0 + (rt >> z.log_tokens);
+          if (tk >= T.n || hd >= a.group) continue;
+          const uint4 y = *reinterpret_cast<const uint4*>(stg + rr * 128 + ((e8 ^ (rr & 7)) << 4));
+          if (wide)
+            reinterpret_cast<uint4*>(a.part_o + (static_cast<long long>(T.slot) * P::kRows + t * kTileM + rt) * D)[c * 8 + e8] = y;
+          else
+            reinterpret_cast<uint4*>(a.o + (static_cast<long long>(T.h * a.group + hd) * a.c.total_new + T.a + tk) * D)[(c >> 1) * 8 + e8] = y;
         }
       }
       __syncwarp();  // the block is free for the next unit's epilogue
@@ -737,8 +711,9 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 template <int D, bool kE4M3>
 fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s) {
   using C = Cfg<D>;
-  CUtensorMap mq, mk = {}, mv = {};
-  if (const fcp_status st = make_bf16_map(&mq, a.q, hq, a.c.total_new, D, kQBox); st != FCP_OK) return st;
+  CUtensorMap mq, mq16, mk = {}, mv = {};
+  if (const fcp_status st = make_bf16_map(&mq, a.q, hq, a.c.total_new, D, kTileM); st != FCP_OK) return st;
+  if (const fcp_status st = make_bf16_map(&mq16, a.q, hq, a.c.total_new, D, kQBox); st != FCP_OK) return st;
   if constexpr (!kE4M3) {
     // pages and heads are the maps' outer dimension; a box is a page's rows, at most a tile
     const long long outer = static_cast<long long>(a.c.n_pages) * a.c.hkv;
@@ -752,7 +727,7 @@ fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s)
   set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
   FCP_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes),
                "paged chunk smem attribute");
-  chunk_kernel<D, kE4M3><<<blocks, kThreads<kE4M3>, C::kSmemBytes, s>>>(mq, mk, mv, a);
+  chunk_kernel<D, kE4M3><<<blocks, kThreads<kE4M3>, C::kSmemBytes, s>>>(mq, mq16, mk, mv, a);
   FCP_CUDA_TRY(cudaGetLastError(), "paged chunk launch");
   return launch_merge<ChunkRows, D>(a, blocks, 32, s);
 }

@@ -35,6 +35,12 @@ struct AttnArgs {
   const __nv_bfloat16* q;
 };
 
+// a / b of lengths that nearly always fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // First key that no row of a unit ending with new token `last` sees.
 __device__ __forceinline__ int key_end(const SeqShape& s, int last, int causal) {
   return causal ? max(0, s.len - s.n + min(last, s.n - 1) + 1) : s.len;
@@ -52,7 +58,7 @@ struct FewRows {
     return static_cast<int>((static_cast<long long>(s.n) * group + kRows - 1) / kRows);
   }
   static __device__ __forceinline__ int end(const SeqShape& s, int group, int u, int causal) {
-    return key_end(s, static_cast<int>(((u + 1ll) * kRows - 1) / group), causal);
+    return key_end(s, static_cast<int>(quotient((u + 1ll) * kRows - 1, group)), causal);
   }
   static __device__ __forceinline__ long long head_length(const SeqShape& s, int group, int causal) {
     long long sum = 0;
@@ -72,7 +78,7 @@ struct FewRows {
   // (token, head of the group) of row r of unit u; false behind the last
   static __device__ __forceinline__ bool row(const SeqShape& s, int group, int u, int r, int& tok, int& head) {
     const long long x = static_cast<long long>(u) * kRows + r;
-    tok = static_cast<int>(x / group);
+    tok = static_cast<int>(quotient(x, group));
     head = static_cast<int>(x - static_cast<long long>(tok) * group);
     return tok < s.n;
   }
@@ -117,7 +123,7 @@ struct ChunkRows {
       const int next = z.first_unit(tt + 1), len = z.length(s, tt, causal);
       const long long behind = f0 + static_cast<long long>(next - u) * len;
       if (f < behind) {
-        const int x = static_cast<int>((f - f0) / len);
+        const int x = static_cast<int>(quotient(f - f0, len));
         f0 += static_cast<long long>(x) * len;
         return u + x;
       }
@@ -231,7 +237,7 @@ __device__ __forceinline__ bool seek(const AttnArgs& a, const Line<kThreads>& li
     w.f0 += per_head * a.c.hkv;
     ++w.i;
   }
-  w.h = static_cast<int>((f - w.f0) / per_head);
+  w.h = static_cast<int>(quotient(f - w.f0, per_head));
   w.f0 += w.h * per_head;
   w.n_units = P::units(w.s, a.group);
   w.u = P::find(w.s, a.group, a.causal, f, w.f0);
@@ -246,13 +252,13 @@ struct Shares {
   int rem, blocks;
   __device__ __forceinline__ Shares(long long total, int grid)
       : blocks(static_cast<int>(min(total, static_cast<long long>(grid)))) {
-    base = blocks > 0 ? total / blocks : 0;
+    base = blocks > 0 ? quotient(total, blocks) : 0;
     rem = static_cast<int>(total - base * blocks);
   }
   __device__ __forceinline__ long long begin(int b) const { return base * b + rem * b / blocks; }
   // The block that takes place f.
   __device__ __forceinline__ int owner(long long f) const {
-    int b = static_cast<int>(f / (base + 1));
+    int b = static_cast<int>(quotient(f, base + 1));
     while (begin(b + 1) <= f) ++b;
     return b;
   }
@@ -273,8 +279,8 @@ struct SplitGroup {
 static_assert(sizeof(SplitGroup) == 32, "two 16-byte loads");
 
 // Joins the pieces of the groups that blocks split: with M the largest of a row's maxima,
-// O = sum 2^(m - M) o / sum 2^(m - M) l, over the pieces in their order. grid (blocks, row
-// slices); a block takes one row after another, its warps every fourth piece of it. Launched
+// O = sum 2^(m - M) o / sum 2^(m - M) l, over the pieces in a fixed order. grid (blocks, row
+// slices); a warp takes a row of up to 8 pieces, the whole block one of more. Launched
 // so that it may start while the attention still runs: it waits for it in the kernel.
 constexpr int kMergeWarps = 4;
 template <class P, int D>
@@ -290,6 +296,49 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Att
   const int count = g.last - b + 1;
   if (count <= 1) return;
   const SeqShape s{g.a, g.n, 0};
+  if (count <= 8) {
+    // few pieces: a warp takes a row on its own
+    constexpr int kEach = D / 32;  // channels of a lane
+    for (int r = blockIdx.y * kMergeWarps + warp; r < P::kRows; r += gridDim.y * kMergeWarps) {
+      int tok, head;
+      if (!P::row(s, a.group, g.u, r, tok, head)) continue;
+      float y[8][kEach];
+      float2 ml[8];
+      float m = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        ml[x] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) y[x][e] = 0.f;
+        if (x < count) {
+          const long long at = static_cast<long long>(2 * (b + x) + (x == 0)) * P::kRows + r;
+          ml[x] = a.part_ml[at];
+#pragma unroll
+          for (int e = 0; e < kEach; e += 2)
+            *reinterpret_cast<float2*>(&y[x][e]) = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * kEach + e);
+        }
+        m = fmaxf(m, ml[x].x);
+      }
+      const float mb = m == -INFINITY ? 0.f : m;
+      float l = 0.f, acc[kEach];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float f = exp2f(ml[x].x - mb);
+        l = fmaf(f, ml[x].y, l);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) acc[e] = fmaf(f, y[x][e], acc[e]);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const long long row = static_cast<long long>(g.h * a.group + head) * a.c.total_new + s.a + tok;
+#pragma unroll
+      for (int e = 0; e < kEach; e += 2)
+        *reinterpret_cast<uint32_t*>(a.o + row * D + lane * kEach + e) = dev::pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+      if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+    return;
+  }
   for (int r = blockIdx.y; r < P::kRows; r += gridDim.y) {
     int tok, head;
     if (!P::row(s, a.group, g.u, r, tok, head)) continue;
