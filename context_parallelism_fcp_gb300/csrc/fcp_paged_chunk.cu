@@ -85,23 +85,20 @@ struct Cfg {
   static constexpr uint32_t kIdescPV = idesc_bf16(kTileM, D, false, true);
 };
 
-// 16 codes and their row's scale byte as 16 bf16 channels: code * 2^(byte - 127). The code's bits
-// in bf16's fields are code * 2^-120, and 2^120 is taken into the scale where bf16 holds the
+// 8 codes and their row's scale byte as 8 bf16 channels: code * 2^(byte - 127). The code's bits in
+// bf16's fields are code * 2^-120, and 2^120 is taken into the scale where bf16 holds the
 // product of both; larger scales take two exact products.
-__device__ __forceinline__ void scaled16(const uint4 x, uint32_t byte, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t r[8];
+__device__ __forceinline__ uint4 scaled8(const uint2 x, uint32_t byte) {
+  uint32_t r[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t y = __byte_perm(w[i], 0, j ? 0x3424 : 0x1404);
-      r[2 * i + j] = (y & 0x80008000u) | ((y & 0x7f007f00u) >> 4);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t y = __byte_perm(i < 2 ? x.x : x.y, 0, i & 1 ? 0x3424 : 0x1404);
+    r[i] = (y & 0x80008000u) | ((y & 0x7f007f00u) >> 4);
+  }
   auto times = [&](uint32_t f) {
     f |= f << 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 y =
           __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]), *reinterpret_cast<const __nv_bfloat162*>(&f));
       r[i] = *reinterpret_cast<const uint32_t*>(&y);
@@ -109,8 +106,7 @@ __device__ __forceinline__ void scaled16(const uint4 x, uint32_t byte, uint4& lo
   };
   times((min(byte, 134u) + 120u) << 7);
   if (byte > 134u) times(byte == 255u ? 0x7fc0u : (byte - 7u) << 7);
-  lo = make_uint4(r[0], r[1], r[2], r[3]);
-  hi = make_uint4(r[4], r[5], r[6], r[7]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <int D, bool kE4M3>
@@ -204,90 +200,91 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
     if constexpr (kE4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp >= 10) {
       // ---------------------------------------------------------- loaders (e4m3)
-      // The 16-row groups of K of a tile, then of V, then of the next tile's K, go round the loader
-      // warps; a group lies in one page. Lane l turns codes [16 (l % kLanes), + 16) of rows l /
-      // kLanes + kRowsAtOnce x into 32 bytes of bf16. A warp's next group is loaded before its
-      // current one is converted.
-      constexpr int kLanes = D / 16;
-      constexpr int kRowsAtOnce = 32 / kLanes;
-      constexpr int kPasses = 16 / kRowsAtOnce;
-      const int r0 = lane / kLanes, c = lane % kLanes;
+      // The work is 16-row groups, each in one page: K's eight of a tile, V's eight, the next tile's.
+      // They go round the six warps; the two that share their scheduler with no other loader take a
+      // sixth turn in every 32. A warp's next group is on its way while it converts one, and the
+      // page of the one after is looked up (and only looked at when its turn has come: a check at
+      // once would wait for the lookup). Lane l has codes [8 (l % 8), + 8) of each 64 channels of rows
+      // l / 8 + 4 x: a 16-byte piece of bf16 each, eight lanes to a 128-byte line.
+      const int r0 = lane >> 3, c = lane & 7;
       const int page_mask = (1 << a.c.page_shift) - 1;
+      const int order = warp == 12 ? 0 : (warp == 13 ? 1 : (warp < 12 ? warp - 8 : warp - 10));
+      int turn = 0;
+      // from a group of this warp to its next: 32 groups are five rounds of six and two more
+      auto step = [&]() -> int {
+        const int last = order < 2 ? 5 : 4;
+        const int d = turn < last ? 6 : (order < 2 ? 2 : 8);
+        turn = turn < last ? turn + 1 : 0;
+        return d;
+      };
       bool ok = true;
-      int J0 = 0;       // key tiles before this unit
-      int skip = warp - 10;  // groups of this unit that come before the warp's first
+      int J0 = 0;                            // key tiles before this unit
+      int g1 = order, g2 = g1 + step();      // groups held: converted next, and after that
       for (int v = 0; ok; ++v) {
         const Unit t = next_unit(v, kErrPagedWait + 1);
         if (t.valid <= 0) break;
         const int* table = a.c.table + static_cast<long long>(t.i) * a.c.max_pages;
-        const int n_groups = (t.kt1 - t.kt0) * 16;
-        auto lookup = [&](int gi) -> int {  // the page of group gi; -1: its rows become zeros
-          const int key0 = (t.kt0 + (gi >> 4)) * kTileN + 16 * (gi & 7);
-          if (gi >= n_groups || key0 >= t.len) return -1;
-          const int page = __ldg(table + (key0 >> a.c.page_shift));
-          if (page >= 0 && page < a.c.n_pages) return page;
-          atomicCAS(err, 0, kErrCachePage);
-          return -1;
+        const int g_end = (J0 + t.kt1 - t.kt0) * 16;
+        auto first_key = [&](int g) -> int { return (t.kt0 + (g >> 4) - J0) * kTileN + 16 * (g & 7); };
+        auto lookup = [&](int g) -> int {  // the block table's entry for group g; -1: nothing to read
+          const int key0 = first_key(g);
+          return g < g_end && key0 < t.len ? __ldg(table + (key0 >> a.c.page_shift)) : -1;
         };
-        uint4 raw[kPasses];
-        uint32_t byte[kPasses];
-        auto load = [&](int gi, int page) {
-          const int key0 = (t.kt0 + (gi >> 4)) * kTileN + 16 * (gi & 7);
-          const bool is_v = (gi & 8) != 0;
-          const long long row0 = (page >= 0 ? page_row(a.c, page, t.h) + (key0 & page_mask) : 0) + r0;
-          const uint8_t* src = (is_v ? a.c.v_pages : a.c.k_pages) + row0 * D + c * 16;
-          const uint8_t* sc = (is_v ? a.c.v_scales : a.c.k_scales) + row0;
-          const int held = page >= 0 ? t.len - key0 - r0 : 0;  // rows below held are there
+        uint2 raw[4][C::kPanels];
+        uint32_t byte[4];
+        const uint8_t* src = nullptr;
+        const uint8_t* sc = nullptr;
+        int held = 0;  // rows r0 + 4 x with 4 x below it are there; the others become zeros
+        auto aim = [&](int g, int page) {
+          const int key0 = first_key(g);
+          const bool is_v = (g & 8) != 0, in = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages);
+          if (!in && g < g_end && key0 < t.len) atomicCAS(err, 0, kErrCachePage);
+          const long long row = (in ? page_row(a.c, page, t.h) + (key0 & page_mask) : 0) + r0;
+          src = (is_v ? a.c.v_pages : a.c.k_pages) + row * D + c * 8;
+          sc = (is_v ? a.c.v_scales : a.c.k_scales) + row;
+          held = in ? t.len - key0 - r0 : 0;
+        };
+        auto load = [&](int x) {
 #pragma unroll
-          for (int x = 0; x < kPasses; ++x) {
-            raw[x] = make_uint4(0u, 0u, 0u, 0u);
-            byte[x] = 127u;
-            if (x * kRowsAtOnce < held) {
-              raw[x] = __ldg(reinterpret_cast<const uint4*>(src + x * kRowsAtOnce * D));
-              byte[x] = __ldg(sc + x * kRowsAtOnce);
-            }
+          for (int p = 0; p < C::kPanels; ++p) raw[x][p] = make_uint2(0u, 0u);
+          byte[x] = 127u;
+          if (4 * x < held) {
+#pragma unroll
+            for (int p = 0; p < C::kPanels; ++p)
+              raw[x][p] = __ldg(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
+            byte[x] = __ldg(sc + 4 * x);
           }
         };
-        int gi = skip;
-        int page_next = lookup(gi);
-        load(gi, page_next);
-        page_next = lookup(gi + kLoaders);
-        for (; gi < n_groups; gi += kLoaders) {
-          uint4 cur[kPasses];
-          uint32_t f[kPasses];
+        aim(g1, lookup(g1));
 #pragma unroll
-          for (int x = 0; x < kPasses; ++x) {
-            cur[x] = raw[x];
-            f[x] = byte[x];
-          }
-          load(gi + kLoaders, page_next);
-          page_next = lookup(gi + 2 * kLoaders);
-          const int J = J0 + (gi >> 4), s = J & 1;
-          const bool is_v = (gi & 8) != 0;
+        for (int x = 0; x < 4; ++x) load(x);
+        int page2 = lookup(g2);
+        while (g1 < g_end) {
+          const int J = g1 >> 4, s = J & 1;  // the block's key tile
+          const bool is_v = (g1 & 8) != 0;
+          aim(g2, page2);
+          const int g3 = g2 + step();
+          page2 = lookup(g3);
           ok = mbar_wait(bar((is_v ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          uint8_t* dst = smem + (is_v ? C::kV : C::kK) + s * C::kTileBytes + (c >> 2) * kPanelBytes + 16 * (gi & 7) * 128;
-          // lanes of the row's other panel store their two pieces in the other order, so that the
-          // eight lanes that store together always hit different banks
-          const int swap = (c >> 2) & 1;
+          uint8_t* dst = smem + (is_v ? C::kV : C::kK) + s * C::kTileBytes + (16 * (g1 & 7) + r0) * 128;
 #pragma unroll
-          for (int x = 0; x < kPasses; ++x) {
-            const int r = r0 + x * kRowsAtOnce;
-            uint4 lo, hi;
-            scaled16(cur[x], f[x], lo, hi);
-            const int p = (2 * c) & 7;
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((p + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((p + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+          for (int x = 0; x < 4; ++x) {
+            uint8_t* to = dst + 4 * x * 128 + ((c ^ ((r0 + 4 * x) & 7)) << 4);  // swizzled by the row's last bits
+#pragma unroll
+            for (int p = 0; p < C::kPanels; ++p)
+              *reinterpret_cast<uint4*>(to + p * kPanelBytes) = scaled8(raw[x][p], byte[x]);
+            load(x);  // of the next group
           }
           fence_proxy_async_smem();
           mbar_arrive_warp(bar((is_v ? B_VFULL : B_KFULL) + s));
+          g1 = g2;
+          g2 = g3;
         }
-        skip = gi - n_groups;
         J0 += t.kt1 - t.kt0;
       }
-    } else
-    if (warp == 8) {
+    } else if (warp == 8) {
       // ---------------------------------------------------------- walk, Q and (bf16) K, V loads
       // Lane 0 walks along the block's share and publishes each unit; then the lanes issue its
       // loads side by side: box j of Q, or page j of a key tile, is lane j's.
