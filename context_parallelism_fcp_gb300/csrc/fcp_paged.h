@@ -65,6 +65,11 @@ __device__ __forceinline__ float e8m0_to_float(uint32_t b) {
   return __uint_as_float(bits);
 }
 
+// log2 of the same.
+__device__ __forceinline__ float e8m0_log2(uint32_t b) {
+  return b == 255u ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(b) - 127);
+}
+
 // Two e4m3 codes in bits 8-15 and 24-31 as bf16x2. The code's exponent and mantissa sit in
 // bf16's fields with its bias 7 instead of 127, so one exact product with 2^120 gives the
 // value; code subnormals are bf16 subnormals before it. (Codes 0x7f and 0xff, which a written

@@ -11,12 +11,20 @@
 // with float32 sums: with 16 rows tcgen05's 128-row tile would be seven eighths empty, and
 // both units are far faster than the loads.
 //
+// An e4m3 cache's codes become f16 by the hardware's conversion, two to an instruction, and the
+// products run in f16: a code is exact there, Q's rows are scaled to a largest exponent of 14
+// (a power of two for each row, exact but for elements 2^-28 times the largest), and the rows'
+// scales multiply the scores. V's scale goes into the exponent of P: with s' = s + log2(scale)
+// the sum for O runs relative to the maximum of s', the sum of weights relative to that of s.
+//
 // K is read from shared memory 16 bytes to a lane: the product over channels does not care for
 // their order, so lane j of a quad takes 8 (bf16) or 16 (e4m3) neighbouring channels and Q's
 // fragments are laid out the same way. V goes through ldmatrix.trans; for e4m3 the 16-bit
 // elements that it transposes are channel pairs, whose low and high bytes become the fragments
 // of two 8-channel tiles. 16-byte pieces of a row are XOR-swizzled so that neither reading has
 // bank conflicts.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -83,6 +91,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the same in f16
+__device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes as f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n.reg .b16 h;\ncvt.u16.u32 h, %1;\ncvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 struct Piece {
@@ -189,12 +215,43 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
         }
       }
 
-    float m[MT][2], l[MT][2], acc[MT][D / 8][4];
+    // e4m3: Q's rows as f16 scaled by 2^(14 - e), e the largest exponent of the row; scores take
+    // back 2^(e - 14) with the factor that brings them to log2 units
+    float row_factor[MT][2];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        row_factor[t][x] = a.scale_log2;
+        if constexpr (kE4M3) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int y = 0; y < 4; y += 2)
+              top = max(top, max(q[t][c][y + x] & 0x7fffu, (q[t][c][y + x] >> 16) & 0x7fffu));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int up = min(126, 141 - static_cast<int>(top >> 7));  // 14 - (exponent - 127), of rows past 2^-113
+          const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+          row_factor[t][x] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int y = 0; y < 4; y += 2)
+              q[t][c][y + x] = pack_f16(__uint_as_float(q[t][c][y + x] << 16) * f,
+                                        __uint_as_float(q[t][c][y + x] & 0xffff0000u) * f);
+        }
+      }
+
+    // m: the maximum of a row's scores, which its weights' sum l is relative to; mo: for e4m3 that of
+    // scores with V's scale, which acc is relative to
+    float m[MT][2], l[MT][2], mo[MT][2], acc[MT][D / 8][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        m[t][x] = -INFINITY;
+        m[t][x] = mo[t][x] = -INFINITY;
         l[t][x] = 0.f;
       }
 #pragma unroll
@@ -262,10 +319,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
             const uint32_t raw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const uint32_t b0 = e4m3x2_to_bf16x2(__byte_perm(raw[x], 0, 0x1404));
-              const uint32_t b1 = e4m3x2_to_bf16x2(__byte_perm(raw[x], 0, 0x3424));
+              const uint32_t b0 = e4m3x2_to_f16x2(raw[x]), b1 = e4m3x2_to_f16x2(raw[x] >> 16);
 #pragma unroll
-              for (int t = 0; t < MT; ++t) mma16816(sc[t][y], q[t][4 * c + x], b0, b1);
+              for (int t = 0; t < MT; ++t) mma16816h(sc[t][y], q[t][4 * c + x], b0, b1);
             }
           }
         } else {
@@ -281,28 +337,27 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
         }
       }
       // scores in log2 units; columns of this lane: keys key + 8 y + 2 j + {0, 1}
-      float vs[2][2];
+      float vs[2][2];  // log2 of V's scales
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        float f0 = a.scale_log2, f1 = a.scale_log2;
+        float f0 = 1.f, f1 = 1.f;
         if constexpr (kE4M3) {
           const uint32_t kb = lds_u16(kt + 2 * C::kTile + 8 * y + 2 * j);
           const uint32_t vb = lds_u16(kt + 2 * C::kTile + 16 + 8 * y + 2 * j);
-          f0 *= e8m0_to_float(kb & 255u);
-          f1 *= e8m0_to_float(kb >> 8);
-          vs[y][0] = e8m0_to_float(vb & 255u);
-          vs[y][1] = e8m0_to_float(vb >> 8);
+          f0 = e8m0_to_float(kb & 255u);
+          f1 = e8m0_to_float(kb >> 8);
+          vs[y][0] = e8m0_log2(vb & 255u);
+          vs[y][1] = e8m0_log2(vb >> 8);
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          sc[t][y][0] *= f0;
-          sc[t][y][1] *= f1;
-          sc[t][y][2] *= f0;
-          sc[t][y][3] *= f1;
-        }
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            sc[t][y][2 * x] *= kE4M3 ? row_factor[t][x] * f0 : row_factor[t][x];
+            sc[t][y][2 * x + 1] *= kE4M3 ? row_factor[t][x] * f1 : row_factor[t][x];
+          }
       }
-      const bool masked = key + kChunk > lim_min;  // some row does not see the whole chunk
-      if (masked) {
+      if (key + kChunk > lim_min) {  // some row does not see the whole chunk
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -313,26 +368,35 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
       }
       // raise the running maxima only when some row's grew by more than 2^8: P stays below 2^8
       bool grow = false;
-      float top[MT][2];
+      float top[MT][2], topo[MT][2];
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top[t][x] = fmaxf(fmaxf(sc[t][0][2 * x], sc[t][0][2 * x + 1]), fmaxf(sc[t][1][2 * x], sc[t][1][2 * x + 1]));
           grow = grow || top[t][x] > m[t][x] + kGrow;
+          if constexpr (kE4M3) {
+            topo[t][x] = fmaxf(fmaxf(sc[t][0][2 * x] + vs[0][0], sc[t][0][2 * x + 1] + vs[0][1]),
+                               fmaxf(sc[t][1][2 * x] + vs[1][0], sc[t][1][2 * x + 1] + vs[1][1]));
+            grow = grow || topo[t][x] > mo[t][x] + kGrow;
+          }
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float mx = top[t][x];
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            mx = fmaxf(mx, m[t][x]);
-            const float f = mx == -INFINITY ? 1.f : fast_exp2(m[t][x] - mx);
-            m[t][x] = mx;
+            auto raise = [](float& at, float to) -> float {  // the factor of what was relative to `at`
+              to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 1));
+              to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 2));
+              to = fmaxf(to, at);
+              const float f = to == -INFINITY ? 1.f : fast_exp2(at - to);
+              at = to;
+              return f;
+            };
+            float f = raise(m[t][x], top[t][x]);
             l[t][x] *= f;
+            if constexpr (kE4M3) f = raise(mo[t][x], topo[t][x]);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
               acc[t][c][2 * x] *= f;
@@ -344,22 +408,24 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int x = 0; x < 2; ++x) {
+          const float mb = m[t][x] == -INFINITY ? 0.f : m[t][x];
+          const float mob = mo[t][x] == -INFINITY ? 0.f : mo[t][x];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float mb = m[t][x] == -INFINITY ? 0.f : m[t][x];
-            float p0 = fast_exp2(sc[t][y][2 * x] - mb);
-            float p1 = fast_exp2(sc[t][y][2 * x + 1] - mb);
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = fast_exp2(sc[t][y][2 * x] - mb), p1 = fast_exp2(sc[t][y][2 * x + 1] - mb);
             l[t][x] += p0 + p1;
             if constexpr (kE4M3) {
-              // V's scale goes with P; a key that the row does not see keeps its exact zero,
-              // whatever its scale
-              const int k = key + 8 * y + 2 * j;
-              p0 = masked && k >= lim[t][x] ? 0.f : p0 * vs[y][0];
-              p1 = masked && k + 1 >= lim[t][x] ? 0.f : p1 * vs[y][1];
+              // in f16: off by 2^-11 of itself, or 2^-25 of a row's largest. An unseen key's -inf stays
+              // -inf whatever V's scale is, except NaN
+              const float s0 = sc[t][y][2 * x], s1 = sc[t][y][2 * x + 1];
+              pa[t][2 * y + x] = pack_f16(s0 == -INFINITY ? 0.f : fast_exp2(s0 + vs[y][0] - mob),
+                                          s1 == -INFINITY ? 0.f : fast_exp2(s1 + vs[y][1] - mob));
+            } else {
+              pa[t][2 * y + x] = pack_bf16(p0, p1);  // off by 2^-8 of itself at most
             }
-            pa[t][2 * y + x] = pack_bf16(p0, p1);  // P in bf16: off by 2^-9 of itself at most
           }
+        }
       const int vr = (lane & 7) + (lane & 8);  // ldmatrix: keys 0-7, 8-15, then the next piece
 #pragma unroll
       for (int c = 0; c < C::kPieces; c += 2) {
@@ -368,14 +434,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
         if constexpr (kE4M3) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint32_t even0 = e4m3x2_to_bf16x2((f[2 * y] & 0x00ff00ffu) << 8);
-            const uint32_t even1 = e4m3x2_to_bf16x2((f[2 * y + 1] & 0x00ff00ffu) << 8);
-            const uint32_t odd0 = e4m3x2_to_bf16x2(f[2 * y]);
-            const uint32_t odd1 = e4m3x2_to_bf16x2(f[2 * y + 1]);
+            // bytes: even and odd channel of one key, then of the next; a fragment wants two keys
+            const uint32_t k0 = __byte_perm(f[2 * y], 0, 0x3120), k1 = __byte_perm(f[2 * y + 1], 0, 0x3120);
+            const uint32_t even0 = e4m3x2_to_f16x2(k0), odd0 = e4m3x2_to_f16x2(k0 >> 16);
+            const uint32_t even1 = e4m3x2_to_f16x2(k1), odd1 = e4m3x2_to_f16x2(k1 >> 16);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-              mma16816(acc[t][2 * (c + y)], pa[t], even0, even1);
-              mma16816(acc[t][2 * (c + y) + 1], pa[t], odd0, odd1);
+              mma16816h(acc[t][2 * (c + y)], pa[t], even0, even1);
+              mma16816h(acc[t][2 * (c + y) + 1], pa[t], odd0, odd1);
             }
           }
         } else {
@@ -409,8 +475,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
         float mx = warp_m[0][r];
 #pragma unroll
         for (int y = 1; y < kWarps; ++y) mx = fmaxf(mx, warp_m[y][r]);
-        const float f = mx == -INFINITY ? 0.f : fast_exp2(m[t][x] - mx);
+        float f = mx == -INFINITY ? 0.f : fast_exp2(m[t][x] - mx);
         if (j == 0) warp_l[warp][r] = l[t][x] * f;
+        if constexpr (kE4M3) f = mx == -INFINITY ? 0.f : fast_exp2(mo[t][x] - mx);  // acc's own reference
         float* dst = sums + (static_cast<size_t>(warp) * kRows + r) * D;
         if constexpr (kE4M3) {
           // tiles 2 c and 2 c + 1 hold the even and odd channels of piece c: 4 in a row
