@@ -118,9 +118,10 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   using C = Cfg<D>;
   using P = ChunkRows;
   extern __shared__ __align__(1024) uint8_t smem[];
-  // the line lies where the first epilogue writes, long after the walk has been placed on it
+  // these lie where the first epilogue writes, long after the walk has begun
   Line<kThreads>& line = *reinterpret_cast<Line<kThreads>*>(smem + C::kStage);
-  static_assert(sizeof(Line<kThreads>) <= C::kStageBytes, "the line fits the epilogue's staging");
+  Walk<P>& walk = *reinterpret_cast<Walk<P>*>(smem + C::kStage + 1024);
+  static_assert(sizeof(Line<kThreads>) <= 1024 && 1024 + sizeof(Walk<P>) <= C::kStageBytes, "they fit the staging");
   const uint32_t sb = smem_u32(smem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + B_COUNT * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBar + B_COUNT * 8 + 4);
@@ -133,9 +134,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x;
   if (threadIdx.x == 0) a.split[b].last = b;
-  build_line<P, kThreads>(a, line, b == 0);
+  const Shares sh = begin_walk<P, kThreads>(a, line, walk, b == 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Shares sh(line.prefix[kThreads], gridDim.x);
   if (b >= sh.blocks) return;
   // 128-byte-swizzled tiles need a 1024-byte aligned base; report, never fault
   if ((sb & 1023u) != 0) {
@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         }
       }
       const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
-      Walk<P> w;
-      bool more = lane == 0 && seek<P, kThreads>(a, line, w0, w);
+      Walk<P> w = walk;
+      bool more = true;
       bool ok = true;
       int J = 0;                                    // key tiles loaded
       int last_q = -1, last_kj = -1, last_vj = -1;  // round of the last Q load, tiles of the last K, V loads

@@ -39,10 +39,14 @@ constexpr int kWarps = 4;
 constexpr int kFewThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys of a stage
 constexpr float kGrow = 8.0f;               // a row maximum is raised when it grows by over 2^8
-constexpr int kStageBudget = 96 * 1024;     // shared memory for stages: two blocks fit an SM
+// Blocks to an SM, and the shared memory of their stages. bf16 is at HBM's rate with two; the
+// e4m3 conversion leaves more latency to hide: three (where 16 rows leave the registers).
+template <bool kE4M3, int MT>
+constexpr int kPerSm = kE4M3 && MT == 1 ? 3 : 2;
 
-template <int D, bool kE4M3>
+template <int D, bool kE4M3, int MT>
 struct FewCfg {
+  static constexpr int kStageBudget = (kPerSm<kE4M3, MT> == 3 ? 66 : 96) * 1024;
   static constexpr int kRowBytes = kE4M3 ? D : 2 * D;
   static constexpr int kPieces = kRowBytes / 16;               // 16-byte pieces of a row
   static constexpr int kTile = kChunk * kRowBytes;             // K or V of a chunk
@@ -61,8 +65,11 @@ __device__ __forceinline__ int piece_at(int r, int c) {
   else return r * kRowBytes + ((c ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zeros(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
@@ -80,9 +87,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 // c[16 x 8] += a[16 x 16] b[16 x 8], bf16 in, float32 out
@@ -100,11 +107,11 @@ __device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4],
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 codes as f16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("{\n.reg .b16 h;\ncvt.u16.u32 h, %1;\ncvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(two));
-  return r;
+// Four e4m3 codes as two f16x2, exactly (the NaN codes as NaN).
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -116,40 +123,37 @@ struct Piece {
 };
 
 template <int D, bool kE4M3, int MT>
-__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
-  using C = FewCfg<D, kE4M3>;
+__global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(const AttnArgs a) {
+  using C = FewCfg<D, kE4M3, MT>;
   using P = FewRows<16 * MT>;
   constexpr int kRows = P::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Line<kFewThreads> line;
+  __shared__ Walk<P> walk;
   __shared__ Piece shared_piece;
   __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = lane >> 2, j = lane & 3;  // this lane's fragment rows (row, row + 8) and columns
-  const int b = blockIdx.x, blocks = gridDim.x;
-  build_line<P, kFewThreads>(a, line, b == 0);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long total = line.prefix[kFewThreads];
-  const Shares sh(total, blocks);
+  const int b = blockIdx.x;
   if (threadIdx.x == 0) a.split[b].last = b;
+  const Shares sh = begin_walk<P, kFewThreads>(a, line, walk, b == 0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (b >= sh.blocks) return;
   const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
 
   const uint32_t stages = smem_u32(smem) + warp * C::kWarpBytes;
   float* sums = reinterpret_cast<float*>(smem);  // [kWarps][kRows][D], over the stages at a piece's end
-  static_assert(kWarps * kRows * D * 4 <= kStageBudget, "the warps' sums fit the stages");
+  static_assert(kWarps * kRows * D * 4 <= C::kStageBudget, "the warps' sums fit the stages");
   const int page_mask = (1 << a.c.page_shift) - 1;
 
-  Walk<P> w;
-  bool walking = true;
-  if (threadIdx.x == 0) walking = seek<P, kFewThreads>(a, line, w0, w);
+  Walk<P> w = walk;  // thread 0 goes on from there
   for (bool first = true;; first = false) {
     if (threadIdx.x == 0) {
       if (!first) w.next(a);
       Piece p;
       p.ga = p.gb = 0;
-      while ((p.valid = walking && w.i < a.c.n_seqs && w.f0 < w1)) {
+      while ((p.valid = w.i < a.c.n_seqs && w.f0 < w1)) {
         w.part(w0, w1, p.ga, p.gb);
         if (p.gb > p.ga) break;
         w.next(a);  // the share has the group's overhead only
@@ -171,6 +175,55 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
     const Piece p = shared_piece;
     if (!p.valid) break;
     const SeqShape s{p.a, p.n, p.len};
+
+    // chunks of this warp: keys k0 + 16 * (warp + 4 n) below kend
+    const int k0 = p.ga * kGranule, kend = min(p.gb * kGranule, p.end);
+    const int* table = a.c.table + static_cast<long long>(p.i) * a.c.max_pages;
+    auto page_of = [&](int key) -> int { return key < kend ? __ldg(table + (key >> a.c.page_shift)) : 0; };
+    int issue_key = k0 + kChunk * warp;
+    int issue_page = page_of(issue_key);
+    int issue_stage = 0;
+    auto issue = [&]() {
+      const int key = issue_key;
+      if (key < kend) {
+        bool ok = issue_page >= 0 && issue_page < a.c.n_pages;
+        if (!ok && lane == 0) atomicCAS(a.c.status, 0, kErrCachePage);
+        const long long r0 = ok ? page_row(a.c, issue_page, p.h) + (key & page_mask) : 0;
+        issue_key += kChunk * kWarps;
+        issue_page = page_of(issue_key);
+        const uint32_t dst = stages + issue_stage * C::kStage;
+        constexpr int kPer = 32 / C::kPieces;  // rows of one instruction
+        const int lr = lane / C::kPieces, c = lane % C::kPieces;
+        const long long at = (r0 + lr) * C::kRowBytes + c * 16;
+        const uint8_t* gk = a.c.k_pages + at;
+        const uint8_t* gv = a.c.v_pages + at;
+        if (ok && key + kChunk <= s.len) {
+#pragma unroll
+          for (int x = 0; x < kChunk / kPer; ++x) {
+            const int to = piece_at<C::kRowBytes>(x * kPer + lr, c);
+            cp_async16(dst + to, gk + x * kPer * C::kRowBytes);
+            cp_async16(dst + C::kTile + to, gv + x * kPer * C::kRowBytes);
+          }
+        } else {  // rows behind the last key may hold anything: zeros come in their place
+#pragma unroll 1
+          for (int x = 0; x < kChunk / kPer; ++x) {
+            const bool on = ok && key + x * kPer + lr < s.len;
+            const int to = piece_at<C::kRowBytes>(x * kPer + lr, c);
+            cp_async16_or_zeros(dst + to, on ? gk + x * kPer * C::kRowBytes : a.c.k_pages, on);
+            cp_async16_or_zeros(dst + C::kTile + to, on ? gv + x * kPer * C::kRowBytes : a.c.v_pages, on);
+          }
+        }
+        if constexpr (kE4M3) {
+          if (lane < 2)
+            cp_async16_or_zeros(dst + 2 * C::kTile + 16 * lane, (lane ? a.c.v_scales : a.c.k_scales) + r0, ok);
+        }
+      }
+      cp_commit();
+      issue_stage = issue_stage + 1 == C::kStages ? 0 : issue_stage + 1;
+    };
+#pragma unroll
+    for (int x = 0; x < C::kStages - 1; ++x) issue();
+
 
     // this lane's rows (2 for each 16-row tile): query row, first key it does not see
     uint32_t q[MT][D / 16][4];
@@ -260,41 +313,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
         for (int e = 0; e < 4; ++e) acc[t][c][e] = 0.f;
     }
 
-    // chunks of this warp: keys k0 + 16 * (warp + 4 n) below kend
-    const int k0 = p.ga * kGranule, kend = min(p.gb * kGranule, p.end);
-    const int* table = a.c.table + static_cast<long long>(p.i) * a.c.max_pages;
-    auto page_of = [&](int key) -> int { return key < kend ? __ldg(table + (key >> a.c.page_shift)) : 0; };
-    int issue_key = k0 + kChunk * warp;
-    int issue_page = page_of(issue_key);
-    int issue_stage = 0;
-    auto issue = [&]() {
-      const int key = issue_key;
-      if (key < kend) {
-        bool ok = issue_page >= 0 && issue_page < a.c.n_pages;
-        if (!ok && lane == 0) atomicCAS(a.c.status, 0, kErrCachePage);
-        const long long r0 = ok ? page_row(a.c, issue_page, p.h) + (key & page_mask) : 0;
-        issue_key += kChunk * kWarps;
-        issue_page = page_of(issue_key);
-        const uint32_t dst = stages + issue_stage * C::kStage;
-        constexpr int kPer = 32 / C::kPieces;  // rows of one instruction
-#pragma unroll
-        for (int x = 0; x < kChunk / kPer; ++x) {
-          const int r = x * kPer + lane / C::kPieces, c = lane % C::kPieces;
-          const long long at = (r0 + r) * C::kRowBytes + c * 16;
-          const bool on = ok && key + r < s.len;  // rows behind the last key may hold anything
-          cp_async16(dst + piece_at<C::kRowBytes>(r, c), a.c.k_pages + (on ? at : 0), on);
-          cp_async16(dst + C::kTile + piece_at<C::kRowBytes>(r, c), a.c.v_pages + (on ? at : 0), on);
-        }
-        if constexpr (kE4M3) {
-          if (lane < 2) cp_async16(dst + 2 * C::kTile + 16 * lane, (lane ? a.c.v_scales : a.c.k_scales) + r0, ok);
-        }
-      }
-      cp_commit();
-      issue_stage = issue_stage + 1 == C::kStages ? 0 : issue_stage + 1;
-    };
-#pragma unroll
-    for (int x = 0; x < C::kStages - 1; ++x) issue();
-
     int stage = 0;
     for (int key = k0 + kChunk * warp; key < kend; key += kChunk * kWarps) {
       cp_wait<C::kStages - 2>();
@@ -319,7 +337,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
             const uint32_t raw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const uint32_t b0 = e4m3x2_to_f16x2(raw[x]), b1 = e4m3x2_to_f16x2(raw[x] >> 16);
+              uint32_t b0, b1;
+              e4m3x4_to_f16x2(raw[x], b0, b1);
 #pragma unroll
               for (int t = 0; t < MT; ++t) mma16816h(sc[t][y], q[t][4 * c + x], b0, b1);
             }
@@ -336,27 +355,35 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
           }
         }
       }
-      // scores in log2 units; columns of this lane: keys key + 8 y + 2 j + {0, 1}
-      float vs[2][2];  // log2 of V's scales
+      // Scores in log2 units; columns of this lane: keys key + 8 y + 2 j + {0, 1}. For e4m3 so is the
+      // score with log2 of V's scale added, else it is the score. Lane l turns one of the 32 scales
+      // (16 of K, 16 of V) into what is needed of it, and the others ask for it.
+      float so[MT][2][4];
+      float kf[2][2], vf[2][2];
+      if constexpr (kE4M3) {
+        const uint32_t byte = lds_u8(kt + 2 * C::kTile + lane);
+        const float mine = lane < 16 ? e8m0_to_float(byte) : e8m0_log2(byte);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float f0 = 1.f, f1 = 1.f;
-        if constexpr (kE4M3) {
-          const uint32_t kb = lds_u16(kt + 2 * C::kTile + 8 * y + 2 * j);
-          const uint32_t vb = lds_u16(kt + 2 * C::kTile + 16 + 8 * y + 2 * j);
-          f0 = e8m0_to_float(kb & 255u);
-          f1 = e8m0_to_float(kb >> 8);
-          vs[y][0] = e8m0_log2(vb & 255u);
-          vs[y][1] = e8m0_log2(vb >> 8);
-        }
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            sc[t][y][2 * x] *= kE4M3 ? row_factor[t][x] * f0 : row_factor[t][x];
-            sc[t][y][2 * x + 1] *= kE4M3 ? row_factor[t][x] * f1 : row_factor[t][x];
+          for (int e = 0; e < 2; ++e) {
+            kf[y][e] = __shfl_sync(0xffffffffu, mine, 8 * y + 2 * j + e);
+            vf[y][e] = __shfl_sync(0xffffffffu, mine, 16 + 8 * y + 2 * j + e);
           }
       }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (kE4M3) {
+              sc[t][y][e] *= row_factor[t][e >> 1] * kf[y][e & 1];
+              so[t][y][e] = sc[t][y][e] + vf[y][e & 1];
+            } else {
+              sc[t][y][e] *= a.scale_log2;
+            }
+          }
       if (key + kChunk > lim_min) {  // some row does not see the whole chunk
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -364,7 +391,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (key + 8 * y + 2 * j + (e & 1) >= lim[t][e >> 1]) sc[t][y][e] = -INFINITY;
+              if (key + 8 * y + 2 * j + (e & 1) >= lim[t][e >> 1]) sc[t][y][e] = so[t][y][e] = -INFINITY;
       }
       // raise the running maxima only when some row's grew by more than 2^8: P stays below 2^8
       bool grow = false;
@@ -373,11 +400,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          top[t][x] = fmaxf(fmaxf(sc[t][0][2 * x], sc[t][0][2 * x + 1]), fmaxf(sc[t][1][2 * x], sc[t][1][2 * x + 1]));
+          top[t][x] = fmaxf(max3f(sc[t][0][2 * x], sc[t][0][2 * x + 1], sc[t][1][2 * x]), sc[t][1][2 * x + 1]);
           grow = grow || top[t][x] > m[t][x] + kGrow;
           if constexpr (kE4M3) {
-            topo[t][x] = fmaxf(fmaxf(sc[t][0][2 * x] + vs[0][0], sc[t][0][2 * x + 1] + vs[0][1]),
-                               fmaxf(sc[t][1][2 * x] + vs[1][0], sc[t][1][2 * x + 1] + vs[1][1]));
+            topo[t][x] = fmaxf(max3f(so[t][0][2 * x], so[t][0][2 * x + 1], so[t][1][2 * x]), so[t][1][2 * x + 1]);
             grow = grow || topo[t][x] > mo[t][x] + kGrow;
           }
         }
@@ -415,15 +441,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
           for (int y = 0; y < 2; ++y) {
             const float p0 = fast_exp2(sc[t][y][2 * x] - mb), p1 = fast_exp2(sc[t][y][2 * x + 1] - mb);
             l[t][x] += p0 + p1;
-            if constexpr (kE4M3) {
-              // in f16: off by 2^-11 of itself, or 2^-25 of a row's largest. An unseen key's -inf stays
-              // -inf whatever V's scale is, except NaN
-              const float s0 = sc[t][y][2 * x], s1 = sc[t][y][2 * x + 1];
-              pa[t][2 * y + x] = pack_f16(s0 == -INFINITY ? 0.f : fast_exp2(s0 + vs[y][0] - mob),
-                                          s1 == -INFINITY ? 0.f : fast_exp2(s1 + vs[y][1] - mob));
-            } else {
+            if constexpr (kE4M3)  // in f16: off by 2^-11 of itself, or 2^-25 of the row's largest
+              pa[t][2 * y + x] = pack_f16(fast_exp2(so[t][y][2 * x] - mob), fast_exp2(so[t][y][2 * x + 1] - mob));
+            else
               pa[t][2 * y + x] = pack_bf16(p0, p1);  // off by 2^-8 of itself at most
-            }
           }
         }
       const int vr = (lane & 7) + (lane & 8);  // ldmatrix: keys 0-7, 8-15, then the next piece
@@ -435,9 +456,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const AttnArgs a) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             // bytes: even and odd channel of one key, then of the next; a fragment wants two keys
-            const uint32_t k0 = __byte_perm(f[2 * y], 0, 0x3120), k1 = __byte_perm(f[2 * y + 1], 0, 0x3120);
-            const uint32_t even0 = e4m3x2_to_f16x2(k0), odd0 = e4m3x2_to_f16x2(k0 >> 16);
-            const uint32_t even1 = e4m3x2_to_f16x2(k1), odd1 = e4m3x2_to_f16x2(k1 >> 16);
+            uint32_t even0, odd0, even1, odd1;
+            e4m3x4_to_f16x2(__byte_perm(f[2 * y], 0, 0x3120), even0, odd0);
+            e4m3x4_to_f16x2(__byte_perm(f[2 * y + 1], 0, 0x3120), even1, odd1);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
               mma16816h(acc[t][2 * (c + y)], pa[t], even0, even1);
@@ -537,10 +558,10 @@ fcp_status sm_count(int* n) {
 
 template <int D, bool kE4M3, int MT>
 fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaStream_t s) {
-  using C = FewCfg<D, kE4M3>;
+  using C = FewCfg<D, kE4M3, MT>;
   using P = FewRows<16 * MT>;
   constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * D * 4);
-  const int blocks = std::min(2 * n_sm, kMaxBlocks);
+  const int blocks = std::min(kPerSm<kE4M3, MT> * n_sm, kMaxBlocks);
   set_workspace<P>(a, workspace, D, kMaxBlocks);
   FCP_CUDA_TRY(cudaFuncSetAttribute(few_kernel<D, kE4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
                "paged attention smem attribute");

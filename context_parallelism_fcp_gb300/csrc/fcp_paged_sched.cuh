@@ -17,7 +17,7 @@
 namespace fcp {
 
 constexpr int kGranule = 128;    // keys
-constexpr int kMaxBlocks = 320;       // few rows: two blocks to each of up to 160 SMs
+constexpr int kMaxBlocks = 480;       // few rows: three blocks to each of up to 160 SMs
 constexpr int kMaxChunkBlocks = 160;  // chunks: one
 
 struct SplitGroup;
@@ -183,68 +183,6 @@ struct Walk {
   }
 };
 
-// Shared memory of the line's prefix sums: thread t's sequences begin at prefix[t].
-template <int kThreads>
-struct Line {
-  long long prefix[kThreads + 1];
-  long long warp_sum[kThreads / 32];
-  int per;  // sequences to a thread
-};
-
-// All kThreads threads; ends with a barrier.
-template <class P, int kThreads>
-__device__ __forceinline__ void build_line(const AttnArgs& a, Line<kThreads>& line, bool report) {
-  const int per = (a.c.n_seqs + kThreads - 1) / kThreads;
-  long long mine = 0;
-  for (int i = threadIdx.x * per; i < min((static_cast<int>(threadIdx.x) + 1) * per, a.c.n_seqs); ++i) {
-    const SeqShape s = seq_shape(a.c, i, report);
-    if (s.n > 0) mine += P::head_length(s, a.group, a.causal) * a.c.hkv;
-  }
-  long long x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if ((threadIdx.x & 31) >= o) x += y;
-  }
-  if ((threadIdx.x & 31) == 31) line.warp_sum[threadIdx.x >> 5] = x;
-  __syncthreads();
-  for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) x += line.warp_sum[w];
-  line.prefix[threadIdx.x + 1] = x;
-  if (threadIdx.x == 0) {
-    line.prefix[0] = 0;
-    line.per = per;
-  }
-  __syncthreads();
-}
-
-// Place `w` on the group that holds place f of the line (f < the line's length). False only
-// if the lengths no longer are what the line was built from.
-template <class P, int kThreads>
-__device__ __forceinline__ bool seek(const AttnArgs& a, const Line<kThreads>& line, long long f, Walk<P>& w) {
-  int lo = 0, hi = kThreads;  // prefix[lo] <= f < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (line.prefix[mid] <= f) lo = mid; else hi = mid;
-  }
-  w.i = lo * line.per;
-  w.f0 = line.prefix[lo];
-  long long per_head;
-  while (true) {
-    if (w.i >= a.c.n_seqs) return false;
-    w.s = seq_shape(a.c, w.i, false);
-    per_head = w.s.n > 0 ? P::head_length(w.s, a.group, a.causal) : 0;
-    if (f < w.f0 + per_head * a.c.hkv) break;
-    w.f0 += per_head * a.c.hkv;
-    ++w.i;
-  }
-  w.h = static_cast<int>(quotient(f - w.f0, per_head));
-  w.f0 += w.h * per_head;
-  w.n_units = P::units(w.s, a.group);
-  w.u = P::find(w.s, a.group, a.causal, f, w.f0);
-  w.enter(a);
-  return true;
-}
-
 // The blocks' shares of a line of length `total`: block b < blocks takes [begin(b), begin(b + 1)),
 // which is not empty (blocks is less than the grid where the line is shorter).
 struct Shares {
@@ -263,6 +201,68 @@ struct Shares {
     return b;
   }
 };
+
+// Builds the line and places `first` (shared memory) on the group that holds the beginning of
+// this block's share: each thread adds up its sequences, and the thread that finds the place
+// among its own goes there, with the lengths it already has. All kThreads threads; ends with a
+// barrier. report: record the batch's errors.
+template <int kThreads>
+struct Line {
+  long long warp_sum[kThreads / 32];
+};
+template <class P, int kThreads>
+__device__ __forceinline__ Shares begin_walk(const AttnArgs& a, Line<kThreads>& line, Walk<P>& first, bool report) {
+  const int tid = threadIdx.x, per = (a.c.n_seqs + kThreads - 1) / kThreads;
+  const int i0 = tid * per, i1 = min(i0 + per, a.c.n_seqs);
+  SeqShape s{0, 0, 0};
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) {
+    s = seq_shape(a.c, i, report);
+    if (s.n > 0) mine += P::head_length(s, a.group, a.causal) * a.c.hkv;
+  }
+  long long behind = mine;  // where this thread's sequences end on the line
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, behind, o);
+    if ((tid & 31) >= o) behind += y;
+  }
+  if ((tid & 31) == 31) line.warp_sum[tid >> 5] = behind;
+  if (tid == 0) first.i = a.c.n_seqs;  // no share
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == (tid >> 5)) behind += total;
+    total += line.warp_sum[w];
+  }
+  const Shares sh(total, gridDim.x);
+  const int b = blockIdx.x;
+  if (b < sh.blocks) {
+    const long long f = sh.begin(b);
+    if (behind - mine <= f && f < behind) {
+      Walk<P> w;
+      w.f0 = behind - mine;
+      for (w.i = i0; w.i < i1; ++w.i) {
+        w.s = per == 1 ? s : seq_shape(a.c, w.i, false);
+        if (w.s.n == 0) continue;
+        const long long per_head = per == 1 ? quotient(mine, a.c.hkv) : P::head_length(w.s, a.group, a.causal);
+        if (f >= w.f0 + per_head * a.c.hkv) {
+          w.f0 += per_head * a.c.hkv;
+          continue;
+        }
+        w.h = static_cast<int>(quotient(f - w.f0, per_head));
+        w.f0 += w.h * per_head;
+        w.n_units = P::units(w.s, a.group);
+        w.u = P::find(w.s, a.group, a.causal, f, w.f0);
+        w.enter(a);
+        first = w;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  return sh;
+}
 
 // Where a block's piece [ga, gb) of a group of g granules goes: the output itself when it is the
 // whole group, else the block's slot for a group it continues (0) or begins (1).
