@@ -179,18 +179,25 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
     // chunks of this warp: keys k0 + 16 * (warp + 4 n) below kend
     const int k0 = p.ga * kGranule, kend = min(p.gb * kGranule, p.end);
     const int* table = a.c.table + static_cast<long long>(p.i) * a.c.max_pages;
-    auto page_of = [&](int key) -> int { return key < kend ? __ldg(table + (key >> a.c.page_shift)) : 0; };
-    int issue_key = k0 + kChunk * warp;
-    int issue_page = page_of(issue_key);
-    int issue_stage = 0;
+    // lane l holds the block table's entry for chunk l of a batch of 32, and of the batch behind it
+    const int key0 = k0 + kChunk * warp;
+    auto entries = [&](int batch) -> int {
+      const int key = key0 + (32 * batch + lane) * (kChunk * kWarps);
+      return key < kend ? __ldg(table + (key >> a.c.page_shift)) : -1;
+    };
+    int pages = entries(0), pages_next = entries(1);
+    int n_issued = 0, issue_stage = 0;
     auto issue = [&]() {
-      const int key = issue_key;
+      const int key = key0 + n_issued * (kChunk * kWarps);
       if (key < kend) {
-        bool ok = issue_page >= 0 && issue_page < a.c.n_pages;
+        if ((n_issued & 31) == 0 && n_issued > 0) {
+          pages = pages_next;
+          pages_next = entries((n_issued >> 5) + 1);
+        }
+        const int page = __shfl_sync(0xffffffffu, pages, n_issued & 31);
+        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages);
         if (!ok && lane == 0) atomicCAS(a.c.status, 0, kErrCachePage);
-        const long long r0 = ok ? page_row(a.c, issue_page, p.h) + (key & page_mask) : 0;
-        issue_key += kChunk * kWarps;
-        issue_page = page_of(issue_key);
+        const long long r0 = ok ? page_row(a.c, page, p.h) + (key & page_mask) : 0;
         const uint32_t dst = stages + issue_stage * C::kStage;
         constexpr int kPer = 32 / C::kPieces;  // rows of one instruction
         const int lr = lane / C::kPieces, c = lane % C::kPieces;
@@ -219,6 +226,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
         }
       }
       cp_commit();
+      ++n_issued;
       issue_stage = issue_stage + 1 == C::kStages ? 0 : issue_stage + 1;
     };
 #pragma unroll
@@ -567,8 +575,10 @@ fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaSt
                "paged attention smem attribute");
   few_kernel<D, kE4M3, MT><<<blocks, kFewThreads, kSmem, s>>>(a);
   FCP_CUDA_TRY(cudaGetLastError(), "paged attention launch");
-  const long long rows = static_cast<long long>(std::max(max_new, 1)) * a.group;
-  return launch_merge<P, D>(a, blocks, static_cast<int>(std::min<long long>(rows, 16)), s);
+  // the merge's row slices: a warp a row where groups have few pieces (many groups), else a block
+  const long long rows = std::min<long long>(static_cast<long long>(std::max(max_new, 1)) * a.group, P::kRows);
+  const bool few_pieces = 4ll * a.c.n_seqs * a.c.hkv >= blocks;
+  return launch_merge<P, D>(a, blocks, static_cast<int>(few_pieces ? (rows + kMergeWarps - 1) / kMergeWarps : rows), s);
 }
 
 template <int D>

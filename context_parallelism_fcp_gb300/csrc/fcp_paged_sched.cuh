@@ -57,23 +57,19 @@ struct FewRows {
   static __device__ __forceinline__ int units(const SeqShape& s, int group) {
     return static_cast<int>((static_cast<long long>(s.n) * group + kRows - 1) / kRows);
   }
-  static __device__ __forceinline__ int end(const SeqShape& s, int group, int u, int causal) {
-    return key_end(s, static_cast<int>(quotient((u + 1ll) * kRows - 1, group)), causal);
-  }
-  static __device__ __forceinline__ long long head_length(const SeqShape& s, int group, int causal) {
-    long long sum = 0;
-    const int n = units(s, group);
-    for (int u = 0; u < n; ++u) sum += kOverhead + granules_of(end(s, group, u, causal));
-    return sum;
+  // All of the sequence's keys: the mask leaves the last few out where that matters.
+  static __device__ __forceinline__ int end(const SeqShape& s, int, int, int) { return s.len; }
+  static __device__ __forceinline__ long long head_length(const SeqShape& s, int group, int) {
+    return static_cast<long long>(units(s, group)) * (kOverhead + granules_of(s.len));
   }
   // The unit of a head that holds place f >= f0 of the line, where the head begins at f0; f0
   // becomes where the unit begins.
-  static __device__ __forceinline__ int find(const SeqShape& s, int group, int causal, long long f, long long& f0) {
-    for (int u = 0;; ++u) {
-      const long long next = f0 + kOverhead + granules_of(end(s, group, u, causal));
-      if (f < next) return u;
-      f0 = next;
-    }
+  static __device__ __forceinline__ int find(const SeqShape& s, int, int, long long f, long long& f0) {
+    const int len = kOverhead + granules_of(s.len);
+    if (f < f0 + len) return 0;
+    const int u = static_cast<int>(quotient(f - f0, len));
+    f0 += static_cast<long long>(u) * len;
+    return u;
   }
   // (token, head of the group) of row r of unit u; false behind the last
   static __device__ __forceinline__ bool row(const SeqShape& s, int group, int u, int r, int& tok, int& head) {
