@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
   constexpr int kPasses = kMoveTokens / kPass;     // passes to a head
   __shared__ TokenPlace place[kMoveTokens];
   __shared__ int coarse[kCoarse];
+  let_next_start();
+  wait_for_previous();
   const int t0 = blockIdx.x * kMoveTokens;
   find_places(p, t0, place, coarse);
   const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, p.hkv);
@@ -225,12 +227,8 @@ fcp_status launch_move(const PagedArgs& p, int dtype, void* k, void* v, cudaStre
   if (grid.y > 65535u) return FCP_ERR_UNSUPPORTED;
   uint4* pk = static_cast<uint4*>(k);
   uint4* pv = static_cast<uint4*>(v);
-  if (dtype == FCP_CACHE_E4M3)
-    move_kernel<D, true, kRead><<<grid, kMoveThreads, 0, s>>>(p, pk, pv, heads);
-  else
-    move_kernel<D, false, kRead><<<grid, kMoveThreads, 0, s>>>(p, pk, pv, heads);
-  FCP_CUDA_TRY(cudaGetLastError(), kRead ? "cache read launch" : "cache write launch");
-  return FCP_OK;
+  return launch_overlapped(dtype == FCP_CACHE_E4M3 ? move_kernel<D, true, kRead> : move_kernel<D, false, kRead>, grid,
+                           kMoveThreads, 0, s, kRead ? "cache read launch" : "cache write launch", p, pk, pv, heads);
 }
 
 template <bool kRead>

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <utility>
 
 #include "fcp_cuda_util.h"
 
@@ -40,6 +41,29 @@ struct PagedArgs {
 };
 
 fcp_status paged_args(const fcp_cache* cache, const fcp_cache_batch* batch, PagedArgs* out);
+
+// The cache's kernels are launched so that they may start while the kernel before them in the
+// stream still runs, to hide the launch: each waits for that one's end before it touches
+// memory, and lets the next one start in the same way.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... Params, class... Args>
+inline fcp_status launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                    const char* where, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...), where);
+  return FCP_OK;
+}
 
 // The rows [a, a + n) of sequence i and its cached length; n = 0 (with the error recorded by
 // the thread that passes report) where they do not fit the batch.

@@ -133,9 +133,10 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x;
+  let_next_start();
+  wait_for_previous();
   if (threadIdx.x == 0) a.split[b].last = b;
   const Shares sh = begin_walk<P, kThreads>(a, line, walk, b == 0);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (b >= sh.blocks) return;
   // 128-byte-swizzled tiles need a 1024-byte aligned base; report, never fault
   if ((sb & 1023u) != 0) {
@@ -724,8 +725,10 @@ fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s)
   set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
   FCP_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes),
                "paged chunk smem attribute");
-  chunk_kernel<D, kE4M3><<<blocks, kThreads<kE4M3>, C::kSmemBytes, s>>>(mq, mq16, mk, mv, a);
-  FCP_CUDA_TRY(cudaGetLastError(), "paged chunk launch");
+  if (const fcp_status st = launch_overlapped(chunk_kernel<D, kE4M3>, dim3(blocks), kThreads<kE4M3>, C::kSmemBytes, s,
+                                              "paged chunk launch", mq, mq16, mk, mv, a);
+      st != FCP_OK)
+    return st;
   return launch_merge<ChunkRows, D>(a, blocks, 32, s);
 }
 

@@ -136,9 +136,10 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = lane >> 2, j = lane & 3;  // this lane's fragment rows (row, row + 8) and columns
   const int b = blockIdx.x;
+  let_next_start();
+  wait_for_previous();
   if (threadIdx.x == 0) a.split[b].last = b;
   const Shares sh = begin_walk<P, kFewThreads>(a, line, walk, b == 0);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (b >= sh.blocks) return;
   const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
 
@@ -573,8 +574,10 @@ fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaSt
   set_workspace<P>(a, workspace, D, kMaxBlocks);
   FCP_CUDA_TRY(cudaFuncSetAttribute(few_kernel<D, kE4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
                "paged attention smem attribute");
-  few_kernel<D, kE4M3, MT><<<blocks, kFewThreads, kSmem, s>>>(a);
-  FCP_CUDA_TRY(cudaGetLastError(), "paged attention launch");
+  if (const fcp_status st = launch_overlapped(few_kernel<D, kE4M3, MT>, dim3(blocks), kFewThreads, kSmem, s,
+                                              "paged attention launch", a);
+      st != FCP_OK)
+    return st;
   // the merge's row slices: a warp a row where groups have few pieces (many groups), else a block
   const long long rows = std::min<long long>(static_cast<long long>(std::max(max_new, 1)) * a.group, P::kRows);
   const bool few_pieces = 4ll * a.c.n_seqs * a.c.hkv >= blocks;

@@ -276,8 +276,7 @@ static_assert(sizeof(SplitGroup) == 32, "two 16-byte loads");
 
 // Joins the pieces of the groups that blocks split: with M the largest of a row's maxima,
 // O = sum 2^(m - M) o / sum 2^(m - M) l, over the pieces in a fixed order. grid (blocks, row
-// slices); a warp takes a row of up to 8 pieces, the whole block one of more. Launched
-// so that it may start while the attention still runs: it waits for it in the kernel.
+// slices); a warp takes a row of up to 8 pieces, the whole block one of more.
 constexpr int kMergeWarps = 4;
 template <class P, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const AttnArgs a) {
@@ -287,7 +286,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Att
   __shared__ float2 warp_ml[kMergeWarps];
   __shared__ float4 part[kAtOnce][kPieceLanes];
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  wait_for_previous();
   const SplitGroup g = a.split[b];
   const int count = g.last - b + 1;
   if (count <= 1) return;
@@ -413,17 +413,7 @@ inline void set_workspace(AttnArgs& a, void* workspace, int d, int blocks) {
 
 template <class P, int D>
 inline fcp_status launch_merge(const AttnArgs& a, int blocks, int slices, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, slices);
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<P, D>, a), "paged merge launch");
-  return FCP_OK;
+  return launch_overlapped(paged_merge_kernel<P, D>, dim3(blocks, slices), 32 * kMergeWarps, 0, s, "paged merge launch", a);
 }
 
 fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int n_sm, cudaStream_t s);
