@@ -10,6 +10,7 @@
 // Both directions are bound by HBM: 2 * T * Hkv rows in and out, nothing reused. One warp
 // moves whole rows, D / 8 lanes to a row, 16 bytes of bf16 to a lane.
 #include <algorithm>
+#include <type_traits>
 
 #include "fcp_paged.h"
 
@@ -112,19 +113,13 @@ __device__ __forceinline__ void find_places(const PagedArgs& p, int t0, TokenPla
 // Quantise the 8 channels of this lane (of a row shared by LPR lanes): 8 codes and the row's scale byte.
 template <int LPR>
 __device__ __forceinline__ uint2 quantise(const uint4 x, uint32_t& scale_byte) {
-  float v[8];
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // the largest magnitude as bf16 bits, two channels at a time: non-finite values order above
+  // every finite one
+  uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-  // the largest magnitude as bf16 bits: non-finite values order above every finite one
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int o = LPR / 2; o > 0; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+  const uint32_t top = max(two & 0xffffu, two >> 16);
   if (top >= 0x7f80u) {
     scale_byte = 255;
     return make_uint2(0u, 0u);
@@ -134,35 +129,17 @@ __device__ __forceinline__ uint2 quantise(const uint4 x, uint32_t& scale_byte) {
   const int k = top == 0 ? 0 : max(e - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0), -126);
   scale_byte = static_cast<uint32_t>(k + 127);
   const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-  // 256 * 2^120 would be the one product that bf16 cannot hold
-  const float most = k == 120 ? 240.f : 448.f;
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float y0 = fminf(fmaxf(v[2 * i] * inv, -most), most), y1 = fminf(fmaxf(v[2 * i + 1] * inv, -most), most);
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+    float2 y = dev::fmul2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u), inv, inv);
+    if (k == 120) {  // 256 * 2^120 would be the one product that bf16 cannot hold
+      y.x = fminf(fmaxf(y.x, -240.f), 240.f);
+      y.y = fminf(fmaxf(y.y, -240.f), 240.f);
+    }
+    c[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
-
-__device__ __forceinline__ uint4 dequantise(const uint2 c, float scale) {
-  // code values are exact in bf16; their product with a power of two is rounded at most where
-  // it leaves bf16's normal range
-  uint32_t r[4];
-  const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t a = e4m3x2_to_bf16x2(__byte_perm(w[i], 0, 0x1404));  // codes 0, 1
-    const uint32_t b = e4m3x2_to_bf16x2(__byte_perm(w[i], 0, 0x3424));  // codes 2, 3
-    const uint32_t p[2] = {a, b};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const __nv_bfloat162 y =
-          __floats2bfloat162_rn(__uint_as_float(p[j] << 16) * scale, __uint_as_float(p[j] & 0xffff0000u) * scale);
-      r[2 * i + j] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // grid (ceil(T / 32), ceil(Hkv / heads per block), 2: K or V)
@@ -179,44 +156,76 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
   const int t0 = blockIdx.x * kMoveTokens;
   find_places(p, t0, place, coarse);
   const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, p.hkv);
-  uint4* rows = blockIdx.z ? v : k;
-  uint8_t* pages = blockIdx.z ? p.v_pages : p.k_pages;
-  uint8_t* scales = blockIdx.z ? p.v_scales : p.k_scales;
+  uint4* __restrict__ rows = blockIdx.z ? v : k;
+  uint8_t* __restrict__ pages = blockIdx.z ? p.v_pages : p.k_pages;
+  uint8_t* __restrict__ scales = blockIdx.z ? p.v_scales : p.k_scales;
   const int sub = threadIdx.x / LPR, l = threadIdx.x % LPR;
   TokenPlace at[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) at[i] = place[i * kPass + sub];
-#pragma unroll 2
-  for (int h = h0; h < h1; ++h) {
+  // Rows of one head after another: both sides step by a constant. A thread's loads of kHeads heads
+  // go out together, then they are converted and stored.
+  constexpr int kHeads = 4 / kPasses;
+  const long long row_step = 1ll << p.page_shift, my_step = static_cast<long long>(p.total_new) * LPR;
+  long long row[kPasses], mine[kPasses];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int t = t0 + i * kPass + sub;
-      const bool on = at[i].page >= 0;
-      const long long row = on ? page_row(p, at[i].page, h) + at[i].off : 0;
-      const long long mine = (static_cast<long long>(h) * p.total_new + t) * LPR + l;
-      if constexpr (!kE4M3) {
-        uint4* cell = reinterpret_cast<uint4*>(pages) + row * LPR + l;
-        if (on) {
-          if constexpr (kRead) rows[mine] = *cell; else *cell = rows[mine];
-        }
-      } else {
-        uint2* cell = reinterpret_cast<uint2*>(pages) + row * LPR + l;
-        if constexpr (kRead) {
-          if (on) rows[mine] = dequantise(*cell, e8m0_to_float(scales[row]));
+  for (int i = 0; i < kPasses; ++i) {
+    row[i] = at[i].page >= 0 ? page_row(p, at[i].page, h0) + at[i].off : 0;
+    mine[i] = (static_cast<long long>(h0) * p.total_new + t0 + i * kPass + sub) * LPR + l;
+  }
+  using Cell = typename std::conditional<kE4M3, uint2, uint4>::type;  // 8 channels in a page
+  Cell* cells = reinterpret_cast<Cell*>(pages);
+  for (int h = h0; h < h1; h += kHeads) {
+    uint4 x[kHeads][kPasses];
+    uint32_t byte[kHeads][kPasses];
+#pragma unroll
+    for (int y = 0; y < kHeads; ++y)
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        x[y][i] = make_uint4(0u, 0u, 0u, 0u);
+        byte[y][i] = 127u;
+        if (at[i].page < 0 || h + y >= h1) continue;
+        const long long r = row[i] + y * row_step;
+        if constexpr (!kRead) {
+          x[y][i] = __ldcs(rows + mine[i] + y * my_step);
+        } else if constexpr (kE4M3) {
+          const uint2 c = cells[r * LPR + l];
+          x[y][i].x = c.x;
+          x[y][i].y = c.y;
+          byte[y][i] = scales[r];
         } else {
-          const uint4 x = on ? rows[mine] : make_uint4(0u, 0u, 0u, 0u);
-          uint32_t byte;
-          const uint2 codes = quantise<LPR>(x, byte);
-          if (on) {
-            *cell = codes;
-            if (l == 0) scales[row] = static_cast<uint8_t>(byte);
-          }
+          x[y][i] = cells[r * LPR + l];
         }
       }
+#pragma unroll
+    for (int y = 0; y < kHeads; ++y)
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const bool on = at[i].page >= 0 && h + y < h1;
+        const long long r = row[i] + y * row_step;
+        if constexpr (kRead) {
+          if constexpr (kE4M3) x[y][i] = scaled8(make_uint2(x[y][i].x, x[y][i].y), e8m0_to_float(byte[y][i]));
+          if (on) __stcs(rows + mine[i] + y * my_step, x[y][i]);
+        } else if constexpr (kE4M3) {
+          const uint2 codes = quantise<LPR>(x[y][i], byte[y][i]);
+          if (on) {
+            cells[r * LPR + l] = codes;
+            if (l == 0) scales[r] = static_cast<uint8_t>(byte[y][i]);
+          }
+        } else if (on) {
+          cells[r * LPR + l] = x[y][i];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      row[i] += kHeads * row_step;
+      mine[i] += kHeads * my_step;
     }
   }
 }
 
+// The launch overlaps the kernel before it in the stream where there is enough work that this
+// is worth the call's extra microsecond and a half on the host.
 template <int D, bool kRead>
 fcp_status launch_move(const PagedArgs& p, int dtype, void* k, void* v, cudaStream_t s) {
   const unsigned bx = static_cast<unsigned>((p.total_new + kMoveTokens - 1) / kMoveTokens);
@@ -227,8 +236,12 @@ fcp_status launch_move(const PagedArgs& p, int dtype, void* k, void* v, cudaStre
   if (grid.y > 65535u) return FCP_ERR_UNSUPPORTED;
   uint4* pk = static_cast<uint4*>(k);
   uint4* pv = static_cast<uint4*>(v);
-  return launch_overlapped(dtype == FCP_CACHE_E4M3 ? move_kernel<D, true, kRead> : move_kernel<D, false, kRead>, grid,
-                           kMoveThreads, 0, s, kRead ? "cache read launch" : "cache write launch", p, pk, pv, heads);
+  auto* kernel = dtype == FCP_CACHE_E4M3 ? move_kernel<D, true, kRead> : move_kernel<D, false, kRead>;
+  const char* where = kRead ? "cache read launch" : "cache write launch";
+  if (2ll * bx * grid.y >= 1216) return launch_overlapped(kernel, grid, kMoveThreads, 0, s, where, p, pk, pv, heads);
+  kernel<<<grid, kMoveThreads, 0, s>>>(p, pk, pv, heads);
+  FCP_CUDA_TRY(cudaGetLastError(), where);
+  return FCP_OK;
 }
 
 template <bool kRead>

@@ -8,6 +8,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -15,6 +16,7 @@
 #include <utility>
 
 #include "fcp_cuda_util.h"
+#include "fcp_sm100.cuh"
 
 namespace fcp {
 
@@ -94,15 +96,26 @@ __device__ __forceinline__ float e8m0_log2(uint32_t b) {
   return b == 255u ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(b) - 127);
 }
 
-// Two e4m3 codes in bits 8-15 and 24-31 as bf16x2. The code's exponent and mantissa sit in
-// bf16's fields with its bias 7 instead of 127, so one exact product with 2^120 gives the
-// value; code subnormals are bf16 subnormals before it. (Codes 0x7f and 0xff, which a written
-// cache never holds, read as +-480.)
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t x) {
-  const uint32_t r = (x & 0x80008000u) | ((x & 0x7f007f00u) >> 4);
-  const uint32_t f = 0x7b807b80u;  // 2^120
-  __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&f));
-  return *reinterpret_cast<uint32_t*>(&y);
+// Four e4m3 codes as two f16x2, exactly (the NaN codes as NaN).
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
+
+// 8 codes times their row's scale as 8 bf16 channels: the product with a power of two is exact in
+// float32, and exact in bf16 while it is a normal number there.
+__device__ __forceinline__ uint4 scaled8(const uint2 x, float scale) {
+  uint32_t h[4], r[4];
+  e4m3x4_to_f16x2(x.x, h[0], h[1]);
+  e4m3x4_to_f16x2(x.y, h[2], h[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    const float2 y = dev::fmul2(v.x, v.y, scale, scale);
+    r[i] = dev::pack_bf16(y.x, y.y);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 }  // namespace fcp

@@ -23,8 +23,6 @@
 // elements that it transposes are channel pairs, whose low and high bytes become the fragments
 // of two 8-channel tiles. 16-byte pieces of a row are XOR-swizzled so that neither reading has
 // bank conflicts.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 #include <cmath>
 
@@ -106,12 +104,6 @@ __device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4],
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Four e4m3 codes as two f16x2, exactly (the NaN codes as NaN).
-__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(four));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
