@@ -38,7 +38,7 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr int kQBox = 16;                   // tokens of a TMA load of Q for tiles of several heads
 // Registers a thread with the loader warps: the launch gives 128, and the softmax warps take
 // what the others leave (they hold a row of 128 scores).
-constexpr int kRegsSoftmax = 176, kRegsOther = 80;
+constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * 128, "the split fits the launch's registers");
 
 enum : int {
@@ -85,30 +85,24 @@ struct Cfg {
   static constexpr uint32_t kIdescPV = idesc_bf16(kTileM, D, false, true);
 };
 
-// 8 codes and their row's scale byte as 8 bf16 channels, code * 2^(byte - 127), with the same
-// results as scaled8 (but for the codes 0x7f and 0xff, which a written cache never holds: +-480
-// here). The code's bits in bf16's fields are code * 2^-120, and 2^120 is taken into the scale
-// where bf16 holds the product of both; larger scales take two exact products. With scaled8's
-// conversions 2048 tokens over 32768 keys took 2154 us instead of 1891.
-__device__ __forceinline__ uint4 shifted8(const uint2 x, uint32_t byte) {
-  uint32_t r[4];
+// 8 codes times 2^-120 as bf16: a code's exponent and mantissa moved to bf16's fields, four codes
+// at a time (the high bytes, the low bytes, then interleaved).
+__device__ __forceinline__ void code_bits(const uint2 x, uint32_t (&r)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i ? x.y : x.x;
+    const uint32_t hi = (w & 0x80808080u) | ((w >> 4) & 0x07070707u), lo = (w & 0x0f0f0f0fu) * 16u;
+    r[2 * i] = __byte_perm(lo, hi, 0x5140);
+    r[2 * i + 1] = __byte_perm(lo, hi, 0x7362);
+  }
+}
+__device__ __forceinline__ void times(uint32_t (&r)[4], uint32_t f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t y = __byte_perm(i < 2 ? x.x : x.y, 0, i & 1 ? 0x3424 : 0x1404);
-    r[i] = (y & 0x80008000u) | ((y & 0x7f007f00u) >> 4);
+    const __nv_bfloat162 y =
+        __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]), *reinterpret_cast<const __nv_bfloat162*>(&f));
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  auto times = [&](uint32_t f) {
-    f |= f << 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 y =
-          __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]), *reinterpret_cast<const __nv_bfloat162*>(&f));
-      r[i] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-  };
-  times((min(byte, 134u) + 120u) << 7);
-  if (byte > 134u) times(byte == 255u ? 0x7fc0u : (byte - 7u) << 7);
-  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <int D, bool kE4M3>
@@ -233,31 +227,31 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           const int key0 = first_key(g);
           return g < g_end && key0 < t.len ? __ldg(table + (key0 >> a.c.page_shift)) : -1;
         };
-        uint2 raw[4][C::kPanels];
-        uint32_t byte[4];
+        uint2 raw[4][C::kPanels];  // of rows that are not there: anything
         const uint8_t* src = nullptr;
-        const uint8_t* sc = nullptr;
-        int held = 0;  // rows r0 + 4 x with 4 x below it are there; the others become zeros
+        int held = 0;        // rows r0 + 4 x with 4 x below it are there
+        uint32_t byte = 0;   // lane l: scale of row l % 16; 256: not there
         auto aim = [&](int g, int page) {
           const int key0 = first_key(g);
           const bool is_v = (g & 8) != 0, in = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages);
           if (!in && g < g_end && key0 < t.len) atomicCAS(err, 0, kErrCachePage);
-          const long long row = (in ? page_row(a.c, page, t.h) + (key0 & page_mask) : 0) + r0;
-          src = (is_v ? a.c.v_pages : a.c.k_pages) + row * D + c * 8;
-          sc = (is_v ? a.c.v_scales : a.c.k_scales) + row;
+          const long long row = in ? page_row(a.c, page, t.h) + (key0 & page_mask) : 0;
+          src = (is_v ? a.c.v_pages : a.c.k_pages) + (row + r0) * D + c * 8;
           held = in ? t.len - key0 - r0 : 0;
+          byte = 256u;
+          if (in && key0 + (lane & 15) < t.len) byte = __ldg((is_v ? a.c.v_scales : a.c.k_scales) + row + (lane & 15));
         };
         auto load = [&](int x) {
-#pragma unroll
-          for (int p = 0; p < C::kPanels; ++p) raw[x][p] = make_uint2(0u, 0u);
-          byte[x] = 127u;
           if (4 * x < held) {
 #pragma unroll
             for (int p = 0; p < C::kPanels; ++p)
               raw[x][p] = __ldg(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
-            byte[x] = __ldg(sc + 4 * x);
           }
         };
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int p = 0; p < C::kPanels; ++p) raw[x][p] = make_uint2(0u, 0u);
         aim(g1, lookup(g1));
 #pragma unroll
         for (int x = 0; x < 4; ++x) load(x);
@@ -265,19 +259,52 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         while (g1 < g_end) {
           const int J = g1 >> 4, s = J & 1;  // the block's key tile
           const bool is_v = (g1 & 8) != 0;
-          aim(g2, page2);
-          const int g3 = g2 + step();
-          page2 = lookup(g3);
           ok = mbar_wait(bar((is_v ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t* dst = smem + (is_v ? C::kV : C::kK) + s * C::kTileBytes + (16 * (g1 & 7) + r0) * 128;
+          // Piece p of row r0 + 4 x, swizzled by the row's last bits.
+          auto piece = [&](int x, int p) -> uint4* {
+            return reinterpret_cast<uint4*>(dst + p * kPanelBytes + 4 * x * 128 + ((c ^ ((r0 + 4 * x) & 7)) << 4));
+          };
+          // A row's factor is 2^(byte - 127) * 2^120, in bf16 only up to a scale of 2^7. A group with a
+          // larger one, or NaN, is done here, in two exact products; the code below then stores nothing.
+          // (A branch anywhere below would wait for the next group's loads: 2066 us instead of 1724 for
+          // 2048 tokens over 32768 keys.)
+          const uint32_t mine = byte;
+          const bool large = __any_sync(0xffffffffu, mine - 135u <= 255u - 135u);
+          if (large) {
+            const uint32_t f2 = mine <= 134u || mine == 256u ? 0x3f803f80u : (mine == 255u ? 0x7fc0u : (mine - 7u) << 7) * 0x10001u;
+            const uint32_t f1 = mine == 256u ? 0u : ((min(mine, 134u) + 120u) << 7) * 0x10001u;
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t a1 = __shfl_sync(0xffffffffu, f1, r0 + 4 * x), a2 = __shfl_sync(0xffffffffu, f2, r0 + 4 * x);
+#pragma unroll 1
+              for (int p = 0; p < C::kPanels; ++p) {
+                uint2 codes = make_uint2(0u, 0u);
+                if (4 * x < held) codes = __ldg(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
+                uint32_t r[4];
+                code_bits(codes, r);
+                times(r, a1);
+                times(r, a2);
+                *piece(x, p) = make_uint4(r[0], r[1], r[2], r[3]);
+              }
+            }
+          }
+          const uint32_t f1 = mine == 256u ? 0u : ((mine + 120u) << 7) * 0x10001u;  // rows that are not there: zeros
+          aim(g2, page2);
+          const int g3 = g2 + step();
+          page2 = lookup(g3);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            uint8_t* to = dst + 4 * x * 128 + ((c ^ ((r0 + 4 * x) & 7)) << 4);  // swizzled by the row's last bits
+            const uint32_t f = __shfl_sync(0xffffffffu, f1, r0 + 4 * x);
 #pragma unroll
-            for (int p = 0; p < C::kPanels; ++p)
-              *reinterpret_cast<uint4*>(to + p * kPanelBytes) = shifted8(raw[x][p], byte[x]);
+            for (int p = 0; p < C::kPanels; ++p) {
+              uint32_t r[4];
+              code_bits(raw[x][p], r);
+              times(r, f);
+              if (!large) *piece(x, p) = make_uint4(r[0], r[1], r[2], r[3]);
+            }
             load(x);  // of the next group
           }
           fence_proxy_async_smem();
@@ -731,7 +758,7 @@ fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s)
                                               "paged chunk launch", mq, mq16, mk, mv, a);
       st != FCP_OK)
     return st;
-  return launch_merge<ChunkRows, D>(a, blocks, 32, s);
+  return launch_merge<ChunkRows, D>(a, blocks, 8, s);
 }
 
 }  // namespace

@@ -570,10 +570,11 @@ fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaSt
                                               "paged attention launch", a);
       st != FCP_OK)
     return st;
-  // the merge's row slices: a warp a row where groups have few pieces (many groups), else a block
+  // the merge's row slices: a warp takes four rows where groups have few pieces (many groups), else a
+  // block takes one
   const long long rows = std::min<long long>(static_cast<long long>(std::max(max_new, 1)) * a.group, P::kRows);
   const bool few_pieces = 4ll * a.c.n_seqs * a.c.hkv >= blocks;
-  return launch_merge<P, D>(a, blocks, static_cast<int>(few_pieces ? (rows + kMergeWarps - 1) / kMergeWarps : rows), s);
+  return launch_merge<P, D>(a, blocks, static_cast<int>(few_pieces ? (rows + 4 * kMergeWarps - 1) / (4 * kMergeWarps) : rows), s);
 }
 
 template <int D>
@@ -617,6 +618,7 @@ extern "C" fcp_status fcp_paged_attn(const fcp_cache* cache, const fcp_cache_bat
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
+  a.small = (static_cast<long long>(a.c.max_pages) << a.c.page_shift) * a.c.n_seqs * cache->hkv <= 1 << 18;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cache->head_dim == 128 ? launch_attn<128>(a, cache->dtype, hq, batch->max_new, workspace, s)
                                 : launch_attn<64>(a, cache->dtype, hq, batch->max_new, workspace, s);
