@@ -758,7 +758,7 @@ fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s)
                                               "paged chunk launch", mq, mq16, mk, mv, a);
       st != FCP_OK)
     return st;
-  return launch_merge<ChunkRows, D>(a, blocks, 8, s);
+  return launch_merge<ChunkRows, D>(a, blocks, 32, s);
 }
 
 }  // namespace

@@ -570,11 +570,12 @@ fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaSt
                                               "paged attention launch", a);
       st != FCP_OK)
     return st;
-  // the merge's row slices: a warp takes four rows where groups have few pieces (many groups), else a
+  // the merge's row slices: a warp takes two rows where groups have few pieces (many groups), else a
   // block takes one
   const long long rows = std::min<long long>(static_cast<long long>(std::max(max_new, 1)) * a.group, P::kRows);
-  const bool few_pieces = 4ll * a.c.n_seqs * a.c.hkv >= blocks;
-  return launch_merge<P, D>(a, blocks, static_cast<int>(few_pieces ? (rows + 4 * kMergeWarps - 1) / (4 * kMergeWarps) : rows), s);
+  const bool few_pieces = static_cast<long long>(kWarpPieces) * a.c.n_seqs * a.c.hkv >= blocks;
+  return launch_merge<P, D>(
+      a, blocks, static_cast<int>(few_pieces ? (rows + 2 * kMergeWarps - 1) / (2 * kMergeWarps) : rows), s);
 }
 
 template <int D>

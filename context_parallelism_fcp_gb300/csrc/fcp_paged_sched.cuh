@@ -280,8 +280,9 @@ static_assert(sizeof(SplitGroup) == 32, "two 16-byte loads");
 
 // Joins the pieces of the groups that blocks split: with M the largest of a row's maxima,
 // O = sum 2^(m - M) o / sum 2^(m - M) l, over the pieces in a fixed order. grid (blocks, row
-// slices); a warp takes rows of up to 8 pieces, the whole block one of more.
+// slices); a warp takes rows of up to kWarpPieces pieces, the whole block a row of more.
 constexpr int kMergeWarps = 4;
+constexpr int kWarpPieces = 32;
 template <class P, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const AttnArgs a) {
   constexpr int kPieceLanes = D / 4;                             // lanes of a piece, 4 channels each
@@ -296,16 +297,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Att
   const int count = g.last - b + 1;
   if (count <= 1) return;
   const SeqShape s{g.a, g.n, 0};
-  if (count <= 8) {
-    // few pieces: a warp takes four rows on its own, their loads side by side, one piece after another
+  if (count <= kWarpPieces) {
+    // a warp takes two rows on its own, the loads of four pieces of both side by side
     constexpr int kEach = D / 32;  // channels of a lane
-    constexpr int kAtOnceRows = 4;
+    constexpr int kR = 2, kX = 4;
     const int stride = gridDim.y * kMergeWarps;
-    for (int r0 = blockIdx.y * kMergeWarps + warp; r0 < P::kRows; r0 += kAtOnceRows * stride) {
-      float m[kAtOnceRows], l[kAtOnceRows], acc[kAtOnceRows][kEach];
-      long long out[kAtOnceRows];  // output row; -1: none
+    for (int r0 = blockIdx.y * kMergeWarps + warp; r0 < P::kRows; r0 += kR * stride) {
+      float m[kR], l[kR], acc[kR][kEach];
+      long long out[kR];  // output row; -1: none
 #pragma unroll
-      for (int k = 0; k < kAtOnceRows; ++k) {
+      for (int k = 0; k < kR; ++k) {
         int tok, head;
         const int r = r0 + k * stride;
         const bool on = r < P::kRows && P::row(s, a.group, g.u, r, tok, head);
@@ -315,32 +316,46 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Att
 #pragma unroll
         for (int e = 0; e < kEach; ++e) acc[k][e] = 0.f;
       }
-      for (int x = 0; x < count; ++x) {
-        const long long at0 = static_cast<long long>(2 * (b + x) + (x == 0)) * P::kRows + r0;
-        float2 ml[kAtOnceRows];
-        float y[kAtOnceRows][kEach];
+      for (int x0 = 0; x0 < count; x0 += kX) {
+        float2 ml[kX][kR];
+        float y[kX][kR][kEach];
 #pragma unroll
-        for (int k = 0; k < kAtOnceRows; ++k)
-          if (out[k] >= 0) {
-            const long long at = at0 + k * stride;
-            ml[k] = a.part_ml[at];
+        for (int q = 0; q < kX; ++q)
 #pragma unroll
-            for (int e = 0; e < kEach; e += 2)
-              *reinterpret_cast<float2*>(&y[k][e]) = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * kEach + e);
+          for (int k = 0; k < kR; ++k) {
+            ml[q][k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) y[q][k][e] = 0.f;
+            if (x0 + q < count && out[k] >= 0) {
+              const long long at = static_cast<long long>(2 * (b + x0 + q) + (x0 + q == 0)) * P::kRows + r0 + k * stride;
+              ml[q][k] = a.part_ml[at];
+#pragma unroll
+              for (int e = 0; e < kEach; e += 2)
+                *reinterpret_cast<float2*>(&y[q][k][e]) = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * kEach + e);
+            }
           }
 #pragma unroll
-        for (int k = 0; k < kAtOnceRows; ++k)
-          if (out[k] >= 0) {
-            const float top = fmaxf(m[k], ml[k].x), mb = top == -INFINITY ? 0.f : top;
-            const float f0 = exp2f(m[k] - mb), f1 = exp2f(ml[k].x - mb);
-            m[k] = top;
-            l[k] = l[k] * f0 + ml[k].y * f1;
+        for (int k = 0; k < kR; ++k) {
+          float top = m[k];
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) acc[k][e] = acc[k][e] * f0 + y[k][e] * f1;
+          for (int q = 0; q < kX; ++q) top = fmaxf(top, ml[q][k].x);
+          const float mb = top == -INFINITY ? 0.f : top;
+          const float f0 = exp2f(m[k] - mb);
+          m[k] = top;
+          l[k] *= f0;
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) acc[k][e] *= f0;
+#pragma unroll
+          for (int q = 0; q < kX; ++q) {
+            const float f = exp2f(ml[q][k].x - mb);
+            l[k] = fmaf(f, ml[q][k].y, l[k]);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) acc[k][e] = fmaf(f, y[q][k][e], acc[k][e]);
           }
+        }
       }
 #pragma unroll
-      for (int k = 0; k < kAtOnceRows; ++k)
+      for (int k = 0; k < kR; ++k)
         if (out[k] >= 0) {
           const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
 #pragma unroll
