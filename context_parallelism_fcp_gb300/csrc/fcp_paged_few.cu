@@ -1,28 +1,33 @@
 // Attention of few new rows for each cached sequence (single tokens, drafted tokens) over a
 // paged cache, and the entry point of the attention over a paged cache.
 //
-// For a KV head the rows are (new token, query head) pairs, 16 or 32 to a unit, so every query
+// For a KV head the rows are (new token, query head) pairs, 8, 16 or 32 to a unit, so every query
 // head of the group and every drafted token shares one pass over the keys: HBM traffic is the
 // cache once, at 4 * rows flops for every 2 bytes read: far below what the tensor cores need,
-// so the kernel is bound by HBM and its business is to keep enough bytes in flight. Each warp
-// takes every fourth 16-key chunk of its block's piece and runs its own pipeline of cp.async
-// stages (a chunk lies in one page because pages are multiples of 16 keys) and its own running
-// softmax; warps meet only at the end of a piece. S = Q K^T and O += P V are m16n8k16 products
-// with float32 sums: with 16 rows tcgen05's 128-row tile would be seven eighths empty, and
-// both units are far faster than the loads.
+// so the kernel is bound by HBM and its business is to keep enough bytes in flight, and for an
+// e4m3 cache to spend few enough instructions on a byte. Each warp takes every fourth 16-key
+// chunk of its block's piece and runs its own pipeline of cp.async stages (a chunk lies in one
+// page because pages are multiples of 16 keys) and its own running softmax; warps meet only at
+// the end of a piece.
+//
+// The products are S^T = K Q^T and O^T += V^T P^T, m16n8k16 with float32 sums: keys and channels
+// take the 16, rows the 8, so 8 rows (one token of 8 heads) fill the instruction, and K's and
+// V's fragments serve all of a unit's rows. (With rows as the 16, half empty, 128 e4m3 sequences
+// of up to 8192 keys took 171 us; tcgen05's 128 rows would be fifteen sixteenths empty.) A lane
+// has two keys and two rows of S^T; movmatrix turns the weights into P^T's fragment.
+//
+// K is read from shared memory 16 bytes to a lane: the product over channels does not care for
+// their order, so lane j of a quad takes 8 (bf16) or 16 (e4m3) neighbouring channels and Q's
+// fragments are laid out the same way. V goes through ldmatrix.trans; for e4m3 the 16-bit
+// elements that it transposes are channel pairs, whose low and high bytes become the two halves
+// of a 16-channel fragment. 16-byte pieces of a row are XOR-swizzled so that neither reading has
+// bank conflicts.
 //
 // An e4m3 cache's codes become f16 by the hardware's conversion, two to an instruction, and the
 // products run in f16: a code is exact there, Q's rows are scaled to a largest exponent of 14
 // (a power of two for each row, exact but for elements 2^-28 times the largest), and the rows'
 // scales multiply the scores. V's scale goes into the exponent of P: with s' = s + log2(scale)
 // the sum for O runs relative to the maximum of s', the sum of weights relative to that of s.
-//
-// K is read from shared memory 16 bytes to a lane: the product over channels does not care for
-// their order, so lane j of a quad takes 8 (bf16) or 16 (e4m3) neighbouring channels and Q's
-// fragments are laid out the same way. V goes through ldmatrix.trans; for e4m3 the 16-bit
-// elements that it transposes are channel pairs, whose low and high bytes become the fragments
-// of two 8-channel tiles. 16-byte pieces of a row are XOR-swizzled so that neither reading has
-// bank conflicts.
 #include <algorithm>
 #include <cmath>
 
@@ -37,14 +42,15 @@ constexpr int kWarps = 4;
 constexpr int kFewThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys of a stage
 constexpr float kGrow = 8.0f;               // a row maximum is raised when it grows by over 2^8
-// Blocks to an SM, and the shared memory of their stages. bf16 is at HBM's rate with two; the
-// e4m3 conversion leaves more latency to hide: three (where 16 rows leave the registers).
-template <bool kE4M3, int MT>
-constexpr int kPerSm = kE4M3 && MT == 1 ? 3 : 2;
+// Blocks to an SM and the shared memory of a block's stages, for NT tiles of 8 rows. bf16 is at
+// HBM's rate with two; the e4m3 conversion leaves more latency to hide, as far as the registers
+// go.
+template <bool kE4M3, int NT>
+constexpr int kPerSm = !kE4M3 ? 2 : (NT == 1 ? 4 : (NT == 2 ? 3 : 2));
 
-template <int D, bool kE4M3, int MT>
+template <int D, bool kE4M3, int NT>
 struct FewCfg {
-  static constexpr int kStageBudget = (kPerSm<kE4M3, MT> == 3 ? 66 : 96) * 1024;
+  static constexpr int kStageBudget = (kPerSm<kE4M3, NT> == 4 ? 50 : (kPerSm<kE4M3, NT> == 3 ? 67 : 96)) * 1024;
   static constexpr int kRowBytes = kE4M3 ? D : 2 * D;
   static constexpr int kPieces = kRowBytes / 16;               // 16-byte pieces of a row
   static constexpr int kTile = kChunk * kRowBytes;             // K or V of a chunk
@@ -110,14 +116,21 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The 8x8 matrix of 16-bit elements that the warp holds, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 struct Piece {
   int valid, i, h, u, a, n, len, end, ga, gb, slot;
 };
 
-template <int D, bool kE4M3, int MT>
-__global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(const AttnArgs a) {
-  using C = FewCfg<D, kE4M3, MT>;
-  using P = FewRows<16 * MT>;
+template <int D, bool kE4M3, int NT>
+__global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(const AttnArgs a) {
+  using C = FewCfg<D, kE4M3, NT>;
+  using P = FewRows<8 * NT>;
   constexpr int kRows = P::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Line<kFewThreads> line;
@@ -126,7 +139,8 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
   __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = lane >> 2, j = lane & 3;  // this lane's fragment rows (row, row + 8) and columns
+  // this lane's fragment row (a key, or a channel; and that + 8) and its pair of columns
+  const int i8 = lane >> 2, j = lane & 3;
   const int b = blockIdx.x;
   let_next_start();
   wait_for_previous();
@@ -136,8 +150,11 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
   const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
 
   const uint32_t stages = smem_u32(smem) + warp * C::kWarpBytes;
-  float* sums = reinterpret_cast<float*>(smem);  // [kWarps][kRows][D], over the stages at a piece's end
-  static_assert(kWarps * kRows * D * 4 <= C::kStageBudget, "the warps' sums fit the stages");
+  // [kWarps][kRows][kSumRow], over the stages at a piece's end; 4 floats between rows keep a warp's
+  // stores on different banks
+  float* sums = reinterpret_cast<float*>(smem);
+  constexpr int kSumRow = D + 4;
+  static_assert(kWarps * kRows * kSumRow * 4 <= C::kStageBudget, "the warps' sums fit the stages");
   const int page_mask = (1 << a.c.page_shift) - 1;
 
   Walk<P> w = walk;  // thread 0 goes on from there
@@ -226,92 +243,95 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
     for (int x = 0; x < C::kStages - 1; ++x) issue();
 
 
-    // this lane's rows (2 for each 16-row tile): query row, first key it does not see
-    uint32_t q[MT][D / 16][4];
-    int lim[MT][2];
-    int lim_min = p.len;
+    // Q as the second operand: tile t's row 8 t + i8
+    uint32_t q[NT][D / 16][2];
+    int lim_min = p.len;  // first key that some row does not see
     if (a.causal) {
       int tok, head;
       P::row(s, a.group, p.u, 0, tok, head);
       lim_min = s.len - s.n + tok + 1;
     }
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int t = 0; t < NT; ++t) {
+      int tok, head;
+      const bool on = P::row(s, a.group, p.u, 8 * t + i8, tok, head);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + (static_cast<long long>(p.h * a.group + (on ? head : 0)) * a.c.total_new + s.a + (on ? tok : 0)) * D);
+      if constexpr (kE4M3) {
+        // 64 channels: lane j has channels 16 j .. 16 j + 15, in products 0-3 of the 64
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        int tok, head;
-        const bool on = P::row(s, a.group, p.u, 16 * t + 8 * x + row, tok, head);
-        lim[t][x] = !on || !a.causal ? s.len : s.len - s.n + tok + 1;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + (static_cast<long long>(p.h * a.group + (on ? head : 0)) * a.c.total_new + s.a + (on ? tok : 0)) * D);
-        if constexpr (kE4M3) {
-          // 64 channels: lane j has channels 16 j .. 16 j + 15, in products 0-3 of the 64
+        for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint4 v = on ? __ldg(src + c * 8 + 2 * j + y) : make_uint4(0, 0, 0, 0);
-              q[t][4 * c + 2 * y][x] = v.x;
-              q[t][4 * c + 2 * y][2 + x] = v.y;
-              q[t][4 * c + 2 * y + 1][x] = v.z;
-              q[t][4 * c + 2 * y + 1][2 + x] = v.w;
-            }
-        } else {
-          // 32 channels: lane j has channels 8 j .. 8 j + 7, in products 0-1 of the 32
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const uint4 v = on ? __ldg(src + c * 4 + j) : make_uint4(0, 0, 0, 0);
-            q[t][2 * c][x] = v.x;
-            q[t][2 * c][2 + x] = v.y;
-            q[t][2 * c + 1][x] = v.z;
-            q[t][2 * c + 1][2 + x] = v.w;
+          for (int y = 0; y < 2; ++y) {
+            const uint4 v = on ? __ldg(src + c * 8 + 2 * j + y) : make_uint4(0, 0, 0, 0);
+            q[t][4 * c + 2 * y][0] = v.x;
+            q[t][4 * c + 2 * y][1] = v.y;
+            q[t][4 * c + 2 * y + 1][0] = v.z;
+            q[t][4 * c + 2 * y + 1][1] = v.w;
           }
+      } else {
+        // 32 channels: lane j has channels 8 j .. 8 j + 7, in products 0-1 of the 32
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const uint4 v = on ? __ldg(src + c * 4 + j) : make_uint4(0, 0, 0, 0);
+          q[t][2 * c][0] = v.x;
+          q[t][2 * c][1] = v.y;
+          q[t][2 * c + 1][0] = v.z;
+          q[t][2 * c + 1][1] = v.w;
         }
       }
+    }
 
-    // e4m3: Q's rows as f16 scaled by 2^(14 - e), e the largest exponent of the row; scores take
-    // back 2^(e - 14) with the factor that brings them to log2 units
-    float row_factor[MT][2];
+    // The lane's columns of S^T are rows 8 t + 2 j + {0, 1}: the first key that each does not see, and
+    // the factor that brings its scores to log2 units. e4m3: Q's rows as f16 scaled by 2^(14 - e), e
+    // the largest exponent of the row, which the factor takes back.
+    int lim[NT][2];
+    float factor[NT][2];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        row_factor[t][x] = a.scale_log2;
-        if constexpr (kE4M3) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int y = 0; y < 4; y += 2)
-              top = max(top, max(q[t][c][y + x] & 0x7fffu, (q[t][c][y + x] >> 16) & 0x7fffu));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int up = min(126, 141 - static_cast<int>(top >> 7));  // 14 - (exponent - 127), of rows past 2^-113
-          const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-          row_factor[t][x] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int y = 0; y < 4; y += 2)
-              q[t][c][y + x] = pack_f16(__uint_as_float(q[t][c][y + x] << 16) * f,
-                                        __uint_as_float(q[t][c][y + x] & 0xffff0000u) * f);
-        }
+      for (int e = 0; e < 2; ++e) {
+        int tok, head;
+        const bool on = P::row(s, a.group, p.u, 8 * t + 2 * j + e, tok, head);
+        lim[t][e] = !on || !a.causal ? s.len : s.len - s.n + tok + 1;
+        factor[t][e] = a.scale_log2;
       }
+      if constexpr (kE4M3) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) top = max(top, max(q[t][c][y] & 0x7fffu, (q[t][c][y] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int up = min(126, 141 - static_cast<int>(top >> 7));  // 14 - (exponent - 127), of rows past 2^-112
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            q[t][c][y] = pack_f16(__uint_as_float(q[t][c][y] << 16) * f, __uint_as_float(q[t][c][y] & 0xffff0000u) * f);
+        const float back = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) factor[t][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * j + e));
+      }
+    }
 
     // m: the maximum of a row's scores, which its weights' sum l is relative to; mo: for e4m3 that of
-    // scores with V's scale, which acc is relative to
-    float m[MT][2], l[MT][2], mo[MT][2], acc[MT][D / 8][4];
+    // scores with V's scale, which acc is relative to. The eight lanes of a column pair share m and mo;
+    // l is over the lane's own keys.
+    float m[NT][2], l[NT][2], mo[NT][2], acc[D / 16][NT][4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        m[t][x] = mo[t][x] = -INFINITY;
-        l[t][x] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        m[t][e] = mo[t][e] = -INFINITY;
+        l[t][e] = 0.f;
       }
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c)
+      for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][c][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[c][t][e] = 0.f;
     }
 
     int stage = 0;
@@ -322,156 +342,150 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
       const uint32_t kt = stages + stage * C::kStage, vt = kt + C::kTile;
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
 
-      float sc[MT][2][4];
+      // S^T: element 2 y + e is key + 8 y + i8, row 8 t + 2 j + e
+      float sc[NT][4];
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int e = 0; e < 4; ++e) sc[t][e] = 0.f;
+      if constexpr (kE4M3) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[t][y][e] = 0.f;
+        for (int c = 0; c < D / 64; ++c) {
+          const uint4 v0 = lds16(kt + piece_at<C::kRowBytes>(i8, 4 * c + j));
+          const uint4 v1 = lds16(kt + piece_at<C::kRowBytes>(8 + i8, 4 * c + j));
+          const uint32_t raw0[4] = {v0.x, v0.y, v0.z, v0.w}, raw1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        if constexpr (kE4M3) {
+          for (int x = 0; x < 4; ++x) {
+            uint32_t f[4];
+            e4m3x4_to_f16x2(raw0[x], f[0], f[2]);
+            e4m3x4_to_f16x2(raw1[x], f[1], f[3]);
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint4 v = lds16(kt + piece_at<C::kRowBytes>(8 * y + row, 4 * c + j));
-            const uint32_t raw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t b0, b1;
-              e4m3x4_to_f16x2(raw[x], b0, b1);
-#pragma unroll
-              for (int t = 0; t < MT; ++t) mma16816h(sc[t][y], q[t][4 * c + x], b0, b1);
-            }
+            for (int t = 0; t < NT; ++t) mma16816h(sc[t], f, q[t][4 * c + x][0], q[t][4 * c + x][1]);
           }
-        } else {
+        }
+      } else {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const uint4 v = lds16(kt + piece_at<C::kRowBytes>(8 * y + row, 4 * c + j));
+        for (int c = 0; c < D / 32; ++c) {
+          const uint4 v0 = lds16(kt + piece_at<C::kRowBytes>(i8, 4 * c + j));
+          const uint4 v1 = lds16(kt + piece_at<C::kRowBytes>(8 + i8, 4 * c + j));
+          const uint32_t lo[4] = {v0.x, v1.x, v0.y, v1.y}, hi[4] = {v0.z, v1.z, v0.w, v1.w};
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              mma16816(sc[t][y], q[t][2 * c], v.x, v.y);
-              mma16816(sc[t][y], q[t][2 * c + 1], v.z, v.w);
-            }
+          for (int t = 0; t < NT; ++t) {
+            mma16816(sc[t], lo, q[t][2 * c][0], q[t][2 * c][1]);
+            mma16816(sc[t], hi, q[t][2 * c + 1][0], q[t][2 * c + 1][1]);
           }
         }
       }
-      // Scores in log2 units; columns of this lane: keys key + 8 y + 2 j + {0, 1}. For e4m3 so is the
-      // score with log2 of V's scale added, else it is the score. Lane l turns one of the 32 scales
-      // (16 of K, 16 of V) into what is needed of it, and the others ask for it.
-      float so[MT][2][4];
-      float kf[2][2], vf[2][2];
+      // Scores in log2 units; for e4m3 `so` is the score with log2 of V's scale added. Lane l turns one
+      // of the 32 scales (16 of K, 16 of V) into what is needed of it, and the others ask for it.
+      float so[NT][4];
+      float kf[2], vf[2];
       if constexpr (kE4M3) {
         const uint32_t byte = lds_u8(kt + 2 * C::kTile + lane);
         const float mine = lane < 16 ? e8m0_to_float(byte) : e8m0_log2(byte);
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            kf[y][e] = __shfl_sync(0xffffffffu, mine, 8 * y + 2 * j + e);
-            vf[y][e] = __shfl_sync(0xffffffffu, mine, 16 + 8 * y + 2 * j + e);
-          }
+        for (int y = 0; y < 2; ++y) {
+          kf[y] = __shfl_sync(0xffffffffu, mine, 8 * y + i8);
+          vf[y] = __shfl_sync(0xffffffffu, mine, 16 + 8 * y + i8);
+        }
       }
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (kE4M3) {
-              sc[t][y][e] *= row_factor[t][e >> 1] * kf[y][e & 1];
-              so[t][y][e] = sc[t][y][e] + vf[y][e & 1];
-            } else {
-              sc[t][y][e] *= a.scale_log2;
-            }
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (kE4M3) {
+            sc[t][e] *= factor[t][e & 1] * kf[e >> 1];
+            so[t][e] = sc[t][e] + vf[e >> 1];
+          } else {
+            sc[t][e] *= factor[t][e & 1];
           }
+        }
       if (key + kChunk > lim_min) {  // some row does not see the whole chunk
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key + 8 * y + 2 * j + (e & 1) >= lim[t][e >> 1]) sc[t][y][e] = so[t][y][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            if (key + 8 * (e >> 1) + i8 >= lim[t][e & 1]) sc[t][e] = so[t][e] = -INFINITY;
       }
       // raise the running maxima only when some row's grew by more than 2^8: P stays below 2^8
       bool grow = false;
-      float top[MT][2], topo[MT][2];
+      float top[NT][2], topo[NT][2];
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          top[t][x] = fmaxf(max3f(sc[t][0][2 * x], sc[t][0][2 * x + 1], sc[t][1][2 * x]), sc[t][1][2 * x + 1]);
-          grow = grow || top[t][x] > m[t][x] + kGrow;
+        for (int e = 0; e < 2; ++e) {
+          top[t][e] = fmaxf(sc[t][e], sc[t][2 + e]);
+          grow = grow || top[t][e] > m[t][e] + kGrow;
           if constexpr (kE4M3) {
-            topo[t][x] = fmaxf(max3f(so[t][0][2 * x], so[t][0][2 * x + 1], so[t][1][2 * x]), so[t][1][2 * x + 1]);
-            grow = grow || topo[t][x] > mo[t][x] + kGrow;
+            topo[t][e] = fmaxf(so[t][e], so[t][2 + e]);
+            grow = grow || topo[t][e] > mo[t][e] + kGrow;
           }
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int e = 0; e < 2; ++e) {
             auto raise = [](float& at, float to) -> float {  // the factor of what was relative to `at`
-              to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 1));
-              to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 2));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
               to = fmaxf(to, at);
               const float f = to == -INFINITY ? 1.f : fast_exp2(at - to);
               at = to;
               return f;
             };
-            float f = raise(m[t][x], top[t][x]);
-            l[t][x] *= f;
-            if constexpr (kE4M3) f = raise(mo[t][x], topo[t][x]);
+            float f = raise(m[t][e], top[t][e]);
+            l[t][e] *= f;
+            if constexpr (kE4M3) f = raise(mo[t][e], topo[t][e]);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              acc[t][c][2 * x] *= f;
-              acc[t][c][2 * x + 1] *= f;
+            for (int c = 0; c < D / 16; ++c) {
+              acc[c][t][e] *= f;
+              acc[c][t][2 + e] *= f;
             }
           }
       }
-      uint32_t pa[MT][4];
+      // P^T: the packed pairs are (key; rows 2 j, 2 j + 1) and are wanted as (row; keys 2 j, 2 j + 1)
+      uint32_t pt[NT][2];
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        float pw[4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float mb = m[t][x] == -INFINITY ? 0.f : m[t][x];
-          const float mob = mo[t][x] == -INFINITY ? 0.f : mo[t][x];
+        for (int e = 0; e < 4; ++e) {
+          pw[e] = fast_exp2(sc[t][e] - (m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1]));
+          l[t][e & 1] += pw[e];
+          // in f16: off by 2^-11 of itself, or 2^-25 of the row's largest
+          if constexpr (kE4M3) pw[e] = fast_exp2(so[t][e] - (mo[t][e & 1] == -INFINITY ? 0.f : mo[t][e & 1]));
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          pt[t][y] = transpose8x8(kE4M3 ? pack_f16(pw[2 * y], pw[2 * y + 1])
+                                        : pack_bf16(pw[2 * y], pw[2 * y + 1]));  // bf16: off by 2^-8 of itself at most
+      }
+      if constexpr (kE4M3) {
+        const int vr = (lane & 7) + (lane & 8);  // keys 0-7, 8-15 of a 16-channel piece, then of the next
+#pragma unroll
+        for (int c = 0; c < C::kPieces; c += 2) {
+          uint32_t f[4];
+          ldsm4_trans(vt + piece_at<C::kRowBytes>(vr, c + (lane >> 4)), f);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float p0 = fast_exp2(sc[t][y][2 * x] - mb), p1 = fast_exp2(sc[t][y][2 * x + 1] - mb);
-            l[t][x] += p0 + p1;
-            if constexpr (kE4M3)  // in f16: off by 2^-11 of itself, or 2^-25 of the row's largest
-              pa[t][2 * y + x] = pack_f16(fast_exp2(so[t][y][2 * x] - mob), fast_exp2(so[t][y][2 * x + 1] - mob));
-            else
-              pa[t][2 * y + x] = pack_bf16(p0, p1);  // off by 2^-8 of itself at most
+            // bytes: even and odd channel of one key, then of the next; the even channels are the
+            // fragment's rows 0-7, the odd ones 8-15
+            uint32_t v[4];
+            e4m3x4_to_f16x2(__byte_perm(f[2 * y], 0, 0x3120), v[0], v[1]);
+            e4m3x4_to_f16x2(__byte_perm(f[2 * y + 1], 0, 0x3120), v[2], v[3]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816h(acc[c + y][t], v, pt[t][0], pt[t][1]);
           }
         }
-      const int vr = (lane & 7) + (lane & 8);  // ldmatrix: keys 0-7, 8-15, then the next piece
+      } else {
+        const int vr = (lane & 7) + ((lane >> 4) << 3);  // channels 0-7, 8-15 of keys 0-7, then of keys 8-15
 #pragma unroll
-      for (int c = 0; c < C::kPieces; c += 2) {
-        uint32_t f[4];
-        ldsm4_trans(vt + piece_at<C::kRowBytes>(vr, c + (lane >> 4)), f);
-        if constexpr (kE4M3) {
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t v[4];
+          ldsm4_trans(vt + piece_at<C::kRowBytes>(vr, 2 * c + ((lane >> 3) & 1)), v);
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            // bytes: even and odd channel of one key, then of the next; a fragment wants two keys
-            uint32_t even0, odd0, even1, odd1;
-            e4m3x4_to_f16x2(__byte_perm(f[2 * y], 0, 0x3120), even0, odd0);
-            e4m3x4_to_f16x2(__byte_perm(f[2 * y + 1], 0, 0x3120), even1, odd1);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              mma16816h(acc[t][2 * (c + y)], pa[t], even0, even1);
-              mma16816h(acc[t][2 * (c + y) + 1], pa[t], odd0, odd1);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            mma16816(acc[t][c], pa[t], f[0], f[1]);
-            mma16816(acc[t][c + 1], pa[t], f[2], f[3]);
-          }
+          for (int t = 0; t < NT; ++t) mma16816(acc[c][t], v, pt[t][0], pt[t][1]);
         }
       }
     }
@@ -479,39 +493,35 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
 
     // the warps' sums meet: every row relative to the largest of the warps' maxima
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float sum = l[t][x];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        l[t][x] = sum;
-        if (j == 0) warp_m[warp][16 * t + 8 * x + row] = m[t][x];
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], o);
+        if (i8 == 0) warp_m[warp][8 * t + 2 * j + e] = m[t][e];
       }
     __syncthreads();  // also: every warp is done with its stages
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = 16 * t + 8 * x + row;
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * t + 2 * j + e;
         float mx = warp_m[0][r];
 #pragma unroll
         for (int y = 1; y < kWarps; ++y) mx = fmaxf(mx, warp_m[y][r]);
-        float f = mx == -INFINITY ? 0.f : fast_exp2(m[t][x] - mx);
-        if (j == 0) warp_l[warp][r] = l[t][x] * f;
-        if constexpr (kE4M3) f = mx == -INFINITY ? 0.f : fast_exp2(mo[t][x] - mx);  // acc's own reference
-        float* dst = sums + (static_cast<size_t>(warp) * kRows + r) * D;
-        if constexpr (kE4M3) {
-          // tiles 2 c and 2 c + 1 hold the even and odd channels of piece c: 4 in a row
+        float f = mx == -INFINITY ? 0.f : fast_exp2(m[t][e] - mx);
+        if (i8 == 0) warp_l[warp][r] = l[t][e] * f;
+        if constexpr (kE4M3) f = mx == -INFINITY ? 0.f : fast_exp2(mo[t][e] - mx);  // acc's own reference
+        float* dst = sums + (static_cast<size_t>(warp) * kRows + r) * kSumRow;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            reinterpret_cast<float4*>(dst + 16 * c)[j] =
-                make_float4(acc[t][2 * c][2 * x] * f, acc[t][2 * c + 1][2 * x] * f, acc[t][2 * c][2 * x + 1] * f,
-                            acc[t][2 * c + 1][2 * x + 1] * f);
-        } else {
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            reinterpret_cast<float2*>(dst + 8 * c)[j] = make_float2(acc[t][c][2 * x] * f, acc[t][c][2 * x + 1] * f);
+        for (int c = 0; c < D / 16; ++c) {
+          const float x0 = acc[c][t][e] * f, x1 = acc[c][t][2 + e] * f;
+          if constexpr (kE4M3) {  // channels 2 i8 and 2 i8 + 1 of the 16
+            *reinterpret_cast<float2*>(dst + 16 * c + 2 * i8) = make_float2(x0, x1);
+          } else {
+            dst[16 * c + i8] = x0;
+            dst[16 * c + 8 + i8] = x1;
+          }
         }
       }
     __syncthreads();
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, MT>) few_kernel(con
       float sum = 0.f, mx = -INFINITY;
 #pragma unroll
       for (int y = 0; y < kWarps; ++y) {
-        const float4 v = reinterpret_cast<const float4*>(sums + (static_cast<size_t>(y) * kRows + r) * D)[c];
+        const float4 v = reinterpret_cast<const float4*>(sums + (static_cast<size_t>(y) * kRows + r) * kSumRow)[c];
         o.x += v.x;
         o.y += v.y;
         o.z += v.z;
@@ -557,23 +567,23 @@ fcp_status sm_count(int* n) {
   return FCP_OK;
 }
 
-template <int D, bool kE4M3, int MT>
+template <int D, bool kE4M3, int NT>
 fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaStream_t s) {
-  using C = FewCfg<D, kE4M3, MT>;
-  using P = FewRows<16 * MT>;
-  constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * D * 4);
-  const int blocks = std::min(kPerSm<kE4M3, MT> * n_sm, kMaxBlocks);
+  using C = FewCfg<D, kE4M3, NT>;
+  using P = FewRows<8 * NT>;
+  constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * (D + 4) * 4);
+  const int blocks = std::min(kPerSm<kE4M3, NT> * n_sm, kMaxBlocks);
   set_workspace<P>(a, workspace, D, kMaxBlocks);
-  FCP_CUDA_TRY(cudaFuncSetAttribute(few_kernel<D, kE4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+  FCP_CUDA_TRY(cudaFuncSetAttribute(few_kernel<D, kE4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
                "paged attention smem attribute");
-  if (const fcp_status st = launch_overlapped(few_kernel<D, kE4M3, MT>, dim3(blocks), kFewThreads, kSmem, s,
+  if (const fcp_status st = launch_overlapped(few_kernel<D, kE4M3, NT>, dim3(blocks), kFewThreads, kSmem, s,
                                               "paged attention launch", a);
       st != FCP_OK)
     return st;
   // the merge's row slices: a warp takes two rows where groups have few pieces (many groups), else a
   // block takes one
   const long long rows = std::min<long long>(static_cast<long long>(std::max(max_new, 1)) * a.group, P::kRows);
-  const bool few_pieces = static_cast<long long>(kWarpPieces) * a.c.n_seqs * a.c.hkv >= blocks;
+  const bool few_pieces = static_cast<long long>(P::kWarpPieces) * a.c.n_seqs * a.c.hkv >= blocks;
   return launch_merge<P, D>(
       a, blocks, static_cast<int>(few_pieces ? (rows + 2 * kMergeWarps - 1) / (2 * kMergeWarps) : rows), s);
 }
@@ -584,12 +594,11 @@ fcp_status launch_attn(const AttnArgs& a, int dtype, int hq, int max_new, void* 
   if (const fcp_status st = sm_count(&n_sm); st != FCP_OK) return st;
   const long long rows = static_cast<long long>(max_new) * a.group;
   if (rows > 32) return launch_paged_chunk(a, dtype, D, hq, workspace, n_sm, s);
-  const bool wide = rows > 16;
-  if (dtype == FCP_CACHE_E4M3)
-    return wide ? launch_few<D, true, 2>(a, workspace, n_sm, max_new, s)
-                : launch_few<D, true, 1>(a, workspace, n_sm, max_new, s);
-  return wide ? launch_few<D, false, 2>(a, workspace, n_sm, max_new, s)
-              : launch_few<D, false, 1>(a, workspace, n_sm, max_new, s);
+  const bool e = dtype == FCP_CACHE_E4M3;
+  auto* launch = rows <= 8    ? (e ? launch_few<D, true, 1> : launch_few<D, false, 1>)
+                 : rows <= 16 ? (e ? launch_few<D, true, 2> : launch_few<D, false, 2>)
+                              : (e ? launch_few<D, true, 4> : launch_few<D, false, 4>);
+  return launch(a, workspace, n_sm, max_new, s);
 }
 
 }  // namespace

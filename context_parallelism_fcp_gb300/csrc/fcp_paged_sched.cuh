@@ -17,7 +17,7 @@
 namespace fcp {
 
 constexpr int kGranule = 128;    // keys
-constexpr int kMaxBlocks = 480;       // few rows: three blocks to each of up to 160 SMs
+constexpr int kMaxBlocks = 640;       // few rows: up to four blocks to each of up to 160 SMs
 constexpr int kMaxChunkBlocks = 160;  // chunks: one
 
 struct SplitGroup;
@@ -57,6 +57,7 @@ __device__ __forceinline__ int granules_of(int end) { return max(1, (end + kGran
 template <int kRowsPerUnit>
 struct FewRows {
   static constexpr int kRows = kRowsPerUnit;
+  static constexpr int kWarpPieces = 8;  // of a row, up to which the merge gives a row to a warp
   static constexpr int kOverhead = 1;
   static __device__ __forceinline__ int units(const SeqShape& s, int group) {
     return static_cast<int>((static_cast<long long>(s.n) * group + kRows - 1) / kRows);
@@ -88,6 +89,7 @@ struct FewRows {
 // tiles of a KV head are ordered tokens first, heads within them, and a unit is two of them.
 struct ChunkRows {
   static constexpr int kRows = 2 * kTileM;
+  static constexpr int kWarpPieces = 32;
   static constexpr int kOverhead = 3;
   struct Shape {
     int log_tokens, heads, head_tiles, token_tiles, tiles;
@@ -282,7 +284,6 @@ static_assert(sizeof(SplitGroup) == 32, "two 16-byte loads");
 // O = sum 2^(m - M) o / sum 2^(m - M) l, over the pieces in a fixed order. grid (blocks, row
 // slices); a warp takes rows of up to kWarpPieces pieces, the whole block a row of more.
 constexpr int kMergeWarps = 4;
-constexpr int kWarpPieces = 32;
 template <class P, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const AttnArgs a) {
   constexpr int kPieceLanes = D / 4;                             // lanes of a piece, 4 channels each
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Att
   const int count = g.last - b + 1;
   if (count <= 1) return;
   const SeqShape s{g.a, g.n, 0};
-  if (count <= kWarpPieces) {
+  if (count <= P::kWarpPieces) {
     // a warp takes two rows on its own, the loads of four pieces of both side by side
     constexpr int kEach = D / 32;  // channels of a lane
     constexpr int kR = 2, kX = 4;
