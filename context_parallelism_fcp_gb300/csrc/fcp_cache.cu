@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
   wait_for_previous();
   const int t0 = blockIdx.x * kMoveTokens;
   find_places(p, t0, place, coarse);
+  if (blockIdx.x + blockIdx.y + blockIdx.z == 0)  // errors of sequences that no row is found in, too
+    for (int i = threadIdx.x; i < p.n_seqs; i += kMoveThreads) seq_shape(p, i, true);
   const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, p.hkv);
   uint4* __restrict__ rows = blockIdx.z ? v : k;
   uint8_t* __restrict__ pages = blockIdx.z ? p.v_pages : p.k_pages;

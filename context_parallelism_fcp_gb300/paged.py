@@ -19,19 +19,22 @@ __all__ = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn"
 _DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
 
-def _here(device, stream) -> int:
+def _here(index: int, stream) -> int:
     """The stream to launch on. Kernels run on the current device, so that is where the tensors
     have to be."""
-    index = torch._C._cuda_getDevice()
-    if device.index != index:
-        raise ValueError(f"the cache is on {device}, the current device is cuda:{index}")
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError(f"the cache is on cuda:{index}, the current device is cuda:{torch._C._cuda_getDevice()}")
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
 
 
-def _want(t, dtype, shape, name) -> None:
-    """_need, at the cost of a step's few microseconds in mind: the usual case is checked first."""
-    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _need(t, dtype, shape, name)
+def _want(t, dtype, shape, index: int, name: str) -> None:
+    """_need and the device, with a step's few microseconds in mind: what is right passes quickly."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return
+    _need(t, dtype, shape, name)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
 
 
 class PagedCache:
@@ -82,7 +85,7 @@ class PagedCache:
             raise ValueError(f"head_dim must be 64 or 128, got {self.head_dim}")
         if self.page_size not in (16, 32, 64, 128, 256, 512, 1024, 2048, 4096):
             raise ValueError(f"page_size must be a power of two from 16 to 4096, got {self.page_size}")
-        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self.dtype, self.device, self._index = k_pages.dtype, k_pages.device, k_pages.get_device()
         self.status = torch.zeros(64, dtype=torch.int32, device=self.device)
         self._struct = _CacheStruct(
             k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr() if quantised else None,
@@ -119,18 +122,20 @@ class CacheBatch:
             raise ValueError("the batch's tensors must be on one device")
         self.cu_new, self.lens, self.block_table = cu_new, lens, block_table
         self.n_seqs, self.total_new, self.max_new, self.device = n, int(total_new), int(max_new), lens.device
+        self._index = lens.get_device()
         self._struct = _CacheBatchStruct(cu_new.data_ptr(), lens.data_ptr(), block_table.data_ptr(), n,
                                          block_table.shape[1], self.total_new, self.max_new)
         self._ref = ctypes.byref(self._struct)
 
 
 def _move(fn, name, cache: PagedCache, batch: CacheBatch, k, v, stream) -> None:
+    index = cache._index
+    if batch._index != index:
+        raise ValueError("the batch and the cache must be on one device")
     shape = (cache.hkv, batch.total_new, cache.head_dim)
-    _want(k, torch.bfloat16, shape, "k")
-    _want(v, torch.bfloat16, shape, "v")
-    if not (k.device == v.device == batch.device == cache.device):
-        raise ValueError("k, v, the batch and the cache must be on one device")
-    status = fn(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), _here(cache.device, stream))
+    _want(k, torch.bfloat16, shape, index, "k")
+    _want(v, torch.bfloat16, shape, index, "v")
+    status = fn(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), _here(index, stream))
     if status:
         _check(status, name)
 
@@ -153,14 +158,19 @@ def paged_attn(cache: PagedCache, batch: CacheBatch, q, o, lse, workspace, causa
     must be in the cache. workspace: a CUDA uint8 tensor of fcp_paged_attn_workspace_bytes(D)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [Hq, total_new, D]")
-    shape = (q.shape[0], batch.total_new, cache.head_dim)
-    _want(q, torch.bfloat16, shape, "q")
-    _want(o, torch.bfloat16, shape, "o")
-    _want(lse, torch.float32, shape[:2], "lse")
-    if not (q.device == o.device == lse.device == workspace.device == batch.device == cache.device):
-        raise ValueError("q, o, lse, the workspace, the batch and the cache must be on one device")
-    status = lib().fcp_paged_attn(cache._ref, batch._ref, q.data_ptr(), shape[0], 1 if causal else 0, o.data_ptr(),
-                                  lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _here(cache.device, stream))
+    _attend(cache, batch, q, o, lse, workspace, causal, q.shape[0], stream)
+
+
+def _attend(cache, batch, q, o, lse, workspace, causal, hq, stream) -> None:
+    index = cache._index
+    if batch._index != index or workspace.get_device() != index:
+        raise ValueError("the batch, the workspace and the cache must be on one device")
+    shape = (hq, batch.total_new, cache.head_dim)
+    _want(q, torch.bfloat16, shape, index, "q")
+    _want(o, torch.bfloat16, shape, index, "o")
+    _want(lse, torch.float32, shape[:2], index, "lse")
+    status = lib().fcp_paged_attn(cache._ref, batch._ref, q.data_ptr(), hq, 1 if causal else 0, o.data_ptr(),
+                                  lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _here(index, stream))
     if status:
         _check(status, "fcp_paged_attn")
 
@@ -179,11 +189,9 @@ class PagedAttention:
     def forward(self, batch: CacheBatch, q, o=None, lse=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """(o, lse) of the batch's new tokens; rows that belong to no sequence are left as they
         were in the buffers given, and are undefined in those that are allocated here."""
-        if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] != self.hq:
-            raise ValueError(f"q must be a tensor [{self.hq}, total_new, D]")
         if o is None:
             o = torch.empty_like(q)
         if lse is None:
             lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        paged_attn(self.cache, batch, q, o, lse, self.workspace, self.causal, stream)
+        _attend(self.cache, batch, q, o, lse, self.workspace, self.causal, self.hq, stream)
         return o, lse

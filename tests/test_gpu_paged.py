@@ -207,3 +207,332 @@ def test_attention_of_chunks(fcp, b):
     o, lse, before = attend(fcp, b, t, cache, batch)
     cache.check_device_error()
     U.check_attention(b, t, o, lse, *before)
+
+
+# ---------------------------------------------------------------- what goes wrong elsewhere
+@pytest.mark.parametrize("new", [1, 3, 60], ids=["few8", "few16", "chunk"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_with_scales_across_the_range(fcp, new, d):
+    """Rows whose scales differ by many powers of two, in K and in V, some too large for one bf16 product:
+    the weights and sums must not over- or underflow on the way."""
+    b = Batch([new, new], [200, 333], hq=4, hkv=1, d=d, page=32, cache="e4m3", seed=new)
+    t = U.make(b)
+    g = torch.Generator().manual_seed(9)
+    for x, lo, hi in (("k", 110, 119), ("v", 90, 165)):
+        byte = t[x + "_scales"].view(torch.uint8)
+        new_byte = torch.randint(lo, hi, byte.shape, generator=g, dtype=torch.int32).to(torch.uint8).cuda()
+        byte.copy_(torch.where(byte == 255, byte, new_byte))
+    # a sequence in the range where V's rows are tiny, another with one huge row of K that gets all the weight
+    table = t["table"].cpu()
+    t["k_scales"].view(torch.uint8)[int(table[1, 2]), :, 5] = 137
+    cache, batch = U.handles(fcp, b, t)
+    o, lse, before = attend(fcp, b, t, cache, batch)
+    cache.check_device_error()
+    U.check_attention(b, t, o, lse, *before)
+
+
+@pytest.mark.parametrize("new", [1, 50], ids=["few", "chunk"])
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+def test_a_nan_row_reaches_its_readers(fcp, new, c):
+    """A NaN in a key makes every row that sees it NaN, and no other sequence's."""
+    b = Batch([new, new], [100, 100], hq=2, hkv=1, cache=c, page=16)
+    t = U.make(b)
+    page, off = int(t["table"][0, 1]), 3  # position 19 of sequence 0
+    if c == "bf16":
+        t["k_pages"][page, 0, off, 7] = float("nan")
+    else:
+        t["k_scales"].view(torch.uint8)[page, 0, off] = 255
+    cache, batch = U.handles(fcp, b, t)
+    o, lse, _ = attend(fcp, b, t, cache, batch)
+    cache.check_device_error()
+    sees = torch.arange(new) + 100 - new >= 19
+    assert o[:, :new].isnan().all(-1).cpu().equal(sees[None].expand(2, -1)) and lse[:, :new].isnan().cpu().equal(
+        sees[None].expand(2, -1))
+    assert not o[:, new:].isnan().any() and not lse[:, new:].isnan().any()
+
+
+@pytest.mark.parametrize("max_new", [1, 100], ids=["few", "chunk"])
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+def test_broken_batches_are_reported_and_harm_nothing(fcp, max_new, c):
+    """Offsets that fall back or pass the rows, lengths past the block table, page ids outside the cache:
+    the calls finish, the error word tells, what is right is computed and no other row is touched."""
+    b = Batch([2, 3, 1, 2, 2], [40, 30, 20, 33, 50], hq=4, hkv=2, cache=c, max_new=max_new, pad=4)
+    for what, code in (("cu", 0x50), ("back", 0x50), ("len", 0x50), ("negative", 0x50), ("page", 0x51),
+                       ("low page", 0x51)):
+        t = U.make(b)
+        good = U.make(b)
+        if what == "cu":
+            # sequence 2 has no row, 3 has 5 .. 7, and 4 would pass the rows: rows 8 and on are no one's
+            t["cu"][3:] = torch.tensor([5, 8, 99], dtype=torch.int32)
+            good["cu"][3:] = torch.tensor([5, 8, 8], dtype=torch.int32)
+            bad = {4}
+        elif what == "back":
+            t["cu"][5] = 3
+            bad = {4}
+        elif what == "len":
+            t["lens"][1] = 16 * t["table"].shape[1] + 1
+            bad = {1}
+        elif what == "negative":
+            t["lens"][3] = -1
+            bad = {3}
+        else:
+            t["table"][4, 0] = 1 << 30 if what == "page" else -1
+            bad = {4}
+        cache, batch = U.handles(fcp, b, t)
+        o, lse, before = attend(fcp, b, t, cache, batch)
+        with pytest.raises(fcp.FcpError, match=hex(code)):
+            cache.check_device_error()
+        cache.check_device_error()  # read and cleared
+        cache2, batch2 = U.handles(fcp, b, good)
+        want_o, want_l, _ = attend(fcp, b, good, cache2, batch2)
+        row = 0
+        for i, n in enumerate(b.new):
+            if i not in bad:
+                assert torch.equal(o[:, row:row + n], want_o[:, row:row + n]), (what, i)
+                assert torch.equal(lse[:, row:row + n], want_l[:, row:row + n])
+            elif code == 0x50:
+                assert torch.equal(o[:, row:row + n], before[0][:, row:row + n]), (what, i)
+            row += n
+        assert torch.equal(o[:, row:], before[0][:, row:])
+        k = torch.full_like(t["k"], 3.0)
+        fcp.cache_read(cache, batch, k, torch.empty_like(k))
+        with pytest.raises(fcp.FcpError):
+            if what in ("page", "low page"):  # only a needed entry counts: position 0 is not read back here
+                batch4 = fcp.CacheBatch(torch.tensor([0, 1], dtype=torch.int32).cuda(),
+                                        torch.tensor([1], dtype=torch.int32).cuda(), t["table"][4:].contiguous(), 1,
+                                        max_new=1)
+                fcp.cache_read(cache, batch4, k[:, :1].contiguous(), k[:, :1].contiguous())
+            cache.check_device_error()
+
+
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+def test_captured_calls_follow_the_tensors(fcp, c):
+    """write, attention and read captured into one graph on a side stream; replays see new rows, lengths
+    and block tables in the same buffers, for few rows and for chunks."""
+    for new, lens in (([1, 1, 1], [40, 7, 300]), ([45, 3, 0], [60, 200, 5])):
+        b = Batch(new, lens, hq=4, hkv=2, d=128, page=32, cache=c, seed=1)
+        t = U.make(b)
+        cache, batch = U.handles(fcp, b, t)
+        att = fcp.PagedAttention(cache, b.hq)
+        o, lse = torch.zeros_like(t["q"]), torch.zeros(b.hq, b.total, device="cuda")
+        k, v = torch.zeros_like(t["k"]), torch.zeros_like(t["v"])
+        side = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=side):
+            fcp.cache_write(cache, batch, t["k"], t["v"])
+            att.forward(batch, t["q"], o, lse)
+            fcp.cache_read(cache, batch, k, v)
+        for seed in (5, 6):
+            lens2 = [max(n, x - seed) for n, x in zip(new, lens)]
+            other = Batch(new, lens2, hq=4, hkv=2, d=128, page=32, cache=c, seed=seed)
+            u = U.make(other)
+            keep = min(t["table"].shape[1], u["table"].shape[1])
+            order = torch.arange(t["table"].numel(), dtype=torch.int32).view_as(t["table"]).cuda() % cache.n_pages
+            need = [-(-x // 32) for x in lens2]
+            ids = torch.randperm(cache.n_pages, generator=torch.Generator().manual_seed(seed)).int()
+            at = 0
+            for i, x in enumerate(need):
+                order[i, :x] = ids[at:at + x].cuda()
+                at += x
+            assert keep and at <= cache.n_pages
+            t["table"].copy_(order)
+            t["lens"].copy_(u["lens"])
+            for x in ("q", "k", "v"):
+                t[x].copy_(u[x])
+            for x in ("k_pages", "v_pages"):  # what was behind a sequence's end before may be inside now
+                p = torch.randn(t[x].shape, generator=torch.Generator().manual_seed(seed)).cuda()
+                t[x].copy_(p.to(t[x].dtype) if c == "bf16" else p.to(torch.float8_e4m3fn))
+                if c == "e4m3":
+                    t[x[0] + "_scales"].view(torch.uint8).fill_(126)
+            graph.replay()
+            cache.check_device_error()
+            now = Batch(new, lens2, hq=4, hkv=2, d=128, page=32, cache=c)
+            U.check_attention(now, t, o, lse)
+            stored = U.values(t["k_pages"], t["k_scales"])
+            table = t["table"].cpu().numpy()
+            for row, _, _, pg, off in R.places(new, lens2, table, 32):
+                assert np.array_equal(k[:, row].double().cpu().numpy(), stored[pg, :, off])
+
+
+def test_two_streams_with_a_workspace_each(fcp):
+    """Two attentions over one cache at a time, each on its own stream with its own PagedAttention."""
+    b1 = Batch([1, 1], [3000, 700], hq=8, hkv=2, d=128, seed=2)
+    b2 = Batch([70, 9], [3000, 700], hq=8, hkv=2, d=128, seed=2)
+    t = U.make(b1)
+    u = U.make(b2)
+    for x in ("k_pages", "v_pages", "table"):
+        u[x] = t[x]
+    cache, batch1 = U.handles(fcp, b1, t)
+    _, batch2 = U.handles(fcp, b2, u)
+    want1, want2 = attend(fcp, b1, t, cache, batch1)[0], attend(fcp, b2, u, cache, batch2)[0]
+    atts = [fcp.PagedAttention(cache, 8) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        outs.append((torch.empty_like(t["q"]), torch.empty_like(u["q"])))
+        lses = [torch.empty(8, x["q"].shape[1], device="cuda") for x in (t, u)]
+        torch.cuda.synchronize()
+        atts[0].forward(batch1, t["q"], outs[-1][0], lses[0], stream=streams[0])
+        atts[1].forward(batch2, u["q"], outs[-1][1], lses[1], stream=streams[1])
+    torch.cuda.synchronize()
+    cache.check_device_error()
+    for o1, o2 in outs:
+        assert torch.equal(o1, want1) and torch.equal(o2, want2)
+
+
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 40], ids=["few", "chunk"])
+def test_offsets_past_32_bits(fcp, c, new):
+    """Pages whose elements and bytes lie past 2^32: write, read and attention at the far end."""
+    page, hkv, d = 256, 8, 128
+    n_pages = (1 << 32) // (page * hkv * d) + 40  # over 2^32 elements in K and in V
+    cache = fcp.PagedCache(n_pages, page, hkv, d, dtype=torch.bfloat16 if c == "bf16" else torch.float8_e4m3fn)
+    length = 3 * page - 5
+    table = torch.tensor([[n_pages - 1, n_pages - 17, n_pages - 3, -9]], dtype=torch.int32).cuda()
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(hkv, length, d, generator=g).to(torch.bfloat16).cuda() for _ in "kv")
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    fcp.cache_write(cache, fcp.CacheBatch(ints([0, length]), ints([length]), table, length, max_new=length), k, v)
+    back = torch.empty_like(k), torch.empty_like(v)
+    fcp.cache_read(cache, fcp.CacheBatch(ints([0, length]), ints([length]), table, length, max_new=length), *back)
+    cache.check_device_error()
+    if c == "bf16":
+        assert torch.equal(back[0], k) and torch.equal(back[1], v)
+    else:
+        for got, x in zip(back, (k, v)):  # a code is off by at most half a step: 2^-4 of itself, or of 2^-6 * scale
+            top = x.float().abs().amax(-1, keepdim=True)
+            assert ((got.float() - x.float()).abs() <= 2.0 ** -4 * x.float().abs() + 2.0 ** -10 * 2.0 ** -6 * top).all()
+    q = torch.randn(hkv, new, d, generator=g).to(torch.bfloat16).cuda()
+    o, lse = fcp.PagedAttention(cache, hkv).forward(
+        fcp.CacheBatch(ints([0, new]), ints([length]), table, new, max_new=new), q)
+    cache.check_device_error()
+    for h in (0, hkv - 1):
+        ro, rl, spread, _, _ = R.attend(*(x[h].double().cpu().numpy() for x in (q, *back)), new, True)
+        assert (np.abs(o[h].double().cpu().numpy() - ro) <= 2.0 ** -8 * (spread + np.abs(ro)) + 2.0 ** -12 * spread).all()
+        assert np.abs(lse[h].double().cpu().numpy() - rl).max() <= 1e-4
+
+
+# ---------------------------------------------------------------- together, as a server uses them
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+def test_prompt_then_chunk_then_tokens(fcp, c):
+    """Two conversations: the prompt's attention over the work list (FcpAttention) with its K and V written
+    to the cache, then a chunk, then single tokens, each written and attended; every output is the causal
+    attention of the whole conversation at its rows, over the rows that the cache holds. Then the whole
+    conversation is read back and its attention over the work list is the same again."""
+    hq, hkv, d, page = 8, 2, 128, 32
+    prompts, chunks, steps = [300, 129], [70, 33], 3
+    total = [p + m + steps for p, m in zip(prompts, chunks)]
+    g = torch.Generator().manual_seed(8)
+    q, k, v = ([torch.randn(h, n, d, generator=g).to(torch.bfloat16).cuda() for n in total] for h in (hq, hkv, hkv))
+    pages = [-(-n // page) for n in total]
+    cache = fcp.PagedCache(sum(pages) + 1, page, hkv, d, dtype=torch.bfloat16 if c == "bf16" else torch.float8_e4m3fn)
+    ids = torch.randperm(sum(pages) + 1, generator=g).int()
+    table = torch.full((2, max(pages)), -1, dtype=torch.int32)
+    table[0, :pages[0]], table[1, :pages[1]] = ids[:pages[0]], ids[pages[0]:pages[0] + pages[1]]
+    table = table.cuda()
+    lens, cu = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    attention = fcp.PagedAttention(cache, hq)
+    outs = [[], []]
+    at = [0, 0]
+
+    def pack(x, new):
+        return torch.cat([x[i][:, at[i]:at[i] + new[i]] for i in range(2)], 1).contiguous()
+
+    for part, new in enumerate([prompts, chunks] + [[1, 1]] * steps):
+        lens.copy_(torch.tensor([a + n for a, n in zip(at, new)]))
+        cu.copy_(torch.tensor([0, new[0], sum(new)]))
+        batch = fcp.CacheBatch(cu, lens, table, sum(new), max_new=max(new))
+        qn, kn, vn = (pack(x, new) for x in (q, k, v))
+        fcp.cache_write(cache, batch, kn, vn)
+        if part == 0 and c == "bf16":
+            att = fcp.FcpAttention(new, 128, True, 2, hq, hkv, d, backward=False)
+            o, _ = att.forward(qn, kn, vn)
+            att.check_device_error()
+        else:
+            o, _ = attention.forward(batch, qn)
+        for i in range(2):
+            outs[i].append(o[:, int(cu[i]):int(cu[i + 1])])
+            at[i] += new[i]
+    cache.check_device_error()
+    lens.copy_(torch.tensor(total))
+    cu.copy_(torch.tensor([0, total[0], sum(total)]))
+    whole = fcp.CacheBatch(cu, lens, table, sum(total), max_new=max(total))
+    rk, rv = (torch.empty(hkv, sum(total), d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    fcp.cache_read(cache, whole, rk, rv)
+    cache.check_device_error()
+    att = fcp.FcpAttention(total, 128, True, 2, hq, hkv, d, backward=False)
+    o, _ = att.forward(torch.cat(q, 1), rk, rv)
+    att.check_device_error()
+    for i in range(2):
+        got = torch.cat(outs[i], 1).double().cpu().numpy()
+        a = sum(total[:i])
+        again = o[:, a:a + total[i]].double().cpu().numpy()
+        if c == "bf16":
+            assert torch.equal(rk[:, a:a + total[i]], k[i]) and torch.equal(rv[:, a:a + total[i]], v[i])
+        for h in range(hq):
+            kk, vv = (x[h * hkv // hq, a:a + total[i]].double().cpu().numpy() for x in (rk, rv))
+            ro, _, spread, _, _ = R.attend(q[i][h].double().cpu().numpy(), kk, vv, total[i], True)
+            bound = 2.0 ** -8 * (spread + np.abs(ro)) + 2.0 ** -12 * spread
+            assert (np.abs(got[h] - ro) <= bound).all(), (i, h)
+            assert (np.abs(again[h] - ro) <= bound).all(), (i, h)
+
+
+def test_the_binding_refuses_what_does_not_fit(fcp):
+    b = Batch([1, 2], [20, 30])
+    t = U.make(b)
+    cache, batch = U.handles(fcp, b, t)
+    ok = (torch.empty_like(t["q"]), torch.empty(b.hq, b.total, device="cuda"))
+    att = fcp.PagedAttention(cache, b.hq)
+    for q in (t["q"].float(), t["q"][:, :-1], t["q"][:-1], t["q"].transpose(0, 1), t["q"][..., :32].contiguous(), t["q"].cpu()):
+        with pytest.raises((TypeError, ValueError)):
+            att.forward(batch, q, *ok)
+    with pytest.raises((TypeError, ValueError)):
+        att.forward(batch, t["q"], ok[0].float(), ok[1])
+    with pytest.raises((TypeError, ValueError)):
+        att.forward(batch, t["q"], ok[0], ok[1].double())
+    with pytest.raises(ValueError):
+        fcp.PagedAttention(cache, 3)
+    for k in (t["k"].float(), t["k"][:, 1:], t["k"].transpose(1, 2), t["k"].cpu()):
+        with pytest.raises((TypeError, ValueError)):
+            fcp.cache_write(cache, batch, k, t["v"])
+        with pytest.raises((TypeError, ValueError)):
+            fcp.cache_read(cache, batch, t["k"], k)
+    with pytest.raises(ValueError):
+        fcp.CacheBatch(t["cu"][:-1], t["lens"], t["table"], 3, max_new=1)
+    with pytest.raises(ValueError):
+        fcp.CacheBatch(t["cu"], t["lens"], t["table"][:1], 3, max_new=1)
+    with pytest.raises(TypeError):
+        fcp.CacheBatch(t["cu"].long(), t["lens"], t["table"], 3, max_new=1)
+    with pytest.raises(ValueError):
+        fcp.CacheBatch(t["cu"], t["lens"], t["table"], -1, max_new=1)
+    with pytest.raises(ValueError):
+        fcp.PagedCache(2, 24, 1, 64)
+    with pytest.raises(ValueError):
+        fcp.PagedCache(2, 16, 1, 96)
+    with pytest.raises(ValueError):
+        fcp.PagedCache.wrap(t["k_pages"], t["v_pages"], torch.zeros(1, device="cuda"))
+    with pytest.raises(fcp.FcpError):  # a workspace too small for the C call
+        fcp.paged_attn(cache, batch, t["q"], *ok, att.workspace[:256])
+
+
+def test_nothing_to_do(fcp):
+    cache = fcp.PagedCache(2, 16, 1, 64, dtype=torch.float8_e4m3fn)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    none = torch.empty(1, 0, 64, dtype=torch.bfloat16, device="cuda")
+    for batch in (fcp.CacheBatch(ints([0]), torch.empty(0, dtype=torch.int32, device="cuda"),
+                                 torch.empty(0, 1, dtype=torch.int32, device="cuda"), 0, max_new=0),
+                  fcp.CacheBatch(ints([0, 0]), ints([5]), ints([[0]]), 0, max_new=0)):
+        fcp.cache_write(cache, batch, none, none)
+        fcp.cache_read(cache, batch, none, none)
+        o, lse = fcp.PagedAttention(cache, 2).forward(batch, torch.empty(2, 0, 64, dtype=torch.bfloat16, device="cuda"))
+        assert o.shape == (2, 0, 64) and lse.shape == (2, 0)
+    # rows of no sequence at all
+    q = torch.ones(2, 3, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.full_like(q, 4.0), torch.full((2, 3), 4.0, device="cuda")
+    for max_new in (1, 100):
+        batch = fcp.CacheBatch(ints([0, 0]), ints([5]), ints([[0]]), 3, max_new=max_new)
+        fcp.PagedAttention(cache, 2).forward(batch, q, o, lse)
+        assert (o == 4).all() and (lse == 4).all()
+    cache.check_device_error()
