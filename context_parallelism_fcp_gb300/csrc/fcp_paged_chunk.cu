@@ -1,9 +1,8 @@
 // Attention of chunks of new tokens over a paged cache on sm_103a (tcgen05 + TMEM).
 //
-// A unit is up to two tiles of 128 rows of one KV head. A tile is 2^t new tokens (16, 32, 64 or
-// 128, by the sequence's new tokens) times 128 / 2^t query heads of the group, head by head, so
-// that short chunks fill the tile with heads instead of padding, and every key tile loaded
-// serves all of a unit's rows. Rows are computed independently of one another: those past the
+// A unit is up to two tiles of 128 rows of one KV head, each of 16, 32, 64 or 128 new tokens of as
+// many query heads of the group as fill it, and every key tile loaded serves all of a unit's
+// rows. Rows are computed independently of one another: those past the
 // chunk or the group hold whatever is in shared memory and are not stored.
 //
 // As in the forward over a work list, S_t = Q_t K^T and O_t += P_t V run on the tensor core
@@ -374,15 +373,15 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           // Q: a tile of 128 tokens of one head is one box, others are boxes of 16 tokens of one
           // head; rows of boxes without a new token are never read for a stored row
           const ChunkRows::Shape z(seq, a.group);
-          const bool whole = z.log_tokens == 7;
           const int x = x0 + (lane >> 4), box = lane & 7, p = (lane >> 3) & 1;
-          const int tt = z.head_tiles == 1 ? x : x / z.head_tiles;
-          const int log_boxes = z.log_tokens - 4;  // boxes of one head
-          const int tok = (tt << z.log_tokens) + (box & ((1 << log_boxes) - 1)) * kQBox;
-          const int head = (x - tt * z.head_tiles) * z.heads + (box >> log_boxes);
-          const bool mine = p < C::kPanels && x < z.tiles && tok < seq.n && head < a.group && !(whole && box > 0);
-          const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-          if (lane == 0) mbar_arrive_expect_tx(bar(B_QFULL), boxes * (whole ? kTileM : kQBox) * 128);
+          const ChunkRows::Tile tile = z.tile(x, a.group);
+          const bool whole = tile.log_tokens == 7;
+          int tok, head;
+          const bool mine = p < C::kPanels && x < z.tiles && !(whole && box > 0) &&
+                            tile.row(seq, a.group, box * kQBox, tok, head);
+          const int large = __popc(__ballot_sync(0xffffffffu, mine && whole));
+          const int small = __popc(__ballot_sync(0xffffffffu, mine && !whole));
+          if (lane == 0) mbar_arrive_expect_tx(bar(B_QFULL), (large * kTileM + small * kQBox) * 128);
           __syncwarp();
           if (mine)
             tma_load_3d(sb + C::kQ + (x & 1) * C::kTileBytes + p * kPanelBytes + box * kQBox * 128, whole ? &tmQ : &tmQ16,
@@ -561,9 +560,9 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       const ChunkRows::Shape z(seq, a.group);
       const int x = 2 * T.u + t;
       if (x >= z.tiles) continue;  // a unit of one tile
-      const int tok0 = (x / z.head_tiles) << z.log_tokens, head0 = (x % z.head_tiles) * z.heads;
-      const int tok = tok0 + (r & ((1 << z.log_tokens) - 1)), head = head0 + (r >> z.log_tokens);
-      const bool mine = tok < T.n && head < a.group;
+      const ChunkRows::Tile tile = z.tile(x, a.group);
+      int tok, head;
+      const bool mine = tile.row(seq, a.group, r, tok, head);
       const bool idle = !__any_sync(0xffffffffu, mine);  // a warp without a row keeps the barriers only
       // first key that this row does not see; rows that are not stored follow the fast path
       const int lim_row = !mine ? INT32_MAX : (a.causal ? max(0, T.len - T.n + tok + 1) : T.len);
@@ -702,8 +701,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll 2
         for (int i = 0; i < 8; ++i) {
           const int rr = 4 * i + sub, rt = wrow + rr;  // row of the warp, of the tile
-          const int tk = tok0 + (rt & ((1 << z.log_tokens) - 1)), hd = head0 + (rt >> z.log_tokens);
-          if (tk >= T.n || hd >= a.group) continue;
+          int tk, hd;
+          if (!tile.row(seq, a.group, rt, tk, hd)) continue;
           const uint4 y = *reinterpret_cast<const uint4*>(stg + rr * 128 + ((e8 ^ (rr & 7)) << 4));
           if (wide)
             reinterpret_cast<uint4*>(a.part_o + (static_cast<long long>(T.slot) * P::kRows + t * kTileM + rt) * D)[c * 8 + e8] = y;

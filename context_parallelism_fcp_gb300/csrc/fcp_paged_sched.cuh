@@ -85,36 +85,61 @@ struct FewRows {
   }
 };
 
-// Chunks: a tile is 2^log_tokens new tokens of `heads` query heads (128 rows, head by head), the
-// tiles of a KV head are ordered tokens first, heads within them, and a unit is two of them.
+// Chunks: a tile is 128 rows of a KV head, 2^log_tokens new tokens of each of 128 / 2^log_tokens query
+// heads, head by head. Whole 128s of tokens make tiles of one head each, the tokens that are left
+// tiles of 128, 64, 32 or 16 tokens, so that short chunks and remainders fill tiles with heads
+// instead of padding. Tiles are ordered tokens first, heads within them, and a unit is two.
 struct ChunkRows {
   static constexpr int kRows = 2 * kTileM;
   static constexpr int kWarpPieces = 32;
   static constexpr int kOverhead = 3;
-  struct Shape {
-    int log_tokens, heads, head_tiles, token_tiles, tiles;
-    __device__ __forceinline__ Shape(const SeqShape& s, int group) {
-      log_tokens = s.n > 64 ? 7 : (s.n > 32 ? 6 : (s.n > 16 ? 5 : 4));
-      heads = kTileM >> log_tokens;
-      head_tiles = (group + heads - 1) >> (7 - log_tokens);
-      token_tiles = (s.n + (1 << log_tokens) - 1) >> log_tokens;
-      tiles = head_tiles * token_tiles;
-    }
-    // First unit whose last tile is of token tile tt or a later one.
-    __device__ __forceinline__ int first_unit(int tt) const {
-      return tt >= token_tiles ? (tiles + 1) >> 1 : (tt * head_tiles) >> 1;
-    }
-    // Length on the line of a unit whose last tile is of token tile tt.
-    __device__ __forceinline__ int length(const SeqShape& s, int tt, int causal) const {
-      return kOverhead + granules_of(key_end(s, ((tt + 1) << log_tokens) - 1, causal));
+  struct Tile {
+    int tok0, log_tokens, head0;
+    // (token, head of the group) of row r; false for rows of no token or head
+    __device__ __forceinline__ bool row(const SeqShape& s, int group, int r, int& tok, int& head) const {
+      tok = tok0 + (r & ((1 << log_tokens) - 1));
+      head = head0 + (r >> log_tokens);
+      return tok < s.n && head < group;
     }
   };
+  struct Shape {
+    int n128, full, log_rest, tiles;  // whole 128s of tokens, their tiles; the rest's tokens; all tiles
+    __device__ __forceinline__ Shape(const SeqShape& s, int group) {
+      const int rest = s.n & 127;
+      n128 = s.n >> 7;
+      full = n128 * group;
+      log_rest = rest > 64 ? 7 : (rest > 32 ? 6 : (rest > 16 ? 5 : 4));
+      tiles = full + (rest > 0 ? (group + (kTileM >> log_rest) - 1) >> (7 - log_rest) : 0);
+    }
+    __device__ __forceinline__ Tile tile(int x, int group) const {
+      if (x >= full) return Tile{n128 << 7, log_rest, (x - full) << (7 - log_rest)};
+      const int tt = x / group;
+      return Tile{tt << 7, 7, x - tt * group};
+    }
+    // Units whose last tile comes before token tile tt (n128: the rest).
+    __device__ __forceinline__ int first_unit(int tt, int group) const {
+      return tt > n128 ? (tiles + 1) >> 1 : (tt * group) >> 1;
+    }
+  };
+  // Length on the line of a unit whose last tile is of token tile tt.
+  static __device__ __forceinline__ int length(const SeqShape& s, int tt, int causal) {
+    return kOverhead + granules_of(key_end(s, (tt << 7) + 127, causal));
+  }
+  static __device__ __forceinline__ int units(const SeqShape& s, int group) { return (Shape(s, group).tiles + 1) >> 1; }
+  static __device__ __forceinline__ int tiles_of(const SeqShape& s, int group, int u) {
+    return min(2, Shape(s, group).tiles - 2 * u);
+  }
+  static __device__ __forceinline__ int end(const SeqShape& s, int group, int u, int causal) {
+    const Shape z(s, group);
+    const int x = min(2 * u + 1, z.tiles - 1);
+    return key_end(s, ((x < z.full ? x / group : z.n128) << 7) + 127, causal);
+  }
   static __device__ __forceinline__ long long head_length(const SeqShape& s, int group, int causal) {
     const Shape z(s, group);
     long long sum = 0;
-    for (int tt = 0, u = 0; tt < z.token_tiles; ++tt) {
-      const int next = z.first_unit(tt + 1);
-      sum += static_cast<long long>(next - u) * z.length(s, tt, causal);
+    for (int tt = 0, u = 0; tt <= z.n128; ++tt) {
+      const int next = z.first_unit(tt + 1, group);
+      sum += static_cast<long long>(next - u) * length(s, tt, causal);
       u = next;
     }
     return sum;
@@ -122,7 +147,7 @@ struct ChunkRows {
   static __device__ __forceinline__ int find(const SeqShape& s, int group, int causal, long long f, long long& f0) {
     const Shape z(s, group);
     for (int tt = 0, u = 0;; ++tt) {
-      const int next = z.first_unit(tt + 1), len = z.length(s, tt, causal);
+      const int next = z.first_unit(tt + 1, group), len = length(s, tt, causal);
       const long long behind = f0 + static_cast<long long>(next - u) * len;
       if (f < behind) {
         const int x = static_cast<int>(quotient(f - f0, len));
@@ -133,21 +158,10 @@ struct ChunkRows {
       u = next;
     }
   }
-  static __device__ __forceinline__ int units(const SeqShape& s, int group) { return (Shape(s, group).tiles + 1) >> 1; }
-  static __device__ __forceinline__ int tiles_of(const SeqShape& s, int group, int u) {
-    return min(2, Shape(s, group).tiles - 2 * u);
-  }
-  static __device__ __forceinline__ int end(const SeqShape& s, int group, int u, int causal) {
-    const Shape z(s, group);
-    const int x = min(2 * u + 1, z.tiles - 1);
-    return key_end(s, ((x / z.head_tiles + 1) << z.log_tokens) - 1, causal);
-  }
   static __device__ __forceinline__ bool row(const SeqShape& s, int group, int u, int r, int& tok, int& head) {
     const Shape z(s, group);
-    const int x = 2 * u + (r >> 7), rr = r & (kTileM - 1);
-    tok = ((x / z.head_tiles) << z.log_tokens) + (rr & ((1 << z.log_tokens) - 1));
-    head = (x % z.head_tiles) * z.heads + (rr >> z.log_tokens);
-    return x < z.tiles && tok < s.n && head < group;
+    const int x = 2 * u + (r >> 7);
+    return x < z.tiles && z.tile(x, group).row(s, group, r & (kTileM - 1), tok, head);
   }
 };
 
