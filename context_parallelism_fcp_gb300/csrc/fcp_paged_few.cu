@@ -50,7 +50,7 @@ constexpr int kPerSm = !kE4M3 ? 2 : (NT == 1 ? 4 : (NT == 2 ? 3 : 2));
 
 template <int D, bool kE4M3, int NT>
 struct FewCfg {
-  static constexpr int kStageBudget = (kPerSm<kE4M3, NT> == 4 ? 50 : (kPerSm<kE4M3, NT> == 3 ? 67 : 96)) * 1024;
+  static constexpr int kStageBudget = (kPerSm<kE4M3, NT> == 4 ? 50 : (kPerSm<kE4M3, NT> == 3 ? 67 : 97)) * 1024;
   static constexpr int kRowBytes = kE4M3 ? D : 2 * D;
   static constexpr int kPieces = kRowBytes / 16;               // 16-byte pieces of a row
   static constexpr int kTile = kChunk * kRowBytes;             // K or V of a chunk
@@ -137,6 +137,9 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
   __shared__ Walk<P> walk;
   __shared__ Piece shared_piece;
   __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows];
+  __shared__ uint2 shared_q[NT == 4 ? NT : 1][NT == 4 ? D / 16 : 1][32];
+  __shared__ float shared_back[32];
+  static_assert(NT != 4 || NT == kWarps, "a warp prepares each tile of Q");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this lane's fragment row (a key, or a channel; and that + 8) and its pair of columns
@@ -243,8 +246,10 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     for (int x = 0; x < C::kStages - 1; ++x) issue();
 
 
-    // Q as the second operand: tile t's row 8 t + i8
-    uint32_t q[NT][D / 16][2];
+    // Q as the second operand: tile t's row 8 t + i8. With four tiles it would take a quarter of the
+    // registers: warp t prepares tile t, and all read it from shared memory.
+    constexpr bool kSharedQ = NT == 4;
+    uint32_t q[kSharedQ ? 1 : NT][D / 16][2];
     int lim_min = p.len;  // first key that some row does not see
     if (a.causal) {
       int tok, head;
@@ -252,9 +257,9 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
       lim_min = s.len - s.n + tok + 1;
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < (kSharedQ ? 1 : NT); ++t) {
       int tok, head;
-      const bool on = P::row(s, a.group, p.u, 8 * t + i8, tok, head);
+      const bool on = P::row(s, a.group, p.u, 8 * (kSharedQ ? warp : t) + i8, tok, head);
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (static_cast<long long>(p.h * a.group + (on ? head : 0)) * a.c.total_new + s.a + (on ? tok : 0)) * D);
       if constexpr (kE4M3) {
@@ -282,20 +287,12 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
       }
     }
 
-    // The lane's columns of S^T are rows 8 t + 2 j + {0, 1}: the first key that each does not see, and
-    // the factor that brings its scores to log2 units. e4m3: Q's rows as f16 scaled by 2^(14 - e), e
-    // the largest exponent of the row, which the factor takes back.
-    int lim[NT][2];
-    float factor[NT][2];
+    // e4m3: Q's rows as f16 scaled by 2^(14 - e), e the largest exponent of the row; `back` takes the
+    // scores of row i8 of a tile to log2 units.
+    float back[kSharedQ ? 1 : NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        int tok, head;
-        const bool on = P::row(s, a.group, p.u, 8 * t + 2 * j + e, tok, head);
-        lim[t][e] = !on || !a.causal ? s.len : s.len - s.n + tok + 1;
-        factor[t][e] = a.scale_log2;
-      }
+    for (int t = 0; t < (kSharedQ ? 1 : NT); ++t) {
+      back[t] = a.scale_log2;
       if constexpr (kE4M3) {
         uint32_t top = 0;
 #pragma unroll
@@ -311,11 +308,33 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
 #pragma unroll
           for (int y = 0; y < 2; ++y)
             q[t][c][y] = pack_f16(__uint_as_float(q[t][c][y] << 16) * f, __uint_as_float(q[t][c][y] & 0xffff0000u) * f);
-        const float back = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) factor[t][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * j + e));
+        back[t] *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
       }
     }
+    if constexpr (kSharedQ) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) shared_q[warp][c][lane] = make_uint2(q[0][c][0], q[0][c][1]);
+      if (j == 0) shared_back[8 * warp + i8] = back[0];
+      __syncthreads();
+    }
+    // The lane's columns of S^T are rows 8 t + 2 j + {0, 1}: the first key that each does not see, and
+    // its factor.
+    int lim[NT][2];
+    float factor[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        int tok, head;
+        const bool on = P::row(s, a.group, p.u, 8 * t + 2 * j + e, tok, head);
+        lim[t][e] = !on || !a.causal ? s.len : s.len - s.n + tok + 1;
+        if constexpr (kSharedQ) factor[t][e] = shared_back[8 * t + 2 * j + e];
+        else factor[t][e] = kE4M3 ? __shfl_sync(0xffffffffu, back[t], 4 * (2 * j + e)) : a.scale_log2;
+      }
+    auto q_of = [&](int t, int c) -> uint2 {
+      if constexpr (kSharedQ) return shared_q[t][c][lane];
+      else return make_uint2(q[t][c][0], q[t][c][1]);
+    };
 
     // m: the maximum of a row's scores, which its weights' sum l is relative to; mo: for e4m3 that of
     // scores with V's scale, which acc is relative to. The eight lanes of a column pair share m and mo;
@@ -360,7 +379,10 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
             e4m3x4_to_f16x2(raw0[x], f[0], f[2]);
             e4m3x4_to_f16x2(raw1[x], f[1], f[3]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816h(sc[t], f, q[t][4 * c + x][0], q[t][4 * c + x][1]);
+            for (int t = 0; t < NT; ++t) {
+              const uint2 y = q_of(t, 4 * c + x);
+              mma16816h(sc[t], f, y.x, y.y);
+            }
           }
         }
       } else {
@@ -371,8 +393,9 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
           const uint32_t lo[4] = {v0.x, v1.x, v0.y, v1.y}, hi[4] = {v0.z, v1.z, v0.w, v1.w};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma16816(sc[t], lo, q[t][2 * c][0], q[t][2 * c][1]);
-            mma16816(sc[t], hi, q[t][2 * c + 1][0], q[t][2 * c + 1][1]);
+            const uint2 y0 = q_of(t, 2 * c), y1 = q_of(t, 2 * c + 1);
+            mma16816(sc[t], lo, y0.x, y0.y);
+            mma16816(sc[t], hi, y1.x, y1.y);
           }
         }
       }

@@ -57,6 +57,10 @@ __device__ __forceinline__ int granules_of(int end) { return max(1, (end + kGran
 template <int kRowsPerUnit>
 struct FewRows {
   static constexpr int kRows = kRowsPerUnit;
+  // A block's share is two granules at least: finer pieces cost more in the merge than they save (40
+  // sequences of up to 3000 keys of one KV head 27.8 us with 1, 15.5 with 2, 16.7 with 3; 10 of up to
+  // 1000, 4 KV heads: 13.7, 11.0, 11.5).
+  static constexpr int kLeastShare = 2;
   static constexpr int kWarpPieces = 8;  // of a row, up to which the merge gives a row to a warp
   static constexpr int kOverhead = 1;
   static __device__ __forceinline__ int units(const SeqShape& s, int group) {
@@ -91,6 +95,7 @@ struct FewRows {
 // instead of padding. Tiles are ordered tokens first, heads within them, and a unit is two.
 struct ChunkRows {
   static constexpr int kRows = 2 * kTileM;
+  static constexpr int kLeastShare = 1;  // 4, 6 and 8 were slower on every small batch tried
   static constexpr int kWarpPieces = 32;
   static constexpr int kOverhead = 3;
   struct Tile {
@@ -204,8 +209,8 @@ struct Walk {
 struct Shares {
   long long base;
   int rem, blocks;
-  __device__ __forceinline__ Shares(long long total, int grid)
-      : blocks(static_cast<int>(min(total, static_cast<long long>(grid)))) {
+  __device__ __forceinline__ Shares(long long total, int grid, int least)
+      : blocks(static_cast<int>(min(quotient(total + least - 1, least), static_cast<long long>(grid)))) {
     base = blocks > 0 ? quotient(total, blocks) : 0;
     rem = static_cast<int>(total - base * blocks);
   }
@@ -251,7 +256,7 @@ __device__ __forceinline__ Shares begin_walk(const AttnArgs& a, Line<kThreads>& 
     if (w == (tid >> 5)) behind += total;
     total += line.warp_sum[w];
   }
-  const Shares sh(total, gridDim.x);
+  const Shares sh(total, gridDim.x, P::kLeastShare);
   const int b = blockIdx.x;
   if (b < sh.blocks) {
     const long long f = sh.begin(b);
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Att
     __syncthreads();
     const int c = tid % kPieceLanes, x0 = tid / kPieceLanes;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int x = x0; x < count; x += kAtOnce) {
       const float4 y = reinterpret_cast<const float4*>(a.part_o + slot(x) * D)[c];
       const float f = weight[x];
