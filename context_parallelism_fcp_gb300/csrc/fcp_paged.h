@@ -12,6 +12,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <utility>
 
@@ -64,6 +65,16 @@ inline fcp_status launch_overlapped(void (*kernel)(Params...), dim3 grid, int th
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...), where);
+  return FCP_OK;
+}
+
+// cudaFuncSetAttribute for a kernel's dynamic shared memory, once for each device.
+template <class Kernel>
+inline fcp_status allow_smem(Kernel kernel, int bytes, int device, std::atomic<uint64_t>& done, const char* where) {
+  const uint64_t bit = 1ull << (device & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return FCP_OK;
+  FCP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), where);
+  done.fetch_or(bit, std::memory_order_relaxed);
   return FCP_OK;
 }
 

@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 }
 
 template <int D, bool kE4M3>
-fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s) {
+fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaStream_t s) {
   using C = Cfg<D>;
   CUtensorMap mq, mq16, mk = {}, mv = {};
   if (const fcp_status st = make_bf16_map(&mq, a.q, hq, a.c.total_new, D, kTileM); st != FCP_OK) return st;
@@ -751,8 +751,10 @@ fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s)
   }
   const int blocks = std::min(n_sm, kMaxChunkBlocks);
   set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
-  FCP_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes),
-               "paged chunk smem attribute");
+  static std::atomic<uint64_t> allowed{0};
+  if (const fcp_status st = allow_smem(chunk_kernel<D, kE4M3>, C::kSmemBytes, dev, allowed, "paged chunk smem attribute");
+      st != FCP_OK)
+    return st;
   if (const fcp_status st = launch_overlapped(chunk_kernel<D, kE4M3>, dim3(blocks), kThreads<kE4M3>, C::kSmemBytes, s,
                                               "paged chunk launch", mq, mq16, mk, mv, a);
       st != FCP_OK)
@@ -762,10 +764,11 @@ fcp_status launch(AttnArgs a, void* workspace, int n_sm, int hq, cudaStream_t s)
 
 }  // namespace
 
-fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int n_sm, cudaStream_t s) {
+fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int dev, int n_sm,
+                              cudaStream_t s) {
   if (dtype == FCP_CACHE_E4M3)
-    return d == 128 ? launch<128, true>(a, workspace, n_sm, hq, s) : launch<64, true>(a, workspace, n_sm, hq, s);
-  return d == 128 ? launch<128, false>(a, workspace, n_sm, hq, s) : launch<64, false>(a, workspace, n_sm, hq, s);
+    return d == 128 ? launch<128, true>(a, workspace, dev, n_sm, hq, s) : launch<64, true>(a, workspace, dev, n_sm, hq, s);
+  return d == 128 ? launch<128, false>(a, workspace, dev, n_sm, hq, s) : launch<64, false>(a, workspace, dev, n_sm, hq, s);
 }
 
 }  // namespace fcp

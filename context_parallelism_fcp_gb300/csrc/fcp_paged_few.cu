@@ -583,22 +583,30 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
   }
 }
 
-fcp_status sm_count(int* n) {
-  int dev = 0;
-  FCP_CUDA_TRY(cudaGetDevice(&dev), "paged attention device");
-  FCP_CUDA_TRY(cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev), "paged attention SM count");
+// The current device and its number of SMs, which does not change.
+fcp_status this_device(int* dev, int* n_sm) {
+  static std::atomic<int> known[64];
+  FCP_CUDA_TRY(cudaGetDevice(dev), "paged attention device");
+  if (*dev < 0 || *dev >= 64) return FCP_ERR_UNSUPPORTED;
+  *n_sm = known[*dev].load(std::memory_order_relaxed);
+  if (*n_sm == 0) {
+    FCP_CUDA_TRY(cudaDeviceGetAttribute(n_sm, cudaDevAttrMultiProcessorCount, *dev), "paged attention SM count");
+    known[*dev].store(*n_sm, std::memory_order_relaxed);
+  }
   return FCP_OK;
 }
 
 template <int D, bool kE4M3, int NT>
-fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaStream_t s) {
+fcp_status launch_few(AttnArgs a, void* workspace, int dev, int n_sm, int max_new, cudaStream_t s) {
   using C = FewCfg<D, kE4M3, NT>;
   using P = FewRows<8 * NT>;
   constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * (D + 4) * 4);
   const int blocks = std::min(kPerSm<kE4M3, NT> * n_sm, kMaxBlocks);
   set_workspace<P>(a, workspace, D, kMaxBlocks);
-  FCP_CUDA_TRY(cudaFuncSetAttribute(few_kernel<D, kE4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-               "paged attention smem attribute");
+  static std::atomic<uint64_t> allowed{0};
+  if (const fcp_status st = allow_smem(few_kernel<D, kE4M3, NT>, kSmem, dev, allowed, "paged attention smem attribute");
+      st != FCP_OK)
+    return st;
   if (const fcp_status st = launch_overlapped(few_kernel<D, kE4M3, NT>, dim3(blocks), kFewThreads, kSmem, s,
                                               "paged attention launch", a);
       st != FCP_OK)
@@ -613,15 +621,15 @@ fcp_status launch_few(AttnArgs a, void* workspace, int n_sm, int max_new, cudaSt
 
 template <int D>
 fcp_status launch_attn(const AttnArgs& a, int dtype, int hq, int max_new, void* workspace, cudaStream_t s) {
-  int n_sm = 0;
-  if (const fcp_status st = sm_count(&n_sm); st != FCP_OK) return st;
+  int dev = 0, n_sm = 0;
+  if (const fcp_status st = this_device(&dev, &n_sm); st != FCP_OK) return st;
   const long long rows = static_cast<long long>(max_new) * a.group;
-  if (rows > 32) return launch_paged_chunk(a, dtype, D, hq, workspace, n_sm, s);
+  if (rows > 32) return launch_paged_chunk(a, dtype, D, hq, workspace, dev, n_sm, s);
   const bool e = dtype == FCP_CACHE_E4M3;
   auto* launch = rows <= 8    ? (e ? launch_few<D, true, 1> : launch_few<D, false, 1>)
                  : rows <= 16 ? (e ? launch_few<D, true, 2> : launch_few<D, false, 2>)
                               : (e ? launch_few<D, true, 4> : launch_few<D, false, 4>);
-  return launch(a, workspace, n_sm, max_new, s);
+  return launch(a, workspace, dev, n_sm, max_new, s);
 }
 
 }  // namespace

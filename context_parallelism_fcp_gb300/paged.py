@@ -158,19 +158,22 @@ def paged_attn(cache: PagedCache, batch: CacheBatch, q, o, lse, workspace, causa
     must be in the cache. workspace: a CUDA uint8 tensor of fcp_paged_attn_workspace_bytes(D)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [Hq, total_new, D]")
-    _attend(cache, batch, q, o, lse, workspace, causal, q.shape[0], stream)
+    if workspace.get_device() != cache._index:
+        raise ValueError("the workspace and the cache must be on one device")
+    _attend(lib().fcp_paged_attn, cache, batch, q, o, lse, workspace.data_ptr(), workspace.nbytes, 1 if causal else 0,
+            q.shape[0], stream)
 
 
-def _attend(cache, batch, q, o, lse, workspace, causal, hq, stream) -> None:
+def _attend(fn, cache, batch, q, o, lse, workspace, workspace_bytes, causal, hq, stream) -> None:
     index = cache._index
-    if batch._index != index or workspace.get_device() != index:
-        raise ValueError("the batch, the workspace and the cache must be on one device")
+    if batch._index != index:
+        raise ValueError("the batch and the cache must be on one device")
     shape = (hq, batch.total_new, cache.head_dim)
     _want(q, torch.bfloat16, shape, index, "q")
     _want(o, torch.bfloat16, shape, index, "o")
     _want(lse, torch.float32, shape[:2], index, "lse")
-    status = lib().fcp_paged_attn(cache._ref, batch._ref, q.data_ptr(), hq, 1 if causal else 0, o.data_ptr(),
-                                  lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _here(index, stream))
+    status = fn(cache._ref, batch._ref, q.data_ptr(), hq, causal, o.data_ptr(), lse.data_ptr(), workspace,
+                workspace_bytes, _here(index, stream))
     if status:
         _check(status, "fcp_paged_attn")
 
@@ -185,6 +188,8 @@ class PagedAttention:
         self.cache, self.hq, self.causal = cache, int(hq), bool(causal)
         self.workspace = torch.empty(int(lib().fcp_paged_attn_workspace_bytes(cache.head_dim)), dtype=torch.uint8,
                                      device=cache.device)
+        self._call = lib().fcp_paged_attn, cache
+        self._last = self.workspace.data_ptr(), self.workspace.nbytes, 1 if causal else 0, self.hq
 
     def forward(self, batch: CacheBatch, q, o=None, lse=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """(o, lse) of the batch's new tokens; rows that belong to no sequence are left as they
@@ -193,5 +198,5 @@ class PagedAttention:
             o = torch.empty_like(q)
         if lse is None:
             lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        _attend(self.cache, batch, q, o, lse, self.workspace, self.causal, self.hq, stream)
+        _attend(*self._call, batch, q, o, lse, *self._last, stream)
         return o, lse
