@@ -24,10 +24,11 @@ fcp_status paged_args(const fcp_cache* c, const fcp_cache_batch* b, PagedArgs* o
   if (c->dtype != FCP_CACHE_BF16 && c->dtype != FCP_CACHE_E4M3) return FCP_ERR_INVALID;
   if (c->head_dim != 64 && c->head_dim != 128) return FCP_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return FCP_ERR_UNSUPPORTED;
-  if (static_cast<long long>(b->max_pages) * c->page_size > INT32_MAX) return FCP_ERR_UNSUPPORTED;
+  if (static_cast<long long>(b->max_pages) * c->page_size > 1ll << 30) return FCP_ERR_UNSUPPORTED;
   if (b->n_seqs > 65536) return FCP_ERR_UNSUPPORTED;
   if (c->status == nullptr || !aligned16(c->status)) return FCP_ERR_INVALID;
   if (b->n_seqs > 0 && (!b->cu_new || !b->lens || (b->max_pages > 0 && !b->block_table))) return FCP_ERR_INVALID;
+  if (!aligned4(b->cu_new) || !aligned4(b->lens) || !aligned4(b->block_table)) return FCP_ERR_INVALID;
   if (c->n_pages > 0) {
     if (!c->k_pages || !c->v_pages || !aligned16(c->k_pages) || !aligned16(c->v_pages)) return FCP_ERR_INVALID;
     if (c->dtype == FCP_CACHE_E4M3 &&

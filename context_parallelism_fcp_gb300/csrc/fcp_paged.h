@@ -43,6 +43,8 @@ struct PagedArgs {
   int32_t* status;
 };
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 fcp_status paged_args(const fcp_cache* cache, const fcp_cache_batch* batch, PagedArgs* out);
 
 // The cache's kernels are launched so that they may start while the kernel before them in the

@@ -649,7 +649,7 @@ extern "C" fcp_status fcp_paged_attn(const fcp_cache* cache, const fcp_cache_bat
   if (const fcp_status st = paged_args(cache, batch, &a.c); st != FCP_OK) return st;
   if (hq <= 0 || hq % cache->hkv != 0) return FCP_ERR_INVALID;
   if (a.c.total_new == 0 || a.c.n_seqs == 0) return FCP_OK;
-  if (!q || !o || !lse || !workspace || !aligned16(q) || !aligned16(o) ||
+  if (!q || !o || !lse || !workspace || !aligned16(q) || !aligned16(o) || !aligned4(lse) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return FCP_ERR_INVALID;
   if (workspace_bytes < fcp_paged_attn_workspace_bytes(cache->head_dim)) return FCP_ERR_INVALID;

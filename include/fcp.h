@@ -401,7 +401,7 @@ typedef struct {
  * 256 * 2^120 is past bf16's range) and the scale byte is k + 127; a row that holds an infinity or NaN gets byte 255 and codes of zero. New tokens
  * whose position is negative (n_i > lens[i]) are left out. Errors: FCP_ERR_INVALID (nulls,
  * negative sizes, misaligned or missing buffers, an unknown dtype), FCP_ERR_UNSUPPORTED (D,
- * page_size, more than 65536 sequences or 2^31 - 1 positions), FCP_ERR_CUDA. */
+ * page_size, more than 65536 sequences or 2^30 positions in a block table's row), FCP_ERR_CUDA. */
 fcp_status fcp_cache_write(const fcp_cache* cache, const fcp_cache_batch* batch, const void* k, const void* v,
                            void* stream);
 
@@ -425,8 +425,9 @@ size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
  * Rows of the pages past a sequence's length may hold anything, NaN included; a NaN or infinity
  * that a bf16 cache holds in V at a position of the sequence itself may reach the rows of the
  * same batch that come before it. Sums, maxima and the softmax's statistics are float32; P is
- * rounded to bf16 for the product with V. Results do not depend on timing: no atomics are
- * used. workspace: fcp_paged_attn_workspace_bytes, 256-byte aligned, its contents need not be
+ * rounded to bf16 (f16 in the kernel for few rows of an e4m3 cache) for the product with V.
+ * Results do not depend on timing: no atomics are used. o and lse must not overlap the inputs.
+ * workspace: fcp_paged_attn_workspace_bytes, 256-byte aligned, its contents need not be
  * kept or cleared; calls whose work may overlap need one each. Errors: FCP_ERR_INVALID (also
  * hq % hkv, a small or misaligned workspace), FCP_ERR_UNSUPPORTED and FCP_ERR_CUDA as
  * fcp_cache_write. */

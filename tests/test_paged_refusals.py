@@ -28,7 +28,8 @@ BAD = [
     (dict(cu_new=None), INVALID), (dict(lens=None), INVALID), (dict(block_table=None), INVALID),
     (dict(head_dim=96), UNSUPPORTED), (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED),
     (dict(page_size=8192), UNSUPPORTED), (dict(n_seqs=65537), UNSUPPORTED),
-    (dict(page_size=4096, max_pages=1 << 20), UNSUPPORTED),
+    (dict(page_size=4096, max_pages=1 << 20), UNSUPPORTED), (dict(page_size=4096, max_pages=(1 << 18) + 1), UNSUPPORTED),
+    (dict(cu_new=P + 2), INVALID), (dict(lens=P + 1), INVALID), (dict(block_table=P + 3), INVALID),
 ]
 
 
@@ -52,7 +53,7 @@ def test_nulls_and_misaligned_buffers(fcp):
         assert L.fcp_cache_read(c, b, k, v, None) == INVALID
     good = [c, b, P, 4, 1, P, P, P, ws, None]
     for at, value in ((0, None), (1, None), (2, None), (2, P + 8), (3, 0), (3, 3), (3, -2), (5, None), (5, P + 8),
-                      (6, None), (7, None), (7, P + 16), (8, ws - 1)):
+                      (6, None), (6, P + 2), (7, None), (7, P + 16), (8, ws - 1)):
         args = list(good)
         args[at] = value
         assert L.fcp_paged_attn(*args) == INVALID, (at, value)
