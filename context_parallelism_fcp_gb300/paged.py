@@ -8,6 +8,7 @@ and all the work is done by the library's kernels, on the caller's stream.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from typing import Optional, Tuple
 
 import torch
@@ -158,6 +159,7 @@ def paged_attn(cache: PagedCache, batch: CacheBatch, q, o, lse, workspace, causa
     must be in the cache. workspace: a CUDA uint8 tensor of fcp_paged_attn_workspace_bytes(D)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [Hq, total_new, D]")
+    _need(workspace, torch.uint8, None, "workspace")
     if workspace.get_device() != cache._index:
         raise ValueError("the workspace and the cache must be on one device")
     _attend(lib().fcp_paged_attn, cache, batch, q, o, lse, workspace.data_ptr(), workspace.nbytes, 1 if causal else 0,
@@ -193,10 +195,13 @@ class PagedAttention:
 
     def forward(self, batch: CacheBatch, q, o=None, lse=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """(o, lse) of the batch's new tokens; rows that belong to no sequence are left as they
-        were in the buffers given, and are undefined in those that are allocated here."""
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        were in the buffers given, and are undefined in those that are allocated here (as memory
+        of the stream that the call runs on)."""
+        if o is None or lse is None:
+            if stream is not None and not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream(stream), device=q.device)
+            with nullcontext() if stream is None else torch.cuda.stream(stream):
+                o = torch.empty_like(q) if o is None else o
+                lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse is None else lse
         _attend(*self._call, batch, q, o, lse, *self._last, stream)
         return o, lse

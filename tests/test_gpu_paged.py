@@ -536,3 +536,35 @@ def test_nothing_to_do(fcp):
         fcp.PagedAttention(cache, 2).forward(batch, q, o, lse)
         assert (o == 4).all() and (lse == 4).all()
     cache.check_device_error()
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_outputs_allocated_for_another_stream_are_its_own(fcp, raw):
+    """Memory that the current stream may still be using (freed, its kernels perhaps running) does
+    not become the output of a call on another stream."""
+    b = Batch([1, 2], [20, 30], hq=64, hkv=2, d=128)
+    t = U.make(b)
+    cache, batch = U.handles(fcp, b, t)
+    att = fcp.PagedAttention(cache, b.hq)
+    want = att.forward(batch, t["q"])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(t["q"]) for _ in range(8)] + [torch.empty(b.hq, b.total, device="cuda") for _ in range(8)]
+    addresses = {x.data_ptr() for x in freed}
+    del freed
+    got = att.forward(batch, t["q"], stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert not addresses & {x.data_ptr() for x in got}
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_a_workspace_of_another_kind_is_refused(fcp):
+    b = Batch([1], [20])
+    t = U.make(b)
+    cache, batch = U.handles(fcp, b, t)
+    out = torch.empty_like(t["q"]), torch.empty(b.hq, b.total, device="cuda")
+    n = fcp.lib().fcp_paged_attn_workspace_bytes(b.d)
+    for ws in (torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2], torch.empty(n, dtype=torch.uint8),
+               torch.empty(n, dtype=torch.int8, device="cuda")):
+        with pytest.raises((TypeError, ValueError)):
+            fcp.paged_attn(cache, batch, t["q"], *out, ws)
