@@ -25,7 +25,7 @@ fcp_status paged_args(const fcp_cache* c, const fcp_cache_batch* b, PagedArgs* o
   if (c->head_dim != 64 && c->head_dim != 128) return FCP_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return FCP_ERR_UNSUPPORTED;
   if (static_cast<long long>(b->max_pages) * c->page_size > 1ll << 30) return FCP_ERR_UNSUPPORTED;
-  if (b->n_seqs > 65536) return FCP_ERR_UNSUPPORTED;
+  if (b->n_seqs > 65536 || b->total_new > 1 << 30) return FCP_ERR_UNSUPPORTED;
   if (c->status == nullptr || !aligned16(c->status)) return FCP_ERR_INVALID;
   if (b->n_seqs > 0 && (!b->cu_new || !b->lens || (b->max_pages > 0 && !b->block_table))) return FCP_ERR_INVALID;
   if (!aligned4(b->cu_new) || !aligned4(b->lens) || !aligned4(b->block_table)) return FCP_ERR_INVALID;
@@ -74,7 +74,7 @@ __device__ __forceinline__ void find_places(const PagedArgs& p, int t0, TokenPla
   // rest in memory, so that the dependent reads are few however many sequences there are.
   const int step = (p.n_seqs + kCoarse) / kCoarse;
   const int n_coarse = (p.n_seqs + step) / step;  // offsets 0, step, ... <= n_seqs
-  for (int j = threadIdx.x; j < n_coarse; j += kMoveThreads) coarse[j] = __ldg(p.cu + j * step);
+  for (int j = threadIdx.x; j < n_coarse; j += kMoveThreads) coarse[j] = load(p.cu + j * step);
   __syncthreads();
   if (threadIdx.x < kMoveTokens) {
     const int t = t0 + threadIdx.x;
@@ -88,14 +88,14 @@ __device__ __forceinline__ void find_places(const PagedArgs& p, int t0, TokenPla
       int i = lo * step, e = min(i + step, p.n_seqs);
       while (e - i > 1) {
         const int mid = (i + e) >> 1;
-        if (__ldg(p.cu + mid) <= t) i = mid; else e = mid;
+        if (load(p.cu + mid) <= t) i = mid; else e = mid;
       }
       if (i < p.n_seqs) {
         const SeqShape s = seq_shape(p, i, true);
         if (t >= s.a && t < s.a + s.n) {
           const int pos = s.len - s.n + (t - s.a);
           if (pos >= 0) {
-            const int page = __ldg(p.table + static_cast<long long>(i) * p.max_pages + (pos >> p.page_shift));
+            const int page = load(p.table + static_cast<long long>(i) * p.max_pages + (pos >> p.page_shift));
             if (page >= 0 && page < p.n_pages) {
               r.page = page;
               r.off = pos & ((1 << p.page_shift) - 1);
@@ -236,7 +236,6 @@ fcp_status launch_move(const PagedArgs& p, int dtype, void* k, void* v, cudaStre
   int heads = p.hkv;
   while (heads > 1 && 2ll * bx * ((p.hkv + heads - 1) / heads) < 1216) heads = (heads + 1) / 2;
   const dim3 grid(bx, static_cast<unsigned>((p.hkv + heads - 1) / heads), 2);
-  if (grid.y > 65535u) return FCP_ERR_UNSUPPORTED;
   uint4* pk = static_cast<uint4*>(k);
   uint4* pv = static_cast<uint4*>(v);
   auto* kernel = dtype == FCP_CACHE_E4M3 ? move_kernel<D, true, kRead> : move_kernel<D, false, kRead>;

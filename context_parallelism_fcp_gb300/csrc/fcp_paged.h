@@ -53,6 +53,30 @@ fcp_status paged_args(const fcp_cache* cache, const fcp_cache_batch* batch, Page
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Such a kernel is resident while what it reads may still be written, so nothing is read through
+// the path for memory that stays the same as long as a kernel lives; and these loads keep their
+// place behind the wait.
+__device__ __forceinline__ int load(const int32_t* p) {
+  int x;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint32_t load(const uint8_t* p) {
+  uint32_t x;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint2 load(const uint2* p) {
+  uint2 x;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint4 load(const uint4* p) {
+  uint4 x;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+
 template <class... Params, class... Args>
 inline fcp_status launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
                                     const char* where, Args&&... args) {
@@ -86,7 +110,7 @@ struct SeqShape {
   int32_t a, n, len;
 };
 __device__ __forceinline__ SeqShape seq_shape(const PagedArgs& p, int i, bool report) {
-  const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1), len = __ldg(p.lens + i);
+  const int a = load(p.cu + i), b = load(p.cu + i + 1), len = load(p.lens + i);
   const bool ok = a >= 0 && b >= a && b <= p.total_new && len >= 0 &&
                   len <= (static_cast<long long>(p.max_pages) << p.page_shift);
   if (!ok && report) atomicCAS(p.status, 0, kErrCacheBatch);

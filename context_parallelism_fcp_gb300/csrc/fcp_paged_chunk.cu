@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         auto first_key = [&](int g) -> int { return (t.kt0 + (g >> 4) - J0) * kTileN + 16 * (g & 7); };
         auto lookup = [&](int g) -> int {  // the block table's entry for group g; -1: nothing to read
           const int key0 = first_key(g);
-          return g < g_end && key0 < t.len ? __ldg(table + (key0 >> a.c.page_shift)) : -1;
+          return g < g_end && key0 < t.len ? load(table + (key0 >> a.c.page_shift)) : -1;
         };
         uint2 raw[4][C::kPanels];  // of rows that are not there: anything
         const uint8_t* src = nullptr;
@@ -238,13 +238,13 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           src = (is_v ? a.c.v_pages : a.c.k_pages) + (row + r0) * D + c * 8;
           held = in ? t.len - key0 - r0 : 0;
           byte = 256u;
-          if (in && key0 + (lane & 15) < t.len) byte = __ldg((is_v ? a.c.v_scales : a.c.k_scales) + row + (lane & 15));
+          if (in && key0 + (lane & 15) < t.len) byte = load((is_v ? a.c.v_scales : a.c.k_scales) + row + (lane & 15));
         };
-        auto load = [&](int x) {
+        auto load_rows = [&](int x) {
           if (4 * x < held) {
 #pragma unroll
             for (int p = 0; p < C::kPanels; ++p)
-              raw[x][p] = __ldg(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
+              raw[x][p] = load(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
           }
         };
 #pragma unroll
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           for (int p = 0; p < C::kPanels; ++p) raw[x][p] = make_uint2(0u, 0u);
         aim(g1, lookup(g1));
 #pragma unroll
-        for (int x = 0; x < 4; ++x) load(x);
+        for (int x = 0; x < 4; ++x) load_rows(x);
         int page2 = lookup(g2);
         while (g1 < g_end) {
           const int J = g1 >> 4, s = J & 1;  // the block's key tile
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll 1
               for (int p = 0; p < C::kPanels; ++p) {
                 uint2 codes = make_uint2(0u, 0u);
-                if (4 * x < held) codes = __ldg(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
+                if (4 * x < held) codes = load(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
                 uint32_t r[4];
                 code_bits(codes, r);
                 times(r, a1);
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
               times(r, f);
               if (!large) *piece(x, p) = make_uint4(r[0], r[1], r[2], r[3]);
             }
-            load(x);  // of the next group
+            load_rows(x);  // of the next group
           }
           fence_proxy_async_smem();
           mbar_arrive_warp(bar((is_v ? B_VFULL : B_KFULL) + s));
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           auto lookup = [&](int kt) -> int {
             const int key = kt * kTileN + lane * rows;
             if (lane >= n_boxes || kt >= kt1 || key >= seq.len) return -1;
-            const int page = __ldg(table + (key >> a.c.page_shift));
+            const int page = load(table + (key >> a.c.page_shift));
             if (page >= 0 && page < a.c.n_pages) return page;
             atomicCAS(err, 0, kErrCachePage);
             return -1;
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           m_used = m_new;
         }
         const float mb = (m_used == -INFINITY) ? 0.f : m_used;
-        // P (rounded to bf16: off by 2^-9 of itself at most) in two halves of 64 keys, each handed
+        // P (rounded to bf16: off by 2^-8 of itself at most) in two halves of 64 keys, each handed
         // to the MMA warp as soon as it is stored
         float rowsum = 0.f;
 #pragma unroll

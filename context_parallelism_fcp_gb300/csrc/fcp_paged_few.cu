@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     const int key0 = k0 + kChunk * warp;
     auto entries = [&](int batch) -> int {
       const int key = key0 + (32 * batch + lane) * (kChunk * kWarps);
-      return key < kend ? __ldg(table + (key >> a.c.page_shift)) : -1;
+      return key < kend ? load(table + (key >> a.c.page_shift)) : -1;
     };
     int pages = entries(0), pages_next = entries(1);
     int n_issued = 0, issue_stage = 0;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
         for (int c = 0; c < D / 64; ++c)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint4 v = on ? __ldg(src + c * 8 + 2 * j + y) : make_uint4(0, 0, 0, 0);
+            const uint4 v = on ? load(src + c * 8 + 2 * j + y) : make_uint4(0, 0, 0, 0);
             q[t][4 * c + 2 * y][0] = v.x;
             q[t][4 * c + 2 * y][1] = v.y;
             q[t][4 * c + 2 * y + 1][0] = v.z;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
         // 32 channels: lane j has channels 8 j .. 8 j + 7, in products 0-1 of the 32
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          const uint4 v = on ? __ldg(src + c * 4 + j) : make_uint4(0, 0, 0, 0);
+          const uint4 v = on ? load(src + c * 4 + j) : make_uint4(0, 0, 0, 0);
           q[t][2 * c][0] = v.x;
           q[t][2 * c][1] = v.y;
           q[t][2 * c + 1][0] = v.z;

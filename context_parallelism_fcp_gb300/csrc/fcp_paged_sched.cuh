@@ -207,19 +207,18 @@ struct Walk {
 // The blocks' shares of a line of length `total`: block b < blocks takes [begin(b), begin(b + 1)),
 // which is not empty (blocks is less than the grid where the line is shorter).
 struct Shares {
-  long long base;
+  long long total, base;
   int rem, blocks;
-  __device__ __forceinline__ Shares(long long total, int grid, int least)
-      : blocks(static_cast<int>(min(quotient(total + least - 1, least), static_cast<long long>(grid)))) {
+  __device__ __forceinline__ Shares(long long line, int grid, int least)
+      : total(line), blocks(static_cast<int>(min(quotient(total + least - 1, least), static_cast<long long>(grid)))) {
     base = blocks > 0 ? quotient(total, blocks) : 0;
     rem = static_cast<int>(total - base * blocks);
   }
+  // floor(total * b / blocks)
   __device__ __forceinline__ long long begin(int b) const { return base * b + rem * b / blocks; }
-  // The block that takes place f.
+  // The block that takes place f: the last b with total * b / blocks < f + 1.
   __device__ __forceinline__ int owner(long long f) const {
-    int b = static_cast<int>(quotient(f, base + 1));
-    while (begin(b + 1) <= f) ++b;
-    return b;
+    return static_cast<int>(quotient((f + 1) * blocks - 1, total));
   }
 };
 

@@ -358,13 +358,17 @@ fcp_status fcp_reshuffle(const fcp_plan* plan, const void* d_plan, const void* s
  * pages of page_size tokens:
  *   k_pages, v_pages   [n_pages, Hkv, page_size, D], bf16 or e4m3
  *   k_scales, v_scales [n_pages, Hkv, page_size] bytes, e4m3 caches only: the row (token, head)
- *                      stands for code * 2^(byte - 127); byte 255 makes it NaN
+ *                      stands for code * 2^(byte - 127); byte 255 makes it NaN. Codes 0x7f and
+ *                      0xff are never written and must not be in pages filled otherwise, at
+ *                      positions of a sequence (they would read as NaN or as 480)
  * all contiguous and 16-byte aligned. page_size is a power of two, 16 to 4096; D is 64 or 128.
- * status is one int32 on the device (16-byte aligned, zero at first), the error word of every call that uses
- * the cache; read and clear it with fcp_device_error. 0x50: a sequence's offsets or length do
+ * status is one int32 on the device (16-byte aligned, zero at first), the error word of every
+ * call that uses the cache; read and clear it with fcp_device_error. 0x50: a sequence's offsets or length do
  * not fit the batch (its rows are left as they were); 0x51: a block-table entry that was needed
  * lies outside [0, n_pages) (a write or read leaves its row out, attention counts its keys as
  * zeros). Neither stops the rest of the batch, and nothing outside the buffers is touched.
+ * 0x60 to 0x6f: a wait inside the attention ran out of its 2 seconds, 0x01: its shared memory
+ * was misaligned; o and lse are then incomplete.
  *
  * A batch brings new tokens for n_seqs sequences, packed over total_new rows as everywhere in
  * this library (tensors are [heads, total_new, D]): sequence i owns rows [cu_new[i],
@@ -398,10 +402,12 @@ typedef struct {
 /* Write the new tokens' K and V (bf16 [Hkv, total_new, D]) into their pages. An e4m3 cache
  * quantises each row: with k the smallest integer >= -126 such that max|x| <= 448 * 2^k (k = 0
  * for a row of zeros), the codes are x * 2^-k rounded to nearest even (at most 240 where k = 120:
- * 256 * 2^120 is past bf16's range) and the scale byte is k + 127; a row that holds an infinity or NaN gets byte 255 and codes of zero. New tokens
- * whose position is negative (n_i > lens[i]) are left out. Errors: FCP_ERR_INVALID (nulls,
+ * 256 * 2^120 is past bf16's range) and the scale byte is k + 127; a row that holds an
+ * infinity or NaN gets byte 255 and codes of zero. New tokens whose position is negative
+ * (n_i > lens[i]) are left out. Errors: FCP_ERR_INVALID (nulls,
  * negative sizes, misaligned or missing buffers, an unknown dtype), FCP_ERR_UNSUPPORTED (D,
- * page_size, more than 65536 sequences or 2^30 positions in a block table's row), FCP_ERR_CUDA. */
+ * page_size, more than 65536 sequences, 2^30 new tokens or 2^30 positions in a block table's
+ * row), FCP_ERR_CUDA. */
 fcp_status fcp_cache_write(const fcp_cache* cache, const fcp_cache_batch* batch, const void* k, const void* v,
                            void* stream);
 

@@ -29,7 +29,7 @@ BAD = [
     (dict(head_dim=96), UNSUPPORTED), (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED),
     (dict(page_size=8192), UNSUPPORTED), (dict(n_seqs=65537), UNSUPPORTED),
     (dict(page_size=4096, max_pages=1 << 20), UNSUPPORTED), (dict(page_size=4096, max_pages=(1 << 18) + 1), UNSUPPORTED),
-    (dict(cu_new=P + 2), INVALID), (dict(lens=P + 1), INVALID), (dict(block_table=P + 3), INVALID),
+    (dict(total_new=(1 << 30) + 1), UNSUPPORTED), (dict(cu_new=P + 2), INVALID), (dict(lens=P + 1), INVALID), (dict(block_table=P + 3), INVALID),
 ]
 
 
