@@ -77,7 +77,7 @@ __device__ __forceinline__ uint4 load(const uint4* p) {
   return x;
 }
 
-template <class... Params, class... Args>
+template <int kCluster = 1, class... Params, class... Args>
 inline fcp_status launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
                                     const char* where, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
@@ -85,11 +85,14 @@ inline fcp_status launch_overlapped(void (*kernel)(Params...), dim3 grid, int th
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = kCluster > 1 ? 2 : 1;
   FCP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...), where);
   return FCP_OK;
 }

@@ -198,11 +198,17 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       // ---------------------------------------------------------- loaders (e4m3)
       // The work is 16-row groups, each in one page: K's eight of a tile, V's eight, the next tile's.
       // They go round the six warps; the two that share their scheduler with no other loader take a
-      // sixth turn in every 32. A warp's next group is on its way while it converts one, and the
-      // page of the one after is looked up (and only looked at when its turn has come: a check at
-      // once would wait for the lookup). Lane l has codes [8 (l % 8), + 8) of each 64 channels of rows
-      // l / 8 + 4 x: a 16-byte piece of bf16 each, eight lanes to a 128-byte line.
-      const int r0 = lane >> 3, c = lane & 7;
+      // sixth turn in every 32. A warp fetches its next group as soon as it has handed one over, and
+      // looks up the page of the one after (and only looks at it when its turn has come: a check at
+      // once would wait for the lookup). Fetching row by row between a group's conversions instead, as
+      // registers became free, put loads in front of the fence that hands the group over: 2048 tokens
+      // over 32768 keys took 1980 us instead of 1920. A second group in flight, in registers, took 2515:
+      // the code is twice as long and no longer stays in the instruction cache beside the softmax's;
+      // in shared memory it took 2225, whose bandwidth the matrix instructions need.
+      // A lane has 16 codes, two 16-byte pieces of bf16, of rows r0 + kStep x. Eight lanes store at a
+      // time: four of an even and four of an odd row, whose swizzle puts them on different banks.
+      constexpr int kLanes = D / 16, kStep = 32 / kLanes, kLoads = 16 / kStep;
+      const int c = lane % kLanes, r0 = D == 128 ? (lane >> 3) ^ ((lane >> 2) & 1) : lane / kLanes;
       const int page_mask = (1 << a.c.page_shift) - 1;
       const int order = warp == 12 ? 0 : (warp == 13 ? 1 : (warp < 12 ? warp - 8 : warp - 10));
       int turn = 0;
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       };
       bool ok = true;
       int J0 = 0;                            // key tiles before this unit
-      int g1 = order, g2 = g1 + step();      // groups held: converted next, and after that
+      int g1 = order, g2 = g1 + step();      // the group held, and the next
       for (int v = 0; ok; ++v) {
         const Unit t = next_unit(v, kErrPagedWait + 1);
         if (t.valid <= 0) break;
@@ -226,34 +232,26 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           const int key0 = first_key(g);
           return g < g_end && key0 < t.len ? load(table + (key0 >> a.c.page_shift)) : -1;
         };
-        uint2 raw[4][C::kPanels];  // of rows that are not there: anything
+        uint4 raw[kLoads];  // of rows that are not there: anything
         const uint8_t* src = nullptr;
-        int held = 0;        // rows r0 + 4 x with 4 x below it are there
+        int held = 0;        // rows r0 + kStep x with kStep x below it are there
         uint32_t byte = 0;   // lane l: scale of row l % 16; 256: not there
-        auto aim = [&](int g, int page) {
+        auto fetch = [&](int g, int page) {
           const int key0 = first_key(g);
           const bool is_v = (g & 8) != 0, in = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages);
           if (!in && g < g_end && key0 < t.len) atomicCAS(err, 0, kErrCachePage);
           const long long row = in ? page_row(a.c, page, t.h) + (key0 & page_mask) : 0;
-          src = (is_v ? a.c.v_pages : a.c.k_pages) + (row + r0) * D + c * 8;
+          src = (is_v ? a.c.v_pages : a.c.k_pages) + (row + r0) * D + c * 16;
           held = in ? t.len - key0 - r0 : 0;
           byte = 256u;
           if (in && key0 + (lane & 15) < t.len) byte = load((is_v ? a.c.v_scales : a.c.k_scales) + row + (lane & 15));
-        };
-        auto load_rows = [&](int x) {
-          if (4 * x < held) {
 #pragma unroll
-            for (int p = 0; p < C::kPanels; ++p)
-              raw[x][p] = load(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
-          }
+          for (int x = 0; x < kLoads; ++x)
+            if (kStep * x < held) raw[x] = load(reinterpret_cast<const uint4*>(src + kStep * x * D));
         };
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int p = 0; p < C::kPanels; ++p) raw[x][p] = make_uint2(0u, 0u);
-        aim(g1, lookup(g1));
-#pragma unroll
-        for (int x = 0; x < 4; ++x) load_rows(x);
+        for (int x = 0; x < kLoads; ++x) raw[x] = make_uint4(0u, 0u, 0u, 0u);
+        fetch(g1, lookup(g1));
         int page2 = lookup(g2);
         while (g1 < g_end) {
           const int J = g1 >> 4, s = J & 1;  // the block's key tile
@@ -262,54 +260,53 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t* dst = smem + (is_v ? C::kV : C::kK) + s * C::kTileBytes + (16 * (g1 & 7) + r0) * 128;
-          // Piece p of row r0 + 4 x, swizzled by the row's last bits.
-          auto piece = [&](int x, int p) -> uint4* {
-            return reinterpret_cast<uint4*>(dst + p * kPanelBytes + 4 * x * 128 + ((c ^ ((r0 + 4 * x) & 7)) << 4));
+          // Piece 2 c + y of row r0 + kStep x, swizzled by the row's last bits.
+          auto piece = [&](int x, int y) -> uint4* {
+            const int q = 2 * c + y;
+            return reinterpret_cast<uint4*>(dst + (q >> 3) * kPanelBytes + kStep * x * 128 + (((q ^ (r0 + kStep * x)) & 7) << 4));
           };
           // A row's factor is 2^(byte - 127) * 2^120, in bf16 only up to a scale of 2^7. A group with a
           // larger one, or NaN, is done here, in two exact products; the code below then stores nothing.
-          // (A branch anywhere below would wait for the next group's loads: 2066 us instead of 1724 for
-          // 2048 tokens over 32768 keys.)
+          // (As branches of the loop below: 2047 us instead of 1913 for 2048 tokens over 32768 keys.)
           const uint32_t mine = byte;
           const bool large = __any_sync(0xffffffffu, mine - 135u <= 255u - 135u);
           if (large) {
             const uint32_t f2 = mine <= 134u || mine == 256u ? 0x3f803f80u : (mine == 255u ? 0x7fc0u : (mine - 7u) << 7) * 0x10001u;
             const uint32_t f1 = mine == 256u ? 0u : ((min(mine, 134u) + 120u) << 7) * 0x10001u;
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t a1 = __shfl_sync(0xffffffffu, f1, r0 + 4 * x), a2 = __shfl_sync(0xffffffffu, f2, r0 + 4 * x);
+            for (int x = 0; x < kLoads; ++x) {
+              const uint32_t a1 = __shfl_sync(0xffffffffu, f1, r0 + kStep * x);
+              const uint32_t a2 = __shfl_sync(0xffffffffu, f2, r0 + kStep * x);
 #pragma unroll 1
-              for (int p = 0; p < C::kPanels; ++p) {
+              for (int y = 0; y < 2; ++y) {
                 uint2 codes = make_uint2(0u, 0u);
-                if (4 * x < held) codes = load(reinterpret_cast<const uint2*>(src + 4 * x * D + 64 * p));
+                if (kStep * x < held) codes = load(reinterpret_cast<const uint2*>(src + kStep * x * D + 8 * y));
                 uint32_t r[4];
                 code_bits(codes, r);
                 times(r, a1);
                 times(r, a2);
-                *piece(x, p) = make_uint4(r[0], r[1], r[2], r[3]);
+                *piece(x, y) = make_uint4(r[0], r[1], r[2], r[3]);
               }
             }
           }
           const uint32_t f1 = mine == 256u ? 0u : ((mine + 120u) << 7) * 0x10001u;  // rows that are not there: zeros
-          aim(g2, page2);
-          const int g3 = g2 + step();
-          page2 = lookup(g3);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t f = __shfl_sync(0xffffffffu, f1, r0 + 4 * x);
+          for (int x = 0; x < kLoads; ++x) {
+            const uint32_t f = __shfl_sync(0xffffffffu, f1, r0 + kStep * x);
 #pragma unroll
-            for (int p = 0; p < C::kPanels; ++p) {
+            for (int y = 0; y < 2; ++y) {
               uint32_t r[4];
-              code_bits(raw[x][p], r);
+              code_bits(y ? make_uint2(raw[x].z, raw[x].w) : make_uint2(raw[x].x, raw[x].y), r);
               times(r, f);
-              if (!large) *piece(x, p) = make_uint4(r[0], r[1], r[2], r[3]);
+              if (!large) *piece(x, y) = make_uint4(r[0], r[1], r[2], r[3]);
             }
-            load_rows(x);  // of the next group
           }
           fence_proxy_async_smem();
           mbar_arrive_warp(bar((is_v ? B_VFULL : B_KFULL) + s));
+          fetch(g2, page2);
           g1 = g2;
-          g2 = g3;
+          g2 += step();
+          page2 = lookup(g2);
         }
         J0 += t.kt1 - t.kt0;
       }
@@ -749,13 +746,16 @@ fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaSt
     if ((st = make_bf16_map(&mk, a.c.k_pages, n, page, D, std::min(page, kTileN))) != FCP_OK) return st;
     if ((st = make_bf16_map(&mv, a.c.v_pages, n, page, D, std::min(page, kTileN))) != FCP_OK) return st;
   }
-  const int blocks = std::min(n_sm, kMaxChunkBlocks);
+  // A bf16 cache's blocks come in clusters of two, of which only the placement is used: neighbours
+  // on the line mostly read the same keys, and do so from one pair of SMs (4 sequences of 512 new
+  // tokens over up to 16384 keys: 231 to 212 us; other shapes, and an e4m3 cache, within a percent or two either way).
+  const int blocks = std::max(2, std::min(n_sm, kMaxChunkBlocks) & ~1);
   set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
   static std::atomic<uint64_t> allowed{0};
   if (const fcp_status st = allow_smem(chunk_kernel<D, kE4M3>, C::kSmemBytes, dev, allowed, "paged chunk smem attribute");
       st != FCP_OK)
     return st;
-  if (const fcp_status st = launch_overlapped(chunk_kernel<D, kE4M3>, dim3(blocks), kThreads<kE4M3>, C::kSmemBytes, s,
+  if (const fcp_status st = launch_overlapped<kE4M3 ? 1 : 2>(chunk_kernel<D, kE4M3>, dim3(blocks), kThreads<kE4M3>, C::kSmemBytes, s,
                                               "paged chunk launch", mq, mq16, mk, mv, a);
       st != FCP_OK)
     return st;
