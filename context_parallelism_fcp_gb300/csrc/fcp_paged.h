@@ -112,12 +112,14 @@ inline fcp_status allow_smem(Kernel kernel, int bytes, int device, std::atomic<u
 struct SeqShape {
   int32_t a, n, len;
 };
-__device__ __forceinline__ SeqShape seq_shape(const PagedArgs& p, int i, bool report) {
-  const int a = load(p.cu + i), b = load(p.cu + i + 1), len = load(p.lens + i);
+__device__ __forceinline__ SeqShape checked_shape(const PagedArgs& p, int a, int b, int len, bool report) {
   const bool ok = a >= 0 && b >= a && b <= p.total_new && len >= 0 &&
                   len <= (static_cast<long long>(p.max_pages) << p.page_shift);
   if (!ok && report) atomicCAS(p.status, 0, kErrCacheBatch);
   return SeqShape{a, ok ? b - a : 0, ok ? len : 0};
+}
+__device__ __forceinline__ SeqShape seq_shape(const PagedArgs& p, int i, bool report) {
+  return checked_shape(p, load(p.cu + i), load(p.cu + i + 1), load(p.lens + i), report);
 }
 
 // First row of page `page` for head h (a row index into the pages and scales).
