@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Line<kFewThreads> line;
   __shared__ Walk<P> walk;
-  __shared__ Piece shared_piece;
+  __shared__ Piece shared_piece[2];  // the one at work, and the next
   __shared__ float warp_m[kWarps][kRows], warp_l[kWarps][kRows];
   __shared__ uint2 shared_q[NT == 4 ? NT : 1][NT == 4 ? D / 16 : 1][32];
   __shared__ float shared_back[32];
@@ -160,52 +160,56 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
   static_assert(kWarps * kRows * kSumRow * 4 <= C::kStageBudget, "the warps' sums fit the stages");
   const int page_mask = (1 << a.c.page_shift) - 1;
 
-  Walk<P> w = walk;  // thread 0 goes on from there
-  for (bool first = true;; first = false) {
-    if (threadIdx.x == 0) {
-      if (!first) w.next(a);
-      Piece p;
-      p.ga = p.gb = 0;
-      while ((p.valid = w.i < a.c.n_seqs && w.f0 < w1)) {
-        w.part(w0, w1, p.ga, p.gb);
-        if (p.gb > p.ga) break;
-        w.next(a);  // the share has the group's overhead only
-      }
-      if (p.valid) {
-        p.i = w.i;
-        p.h = w.h;
-        p.u = w.u;
-        p.a = w.s.a;
-        p.n = w.s.n;
-        p.len = w.s.len;
-        p.end = w.end;
-        p.slot = piece_slot(b, p.ga, p.gb, w.g);
-        if (p.ga == 0 && p.gb < w.g) a.split[b] = SplitGroup{sh.owner(w.behind() - 1), w.s.a, w.s.n, w.h, w.u, {}};
-      }
-      shared_piece = p;
+  // Thread 0 walks on to the share's next piece.
+  auto advance = [&](bool first, Piece& to) {
+    Walk<P> w = walk;
+    if (!first) w.next(a);
+    Piece p;
+    p.ga = p.gb = 0;
+    while ((p.valid = w.i < a.c.n_seqs && w.f0 < w1)) {
+      w.part(w0, w1, p.ga, p.gb);
+      if (p.gb > p.ga) break;
+      w.next(a);  // the share has the group's overhead only
     }
-    __syncthreads();
-    const Piece p = shared_piece;
+    if (p.valid) {
+      p.i = w.i;
+      p.h = w.h;
+      p.u = w.u;
+      p.a = w.s.a;
+      p.n = w.s.n;
+      p.len = w.s.len;
+      p.end = w.end;
+      p.slot = piece_slot(b, p.ga, p.gb, w.g);
+      if (p.ga == 0 && p.gb < w.g) a.split[b] = SplitGroup{sh.owner(w.behind() - 1), w.s.a, w.s.n, w.h, w.u, {}};
+    }
+    walk = w;
+    to = p;
+  };
+  // Chunks of this warp are keys k0 + 16 * (warp + 4 n) below kend. Lane l holds the block table's
+  // entry for chunk l of a batch of 32.
+  auto entries = [&](const Piece& p, int batch) -> int {
+    const int key = p.ga * kGranule + kChunk * (warp + kWarps * (32 * batch + lane));
+    return p.valid && key < min(p.gb * kGranule, p.end)
+               ? load(a.c.table + static_cast<long long>(p.i) * a.c.max_pages + (key >> a.c.page_shift))
+               : -1;
+  };
+  if (threadIdx.x == 0) advance(true, shared_piece[0]);
+  __syncthreads();
+  int pages = entries(shared_piece[0], 0);
+  for (int turn = 0;; turn ^= 1) {
+    const Piece p = shared_piece[turn];
     if (!p.valid) break;
     const SeqShape s{p.a, p.n, p.len};
-
-    // chunks of this warp: keys k0 + 16 * (warp + 4 n) below kend
     const int k0 = p.ga * kGranule, kend = min(p.gb * kGranule, p.end);
-    const int* table = a.c.table + static_cast<long long>(p.i) * a.c.max_pages;
-    // lane l holds the block table's entry for chunk l of a batch of 32, and of the batch behind it
     const int key0 = k0 + kChunk * warp;
-    auto entries = [&](int batch) -> int {
-      const int key = key0 + (32 * batch + lane) * (kChunk * kWarps);
-      return key < kend ? load(table + (key >> a.c.page_shift)) : -1;
-    };
-    int pages = entries(0), pages_next = entries(1);
+    int pages_next = entries(p, 1);
     int n_issued = 0, issue_stage = 0;
     auto issue = [&]() {
       const int key = key0 + n_issued * (kChunk * kWarps);
       if (key < kend) {
         if ((n_issued & 31) == 0 && n_issued > 0) {
           pages = pages_next;
-          pages_next = entries((n_issued >> 5) + 1);
+          pages_next = entries(p, (n_issued >> 5) + 1);
         }
         const int page = __shfl_sync(0xffffffffu, pages, n_issued & 31);
         const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages);
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     };
 #pragma unroll
     for (int x = 0; x < C::kStages - 1; ++x) issue();
-
+    if (threadIdx.x == 0) advance(false, shared_piece[turn ^ 1]);  // while the first chunks are on their way
 
     // Q as the second operand: tile t's row 8 t + i8. With four tiles it would take a quarter of the
     // registers: warp t prepares tile t, and all read it from shared memory.
@@ -523,7 +527,8 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
         for (int o = 4; o < 32; o <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], o);
         if (i8 == 0) warp_m[warp][8 * t + 2 * j + e] = m[t][e];
       }
-    __syncthreads();  // also: every warp is done with its stages
+    __syncthreads();  // also: every warp is done with its stages, and the next piece is there
+    pages = entries(shared_piece[turn ^ 1], 0);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
         if (c == 0) a.part_ml[at] = make_float2(mx, sum);
       }
     }
-    __syncthreads();  // the stages and the shared piece are free again
+    __syncthreads();  // the stages are free again
   }
 }
 
