@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
   static_assert(kWarps * kRows * kSumRow * 4 <= C::kStageBudget, "the warps' sums fit the stages");
   const int page_mask = (1 << a.c.page_shift) - 1;
 
-  // Thread 0 walks on to the share's next piece.
+  // One thread walks on to the share's next piece.
   auto advance = [&](bool first, Piece& to) {
     Walk<P> w = walk;
     if (!first) w.next(a);
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
                ? load(a.c.table + static_cast<long long>(p.i) * a.c.max_pages + (key >> a.c.page_shift))
                : -1;
   };
-  if (threadIdx.x == 0) advance(true, shared_piece[0]);
+  if (threadIdx.x == kFewThreads - 32) advance(true, shared_piece[0]);
   __syncthreads();
   int pages = entries(shared_piece[0], 0);
   for (int turn = 0;; turn ^= 1) {
@@ -203,6 +203,50 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     const int k0 = p.ga * kGranule, kend = min(p.gb * kGranule, p.end);
     const int key0 = k0 + kChunk * warp;
     int pages_next = entries(p, 1);
+    // (token, head of the group) of the unit's row r, which lane r works out
+    int my_tok, my_head;
+    P::row(s, a.group, p.u, lane & (kRows - 1), my_tok, my_head);
+    auto row = [&](int r, int& tok, int& head) -> bool {
+      tok = __shfl_sync(0xffffffffu, my_tok, r);
+      head = __shfl_sync(0xffffffffu, my_head, r);
+      return tok < s.n;
+    };
+
+    // Q as the second operand: tile t's row 8 t + i8. With four tiles it would take a quarter of the
+    // registers: warp t prepares tile t, and all read it from shared memory.
+    constexpr bool kSharedQ = NT == 4;
+    uint32_t q[kSharedQ ? 1 : NT][D / 16][2];
+#pragma unroll
+    for (int t = 0; t < (kSharedQ ? 1 : NT); ++t) {
+      int tok, head;
+      const bool on = row(8 * (kSharedQ ? warp : t) + i8, tok, head);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + (static_cast<long long>(p.h * a.group + (on ? head : 0)) * a.c.total_new + s.a + (on ? tok : 0)) * D);
+      if constexpr (kE4M3) {
+        // 64 channels: lane j has channels 16 j .. 16 j + 15, in products 0-3 of the 64
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint4 v = on ? load(src + c * 8 + 2 * j + y) : make_uint4(0, 0, 0, 0);
+            q[t][4 * c + 2 * y][0] = v.x;
+            q[t][4 * c + 2 * y][1] = v.y;
+            q[t][4 * c + 2 * y + 1][0] = v.z;
+            q[t][4 * c + 2 * y + 1][1] = v.w;
+          }
+      } else {
+        // 32 channels: lane j has channels 8 j .. 8 j + 7, in products 0-1 of the 32
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const uint4 v = on ? load(src + c * 4 + j) : make_uint4(0, 0, 0, 0);
+          q[t][2 * c][0] = v.x;
+          q[t][2 * c][1] = v.y;
+          q[t][2 * c + 1][0] = v.z;
+          q[t][2 * c + 1][1] = v.w;
+        }
+      }
+    }
+
     int n_issued = 0, issue_stage = 0;
     auto issue = [&]() {
       const int key = key0 + n_issued * (kChunk * kWarps);
@@ -248,48 +292,8 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     };
 #pragma unroll
     for (int x = 0; x < C::kStages - 1; ++x) issue();
-    if (threadIdx.x == 0) advance(false, shared_piece[turn ^ 1]);  // while the first chunks are on their way
-
-    // Q as the second operand: tile t's row 8 t + i8. With four tiles it would take a quarter of the
-    // registers: warp t prepares tile t, and all read it from shared memory.
-    constexpr bool kSharedQ = NT == 4;
-    uint32_t q[kSharedQ ? 1 : NT][D / 16][2];
-    int lim_min = p.len;  // first key that some row does not see
-    if (a.causal) {
-      int tok, head;
-      P::row(s, a.group, p.u, 0, tok, head);
-      lim_min = s.len - s.n + tok + 1;
-    }
-#pragma unroll
-    for (int t = 0; t < (kSharedQ ? 1 : NT); ++t) {
-      int tok, head;
-      const bool on = P::row(s, a.group, p.u, 8 * (kSharedQ ? warp : t) + i8, tok, head);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<long long>(p.h * a.group + (on ? head : 0)) * a.c.total_new + s.a + (on ? tok : 0)) * D);
-      if constexpr (kE4M3) {
-        // 64 channels: lane j has channels 16 j .. 16 j + 15, in products 0-3 of the 64
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint4 v = on ? load(src + c * 8 + 2 * j + y) : make_uint4(0, 0, 0, 0);
-            q[t][4 * c + 2 * y][0] = v.x;
-            q[t][4 * c + 2 * y][1] = v.y;
-            q[t][4 * c + 2 * y + 1][0] = v.z;
-            q[t][4 * c + 2 * y + 1][1] = v.w;
-          }
-      } else {
-        // 32 channels: lane j has channels 8 j .. 8 j + 7, in products 0-1 of the 32
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const uint4 v = on ? load(src + c * 4 + j) : make_uint4(0, 0, 0, 0);
-          q[t][2 * c][0] = v.x;
-          q[t][2 * c][1] = v.y;
-          q[t][2 * c + 1][0] = v.z;
-          q[t][2 * c + 1][1] = v.w;
-        }
-      }
-    }
+    // while Q and the first chunks are on their way, in the warp that has the fewest
+    if (threadIdx.x == kFewThreads - 32) advance(false, shared_piece[turn ^ 1]);
 
     // e4m3: Q's rows as f16 scaled by 2^(14 - e), e the largest exponent of the row; `back` takes the
     // scores of row i8 of a tile to log2 units.
@@ -321,6 +325,8 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
       if (j == 0) shared_back[8 * warp + i8] = back[0];
       __syncthreads();
     }
+    // first key that some row does not see
+    const int lim_min = a.causal ? s.len - s.n + __shfl_sync(0xffffffffu, my_tok, 0) + 1 : s.len;
     // The lane's columns of S^T are rows 8 t + 2 j + {0, 1}: the first key that each does not see, and
     // its factor.
     int lim[NT][2];
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         int tok, head;
-        const bool on = P::row(s, a.group, p.u, 8 * t + 2 * j + e, tok, head);
+        const bool on = row(8 * t + 2 * j + e, tok, head);
         lim[t][e] = !on || !a.causal ? s.len : s.len - s.n + tok + 1;
         if constexpr (kSharedQ) factor[t][e] = shared_back[8 * t + 2 * j + e];
         else factor[t][e] = kE4M3 ? __shfl_sync(0xffffffffu, back[t], 4 * (2 * j + e)) : a.scale_log2;
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     for (int x = threadIdx.x; x < kRows * kLanes; x += kFewThreads) {
       const int r = x / kLanes, c = x % kLanes;
       int tok, head;
-      if (!P::row(s, a.group, p.u, r, tok, head)) continue;
+      if (!row(r, tok, head)) continue;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f, mx = -INFINITY;
 #pragma unroll
