@@ -28,6 +28,12 @@
 // (a power of two for each row, exact but for elements 2^-28 times the largest), and the rows'
 // scales multiply the scores. V's scale goes into the exponent of P: with s' = s + log2(scale)
 // the sum for O runs relative to the maximum of s', the sum of weights relative to that of s.
+//
+// Measured (8 KV heads, D = 128): 128 e4m3 sequences of up to 8192 tokens, 8 query heads a KV head,
+// 150 us (5870 GB/s, 87% of a copy's rate); two bf16 sequences of 131072, 155 us (6900 GB/s, all of
+// it); 32 bf16 sequences of up to 4096 with 4 drafted tokens, 4 query heads a KV head, 39 us (5170
+// GB/s, 76%; the beginnings and ends of pieces are the rest). 10 sequences of up to 1000 take 9 us,
+// of which the lengths, the first rows and the merge are a dependent chain of memory latencies.
 #include <algorithm>
 #include <cmath>
 
@@ -44,7 +50,7 @@ constexpr int kChunk = 16;                  // keys of a stage
 constexpr float kGrow = 8.0f;               // a row maximum is raised when it grows by over 2^8
 // Blocks to an SM and the shared memory of a block's stages, for NT tiles of 8 rows. bf16 is at
 // HBM's rate with two; the e4m3 conversion leaves more latency to hide, as far as the registers
-// go.
+// go: 128, 168 and 255 a thread.
 template <bool kE4M3, int NT>
 constexpr int kPerSm = !kE4M3 ? 2 : (NT == 1 ? 4 : (NT == 2 ? 3 : 2));
 
@@ -635,6 +641,10 @@ fcp_status launch_attn(const AttnArgs& a, int dtype, int hq, int max_new, void* 
   int dev = 0, n_sm = 0;
   if (const fcp_status st = this_device(&dev, &n_sm); st != FCP_OK) return st;
   const long long rows = static_cast<long long>(max_new) * a.group;
+  // Up to 32 rows of a KV head this kernel, in as few tiles of 8 as hold them; beyond, the tensor
+  // core's tiles of 128. (With 64 rows as the border, in two units: 48 rows took 19.0 us instead of
+  // 20.8 from an e4m3 cache and 16.6 instead of 19.6 from a bf16 one, 60 rows 21.4 instead of 18.5,
+  // 64 rows of long sequences 37.4 instead of 36.7, 128 rows far more.)
   if (rows > 32) return launch_paged_chunk(a, dtype, D, hq, workspace, dev, n_sm, s);
   const bool e = dtype == FCP_CACHE_E4M3;
   auto* launch = rows <= 8    ? (e ? launch_few<D, true, 1> : launch_few<D, false, 1>)
