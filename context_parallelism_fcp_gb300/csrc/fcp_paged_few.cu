@@ -154,10 +154,6 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
   let_next_start();
   wait_for_previous();
   if (threadIdx.x == 0) a.split[b].last = b;
-  const Shares sh = begin_walk<P, kFewThreads>(a, line, walk, b == 0);
-  if (b >= sh.blocks) return;
-  const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
-
   const uint32_t stages = smem_u32(smem) + warp * C::kWarpBytes;
   // [kWarps][kRows][kSumRow], over the stages at a piece's end; 4 floats between rows keep a warp's
   // stores on different banks
@@ -166,10 +162,8 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
   static_assert(kWarps * kRows * kSumRow * 4 <= C::kStageBudget, "the warps' sums fit the stages");
   const int page_mask = (1 << a.c.page_shift) - 1;
 
-  // One thread walks on to the share's next piece.
-  auto advance = [&](bool first, Piece& to) {
-    Walk<P> w = walk;
-    if (!first) w.next(a);
+  // One thread walks on to the share's next piece, w1 being the share's end.
+  auto advance = [&](Walk<P>& w, const Shares& sh, long long w0, long long w1, Piece& to) {
     Piece p;
     p.ga = p.gb = 0;
     while ((p.valid = w.i < a.c.n_seqs && w.f0 < w1)) {
@@ -191,6 +185,10 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     walk = w;
     to = p;
   };
+  const Shares sh = begin_walk<P, kFewThreads>(a, line, b == 0, [&](Walk<P>& w, const Shares& sh, long long w0, long long w1) {
+    advance(w, sh, w0, w1, shared_piece[0]);
+  });
+  if (b >= sh.blocks) return;
   // Chunks of this warp are keys k0 + 16 * (warp + 4 n) below kend. Lane l holds the block table's
   // entry for chunk l of a batch of 32.
   auto entries = [&](const Piece& p, int batch) -> int {
@@ -199,8 +197,6 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
                ? load(a.c.table + static_cast<long long>(p.i) * a.c.max_pages + (key >> a.c.page_shift))
                : -1;
   };
-  if (threadIdx.x == kFewThreads - 32) advance(true, shared_piece[0]);
-  __syncthreads();
   int pages = entries(shared_piece[0], 0);
   for (int turn = 0;; turn ^= 1) {
     const Piece p = shared_piece[turn];
@@ -299,7 +295,11 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
 #pragma unroll
     for (int x = 0; x < C::kStages - 1; ++x) issue();
     // while Q and the first chunks are on their way, in the warp that has the fewest
-    if (threadIdx.x == kFewThreads - 32) advance(false, shared_piece[turn ^ 1]);
+    if (threadIdx.x == kFewThreads - 32) {
+      Walk<P> w = walk;
+      w.next(a);
+      advance(w, sh, sh.begin(b), sh.begin(b + 1), shared_piece[turn ^ 1]);
+    }
 
     // e4m3: Q's rows as f16 scaled by 2^(14 - e), e the largest exponent of the row; `back` takes the
     // scores of row i8 of a tile to log2 units.
