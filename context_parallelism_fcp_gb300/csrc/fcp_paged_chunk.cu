@@ -136,13 +136,42 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x;
   let_next_start();
+  wait_for_previous();
+  if (threadIdx.x == 0) a.split[b].last = b;
+  // (The first unit published in there, and what follows done before the wait: no faster for small
+  // batches, and 1930 us instead of 1890 for 2048 tokens over 32768 e4m3 keys.)
+  const Shares sh = begin_walk<P, kThreads>(a, line, b == 0,
+                                            [&](Walk<P>& w, const Shares&, long long, long long) { walk = w; });
+  if (b >= sh.blocks) return;
   // 128-byte-swizzled tiles need a 1024-byte aligned base; report, never fault
   if ((sb & 1023u) != 0) {
-    wait_for_previous();
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrSmemAlign);
     return;
   }
-  // what needs nothing of the kernel before this one
+
+  Unit* unit_slot = reinterpret_cast<Unit*>(smem + C::kBar + kUnitOff);
+  // consumer side: the unit of round v (valid = -1 when a wait gave up)
+  auto next_unit = [&](int v, int code) -> Unit {
+    Unit t;
+    t.valid = -1;
+    if (__all_sync(0xffffffffu, mbar_wait(bar(B_TFULL + (v & 1)), (v >> 1) & 1, abort_flag, err, code))) {
+      const volatile Unit* src = unit_slot + (v & 1);
+      t.valid = src->valid;
+      t.i = src->i;
+      t.a = src->a;
+      t.n = src->n;
+      t.len = src->len;
+      t.h = src->h;
+      t.u = src->u;
+      t.kt0 = src->kt0;
+      t.kt1 = src->kt1;
+      t.slot = src->slot;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_TEMPTY + (v & 1)));
+    }
+    return t;
+  };
+
   if (threadIdx.x == 0) {
     mbar_init(bar(B_QFULL), 1);
     mbar_init(bar(B_QEMPTY), 1);
@@ -167,68 +196,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   if (warp == 9) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
-    tc_fence_before();
   }
-  wait_for_previous();
-  if (threadIdx.x == 0) a.split[b].last = b;
-  Unit* unit_slot = reinterpret_cast<Unit*>(smem + C::kBar + kUnitOff);
-  // Publishes the share's next unit in slot k (one thread); w1 is the share's end.
-  auto publish = [&](Walk<P>& w, const Shares& sh, long long w0, long long w1, int k) {
-    int ga = 0, gb = 0;
-    bool more;
-    while ((more = w.i < a.c.n_seqs && w.f0 < w1)) {
-      w.part(w0, w1, ga, gb);
-      if (gb > ga) break;
-      w.next(a);  // the share has the group's overhead only
-    }
-    volatile Unit* dst = unit_slot + k;
-    dst->valid = more ? 1 : 0;
-    if (more) {
-      dst->i = w.i;
-      dst->a = w.s.a;
-      dst->n = w.s.n;
-      dst->len = w.s.len;
-      dst->h = w.h;
-      dst->u = w.u;
-      dst->kt0 = ga;
-      dst->kt1 = gb;
-      dst->slot = piece_slot(b, ga, gb, w.g);
-      if (ga == 0 && gb < w.g) a.split[b] = SplitGroup{sh.owner(w.behind() - 1), w.s.a, w.s.n, w.h, w.u, {}};
-    }
-  };
-  const Shares sh = begin_walk<P, kThreads>(a, line, b == 0, [&](Walk<P>& w, const Shares& sh, long long w0, long long w1) {
-    publish(w, sh, w0, w1, 0);
-    walk = w;
-  });
-  // consumer side: the unit of round v (valid = -1 when a wait gave up)
-  auto next_unit = [&](int v, int code) -> Unit {
-    Unit t;
-    t.valid = -1;
-    if (__all_sync(0xffffffffu, mbar_wait(bar(B_TFULL + (v & 1)), (v >> 1) & 1, abort_flag, err, code))) {
-      const volatile Unit* src = unit_slot + (v & 1);
-      t.valid = src->valid;
-      t.i = src->i;
-      t.a = src->a;
-      t.n = src->n;
-      t.len = src->len;
-      t.h = src->h;
-      t.u = src->u;
-      t.kt0 = src->kt0;
-      t.kt1 = src->kt1;
-      t.slot = src->slot;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_TEMPTY + (v & 1)));
-    }
-    return t;
-  };
-
-  // begin_walk's barriers have ordered the allocation before this
+  tc_fence_before();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (b >= sh.blocks) {
-    if (warp == 9) tmem_dealloc(tmem, 512);
-    return;
-  }
 
   if (warp >= 8) {
     if constexpr (kE4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -362,6 +334,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       }
       const long long w0 = sh.begin(b), w1 = sh.begin(b + 1);
       Walk<P> w = walk;
+      bool more = true;
       bool ok = true;
       int J = 0;                                    // key tiles loaded
       int last_q = -1, last_kj = -1, last_vj = -1;  // round of the last Q load, tiles of the last K, V loads
@@ -371,9 +344,26 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
-          if (v > 0) {  // the first is there already
-            w.next(a);
-            publish(w, sh, w0, w1, k);
+          if (v > 0) w.next(a);
+          int ga = 0, gb = 0;
+          while ((more = more && w.i < a.c.n_seqs && w.f0 < w1)) {
+            w.part(w0, w1, ga, gb);
+            if (gb > ga) break;
+            w.next(a);  // the share has the group's overhead only
+          }
+          volatile Unit* dst = unit_slot + k;
+          dst->valid = more ? 1 : 0;
+          if (more) {
+            dst->i = w.i;
+            dst->a = w.s.a;
+            dst->n = w.s.n;
+            dst->len = w.s.len;
+            dst->h = w.h;
+            dst->u = w.u;
+            dst->kt0 = ga;
+            dst->kt1 = gb;
+            dst->slot = piece_slot(b, ga, gb, w.g);
+            if (ga == 0 && gb < w.g) a.split[b] = SplitGroup{sh.owner(w.behind() - 1), w.s.a, w.s.n, w.h, w.u, {}};
           }
           mbar_arrive(bar(B_TFULL + k));
         }
