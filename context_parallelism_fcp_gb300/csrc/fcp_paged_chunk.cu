@@ -17,10 +17,10 @@
 //
 // Bound by the chain of each key tile, S -> softmax -> P -> PV, as the forward is: tensor memory has
 // no room for a second S of a tile; an e4m3 cache adds the loaders' instructions to the softmax's.
-// Measured (64 query, 8 KV heads, D = 128, alone): 2048 new tokens over 32768 keys 1495 us from a bf16
-// cache (1425 TFLOP/s) and 1695 us from an e4m3 one (1257), 8192 over 8192 863 and 1034 us, 16 chunks
-// of 512 with nothing before them 163 and 203 us (a quarter of it writes o). Call after call the e4m3
-// figure is 1913 us: blocks then land on other SMs, and the slowest decides.
+// Measured (64 query, 8 KV heads, D = 128, alone): 2048 new tokens over 32768 keys 1480 us from a bf16
+// cache (1440 TFLOP/s) and 1740 us from an e4m3 one (1224), 8192 over 8192 850 and 1034 us, 16 chunks
+// of 512 with nothing before them 163 and 200 us (a quarter of it writes o). Call after call the first
+// two are 1560 and 1890 us: blocks then land on other SMs, and the slowest decides.
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1 (thread = row = TMEM lane); 8: the walk along the
 // block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 only): loaders.

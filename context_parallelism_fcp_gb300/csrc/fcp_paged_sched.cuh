@@ -224,7 +224,7 @@ struct Shares {
 // share (blocks <= its index) makes none. All kThreads threads; ends with a barrier. report: record
 // the batch's errors. (The chain from the lengths to the first keys is most of a small call's
 // time: that the finder also works out the first piece, with few divisions in a row, took
-// 10 sequences of up to 1000 tokens from 8.9 to 8.5 us.)
+// 10 sequences of up to 1000 tokens from 9.1 to 8.6 us.)
 template <int kThreads>
 struct Line {
   long long warp_sum[kThreads / 32];
