@@ -568,3 +568,73 @@ def test_a_workspace_of_another_kind_is_refused(fcp):
                torch.empty(n, dtype=torch.int8, device="cuda")):
         with pytest.raises((TypeError, ValueError)):
             fcp.paged_attn(cache, batch, t["q"], *out, ws)
+
+
+def many(c, new):
+    n = 2600
+    return Batch([new[i % len(new)] for i in range(n)], [(i * 29) % 90 for i in range(n)], hq=2, hkv=1, cache=c, seed=9, pad=2)
+
+
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+def test_more_sequences_than_a_block_has_threads(fcp, c):
+    """Offsets are searched in two steps and a thread has several sequences of the schedule, some of
+    them with no new token."""
+    b = many(c, [0, 1, 2])
+    t = U.make(b)
+    for max_new in (2, 200):  # both kernels
+        b.max_new = max_new
+        cache, batch = U.handles(fcp, b, t)
+        o, lse, before = attend(fcp, b, t, cache, batch)
+        cache.check_device_error()
+        U.check_attention(b, t, o, lse, *before)
+    # every new token's row: what is read back is what the pages hold
+    k, v = (torch.full((1, b.total, b.d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    fcp.cache_write(cache, batch, t["k"], t["v"])
+    fcp.cache_read(cache, batch, k, v)
+    cache.check_device_error()
+    row = 0
+    for n, length in zip(b.new, b.lens):
+        for j in range(n):
+            if length - n + j < 0:
+                assert (k[0, row] == 7).all() and (v[0, row] == 7).all()
+            elif c == "bf16":
+                assert torch.equal(k[0, row], t["k"][0, row]) and torch.equal(v[0, row], t["v"][0, row])
+            row += 1
+    assert (k[:, row:] == 7).all() and row == b.total - 2
+    if c == "e4m3":
+        held = torch.tensor([length - n + j >= 0 for n, length in zip(b.new, b.lens) for j in range(n)], device="cuda")
+        for got, x in ((k, t["k"]), (v, t["v"])):
+            x, got = x[0, :row][held].double(), got[0, :row][held].double()
+            # half a step of e4m3: 2^-4 of the value, or 2^-10 of the scale, which is at most amax / 224
+            assert ((got - x).abs() <= torch.maximum(x.abs() * 2.0 ** -4, x.abs().amax(1, keepdim=True) / 224 * 2.0 ** -10)).all()
+
+
+@pytest.mark.parametrize("new", [1, 40], ids=["few", "chunk"])
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+def test_buffers_at_the_least_alignment(fcp, c, new):
+    """Rows, pages and scales on 16-byte, lse and the batch's arrays on 4-byte boundaries."""
+    b = Batch([new, 3], [300, 70], hq=6, hkv=2, d=128, page=32, cache=c, seed=4)
+    t = U.make(b)
+
+    def shifted(x):
+        if x is None:
+            return None
+        step = 16 // x.element_size() if x.dtype not in (torch.int32, torch.float32) else 1
+        flat = torch.zeros(x.numel() + step, dtype=torch.uint8 if x.element_size() == 1 else x.dtype, device="cuda")
+        out = flat[step:].view(x.dtype).view(x.shape)
+        out.copy_(x) if x.element_size() > 1 else out.view(torch.uint8).copy_(x.view(torch.uint8))
+        return out
+
+    u = {name: shifted(x) for name, x in t.items()}
+    results = []
+    for z in (t, u):
+        cache, batch = U.handles(fcp, b, z)
+        o, lse = shifted(torch.zeros_like(z["q"])), shifted(torch.zeros(b.hq, b.total, device="cuda"))
+        fcp.cache_write(cache, batch, z["k"], z["v"])
+        k, v = shifted(torch.zeros_like(z["k"])), shifted(torch.zeros_like(z["v"]))
+        fcp.cache_read(cache, batch, k, v)
+        fcp.PagedAttention(cache, b.hq).forward(batch, z["q"], o, lse)
+        cache.check_device_error()
+        results.append((o, lse, k, v))
+        U.check_attention(b, z, o, lse)
+    assert all(torch.equal(x, y) for x, y in zip(*results))
