@@ -1,4 +1,8 @@
 """The paged cache and its attention against the float64 definitions (oracle/paged.py)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -638,3 +642,37 @@ def test_buffers_at_the_least_alignment(fcp, c, new):
         results.append((o, lse, k, v))
         U.check_attention(b, z, o, lse)
     assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
+FIRST_CALL = """
+import torch
+import context_parallelism_fcp_gb300 as fcp
+from tests import paged_util as U
+for c in ("bf16", "e4m3"):
+    for new in (1, 40):
+        b = U.Batch([new], [100], hq=2, hkv=1, d=128, cache=c)
+        t = U.make(b)
+        cache, batch = U.handles(fcp, b, t)
+        att = fcp.PagedAttention(cache, b.hq)
+        o, lse = torch.zeros_like(t["q"]), torch.zeros(b.hq, b.total, device="cuda")
+        k, v = torch.zeros_like(t["k"]), torch.zeros_like(t["v"])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fcp.cache_write(cache, batch, t["k"], t["v"])
+            att.forward(batch, t["q"], o, lse)
+            fcp.cache_read(cache, batch, k, v)
+        graph.replay()
+        torch.cuda.synchronize()
+        cache.check_device_error()
+        U.check_attention(b, t, o, lse)
+        assert k.abs().sum() > 0
+print("captured")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """Nothing is set up by a first call that a capture would not allow."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, env={**os.environ, "PYTHONPATH": root},
+                       capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
