@@ -17,10 +17,10 @@
 //
 // Bound by the chain of each key tile, S -> softmax -> P -> PV, as the forward is: tensor memory has
 // no room for a second S of a tile; an e4m3 cache adds the loaders' instructions to the softmax's.
-// Measured (64 query, 8 KV heads, D = 128, alone): 2048 new tokens over 32768 keys 1480 us from a bf16
-// cache (1440 TFLOP/s) and 1740 us from an e4m3 one (1224), 8192 over 8192 850 and 1034 us, 16 chunks
-// of 512 with nothing before them 163 and 200 us (a quarter of it writes o). Call after call the first
-// two are 1560 and 1890 us: blocks then land on other SMs, and the slowest decides.
+// Measured (64 query, 8 KV heads, D = 128, alone): 2048 new tokens over 32768 keys 1330 us from a bf16
+// cache (1600 TFLOP/s) and 1735 us from an e4m3 one (1228), 8192 over 8192 750 and 959 us, 16 chunks
+// of 512 with nothing before them 156 and 189 us (a quarter of it writes o). Call after call the first
+// two are 1440 and 1880 us: blocks then land on other SMs, and the slowest decides.
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1 (thread = row = TMEM lane); 8: the walk along the
 // block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 only): loaders.
@@ -120,11 +120,14 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   using C = Cfg<D>;
   using P = ChunkRows;
   extern __shared__ __align__(1024) uint8_t smem[];
-  // these lie where the first epilogue writes, long after the walk has begun
-  Line<kThreads>& line = *reinterpret_cast<Line<kThreads>*>(smem + C::kStage);
-  Walk<P>& walk = *reinterpret_cast<Walk<P>*>(smem + C::kStage + 1024);
-  static_assert(sizeof(Line<kThreads>) <= 1024 && 1024 + sizeof(Walk<P>) <= C::kStageBytes, "they fit the staging");
-  const uint32_t sb = smem_u32(smem);
+  // As static variables, and with a base of the dynamic part that the compiler does not see through:
+  // with these two laid over the staging area and a constant base, the same steps took 850 us instead
+  // of 750 for 8192 bf16 tokens (D = 64: 178 and 157 us for 8 x 256 over 8192), and 1007 instead of
+  // 959 for e4m3.
+  __shared__ Line<kThreads> line;
+  __shared__ Walk<P> walk;
+  uint32_t sb = smem_u32(smem);
+  asm volatile("" : "+r"(sb));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + B_COUNT * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBar + B_COUNT * 8 + 4);
   // set when an aborted block could not confirm that its issued copies or MMAs have finished
@@ -758,7 +761,7 @@ fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaSt
   }
   // A bf16 cache's blocks come in clusters of two, of which only the placement is used: neighbours
   // on the line mostly read the same keys, and do so from one pair of SMs (4 sequences of 512 new
-  // tokens over up to 16384 keys: 231 to 212 us; other shapes, and an e4m3 cache, within a percent or two either way).
+  // tokens over up to 16384 keys: 195 to 190 us; other shapes, and an e4m3 cache, within a percent or two either way).
   const int blocks = std::max(2, std::min(n_sm, kMaxChunkBlocks) & ~1);
   set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
   static std::atomic<uint64_t> allowed{0};
