@@ -13,7 +13,9 @@
 // their way to shared memory. That product with a power of two is exact, so the kernel computes
 // the attention over what reading the cache gives, and the tensor core runs the same bf16
 // instructions for both. Rows of V past the sequence become zeros, since a zero weight times
-// whatever such a row holds may be NaN.
+// whatever such a row holds may be NaN. So do an e4m3 cache's NaN rows of V, which rows that come
+// before them must not meet: a unit keeps the first position of one, and o of the rows that see it
+// becomes NaN when it is stored.
 //
 // Bound by the chain of each key tile, S -> softmax -> P -> PV, as the forward is: tensor memory has
 // no room for a second S of a tile; an e4m3 cache adds the loaders' instructions to the softmax's.
@@ -68,9 +70,10 @@ enum : int {
 struct Unit {
   int valid, i, a, n, len, h, u, kt0, kt1, slot, pad0, pad1;
 };
+constexpr int kNanKeyOff = B_COUNT * 8 + 12;  // of the last 4 units: the first key whose row of V is NaN
 constexpr int kUnitOff = 256;
 constexpr int kBarArea = kUnitOff + 2 * static_cast<int>(sizeof(Unit));
-static_assert(B_COUNT * 8 + 12 <= kUnitOff, "barrier area");
+static_assert(kNanKeyOff + 4 * 4 <= kUnitOff, "barrier area");
 
 template <int D>
 struct Cfg {
@@ -132,6 +135,9 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBar + B_COUNT * 8 + 4);
   // set when an aborted block could not confirm that its issued copies or MMAs have finished
   volatile int* unquiesced = reinterpret_cast<volatile int*>(smem + C::kBar + B_COUNT * 8 + 8);
+  // unit v's is slot v % 4: when unit v + 4 is published, every warp has read unit v + 2 and so is
+  // done with unit v
+  int* nan_key = reinterpret_cast<int*>(smem + C::kBar + kNanKeyOff);
   auto bar = [&](int i) -> uint32_t { return sb + C::kBar + 8 * i; };
   int* err = a.c.status;
 
@@ -284,8 +290,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           const uint32_t mine = byte;
           const bool large = __any_sync(0xffffffffu, mine - 135u <= 255u - 135u);
           if (large) {
-            const uint32_t f2 = mine <= 134u || mine == 256u ? 0x3f803f80u : (mine == 255u ? 0x7fc0u : (mine - 7u) << 7) * 0x10001u;
-            const uint32_t f1 = mine == 256u ? 0u : ((min(mine, 134u) + 120u) << 7) * 0x10001u;
+            const uint32_t nan = __ballot_sync(0xffffffffu, is_v && mine == 255u);
+            if (nan != 0u && lane == 0) atomicMin(nan_key + (v & 3), first_key(g1) + __ffs(nan) - 1);
+            const bool none = mine == 256u || (nan >> lane & 1u);
+            const uint32_t f2 = none || mine <= 134u ? 0x3f803f80u : (mine == 255u ? 0x7fc0u : (mine - 7u) << 7) * 0x10001u;
+            const uint32_t f1 = none ? 0u : ((min(mine, 134u) + 120u) << 7) * 0x10001u;
 #pragma unroll 1
             for (int x = 0; x < kLoads; ++x) {
               const uint32_t a1 = __shfl_sync(0xffffffffu, f1, r0 + kStep * x);
@@ -356,6 +365,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           }
           volatile Unit* dst = unit_slot + k;
           dst->valid = more ? 1 : 0;
+          if constexpr (kE4M3) nan_key[v & 3] = INT32_MAX;
           if (more) {
             dst->i = w.i;
             dst->a = w.s.a;
@@ -674,7 +684,10 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         mbar_arrive_warp(bar(B_OFREE + t));
         continue;
       }
-      const float inv = T.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      float inv = T.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      // every V of the unit has been loaded: its last PV is complete
+      const bool nan = kE4M3 && *const_cast<volatile int*>(nan_key + (v & 3)) < lim_row;
+      if (nan) inv = __uint_as_float(0x7fc00000u);
       // The warp's rows go through a shared block of 32 rows x 128 bytes (16-byte slots XOR-swizzled
       // by row), 64 bf16 or 32 float32 channels at a time, so that stores write whole row segments:
       // lane l writes slot l % 8 of rows l / 8 + 4 i
@@ -695,6 +708,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<uint4*>(stg + lane * 128 + ((e ^ (lane & 7)) << 4)) =
                 make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          if (nan) {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + (e << 4)) = make_uint4(0x7fc00000u, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u);
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

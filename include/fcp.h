@@ -428,9 +428,11 @@ size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
  * log-sum-exp lse. q and o are [Hq, total_new, D], lse [Hq, total_new] float32. The new tokens'
  * own K and V have to be in the cache already (fcp_cache_write). An e4m3 cache gives the
  * attention over what fcp_cache_read returns. A row that sees no key gets o = 0, lse = -inf.
- * Rows of the pages past a sequence's length may hold anything, NaN included; a NaN or infinity
- * that a bf16 cache holds in V at a position of the sequence itself may reach the rows of the
- * same batch that come before it. Sums, maxima and the softmax's statistics are float32; P is
+ * Rows of the pages past a sequence's length may hold anything, NaN included. A NaN row of an
+ * e4m3 cache (scale byte 255) reaches the rows that see it and no others; a NaN or infinity that a
+ * bf16 cache holds in V at a position of the sequence itself, or that code * 2^k becomes in bf16
+ * (pages filled otherwise than by fcp_cache_write), may reach, in its channel, the new tokens of
+ * the same sequence that come before it. Sums, maxima and the softmax's statistics are float32; P is
  * rounded to bf16 (f16 in the kernel for few rows of an e4m3 cache) for the product with V.
  * Results do not depend on timing: no atomics are used. o and lse must not overlap the inputs.
  * workspace: fcp_paged_attn_workspace_bytes, 256-byte aligned, its contents need not be
