@@ -27,7 +27,9 @@
 // products run in f16: a code is exact there, Q's rows are scaled to a largest exponent of 14
 // (a power of two for each row, exact but for elements 2^-28 times the largest), and the rows'
 // scales multiply the scores. V's scale goes into the exponent of P: with s' = s + log2(scale)
-// the sum for O runs relative to the maximum of s', the sum of weights relative to that of s.
+// the sum for O runs relative to the maximum of s', the sum of weights relative to that of s. A row of
+// V whose scale is far below that of the keys with the large s' gets a P that f16 cannot hold: where
+// a chunk has one, what f16 leaves of P is multiplied by V once more, scaled up.
 //
 // Measured (8 KV heads, D = 128): 128 e4m3 sequences of up to 8192 tokens, 8 query heads a KV head,
 // 150 us (5870 GB/s, 87% of a copy's rate); two bf16 sequences of 131072, 155 us (6900 GB/s, all of
@@ -48,6 +50,15 @@ constexpr int kWarps = 4;
 constexpr int kFewThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys of a stage
 constexpr float kGrow = 8.0f;               // a row maximum is raised when it grows by over 2^8
+constexpr float kUp = 7.0f;                 // e4m3: P starts at 2^7 and grows to 2^15, the top of f16
+// e4m3: below 2^-14 P's rounding to f16 is off by up to 2^-25, which for a key whose V has a scale
+// 2^gap below that of the largest is 2^(gap - 25 - kUp) of the largest weight. Up to this gap (2^-22)
+// that is left so; beyond it the rest of P counts too (which it has to: with gaps of 2^18 and more,
+// channels where the large row is zero were off by tens of times the rounding of P and o, or zero).
+// The test for it costs single tokens up to 1%, 32 x 4 tokens of 2, 4 and 8 heads 26.2 to 27.6, 38.1
+// to 38.6 and 58.5 to 57.6 us.
+constexpr int kScaleGap = 10;
+constexpr float kLift = 0x1p28f;
 // Blocks to an SM and the shared memory of a block's stages, for NT tiles of 8 rows. bf16 is at
 // HBM's rate with two; the e4m3 conversion leaves more latency to hide, as far as the registers
 // go: 128, 168 and 255 a thread.
@@ -127,6 +138,26 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
+}
+
+// f(c, fragment) for each 16 channels of a chunk's V in e4m3, as the first operand in f16.
+template <int kRowBytes, class F>
+__device__ __forceinline__ void each_v(uint32_t vt, int lane, F f) {
+  const int vr = (lane & 7) + (lane & 8);  // keys 0-7, 8-15 of a 16-channel piece, then of the next
+#pragma unroll
+  for (int c = 0; c < kRowBytes / 16; c += 2) {
+    uint32_t x[4];
+    ldsm4_trans(vt + piece_at<kRowBytes>(vr, c + (lane >> 4)), x);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      // bytes: even and odd channel of one key, then of the next; the even channels are the
+      // fragment's rows 0-7, the odd ones 8-15
+      uint32_t v[4];
+      e4m3x4_to_f16x2(__byte_perm(x[2 * y], 0, 0x3120), v[0], v[1]);
+      e4m3x4_to_f16x2(__byte_perm(x[2 * y + 1], 0, 0x3120), v[2], v[3]);
+      f(c + y, v);
+    }
+  }
 }
 
 struct Piece {
@@ -353,8 +384,9 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     };
 
     // m: the maximum of a row's scores, which its weights' sum l is relative to; mo: for e4m3 that of
-    // scores with V's scale, which acc is relative to. The eight lanes of a column pair share m and mo;
-    // l is over the lane's own keys.
+    // scores with V's scale less kUp, which acc is relative to. The eight lanes of a column pair share m
+    // and mo; l is over the lane's own keys. low: the scale byte below which a row of V is far below mo.
+    int low = 0;
     float m[NT][2], l[NT][2], mo[NT][2], acc[D / 16][NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -419,8 +451,9 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
       // of the 32 scales (16 of K, 16 of V) into what is needed of it, and the others ask for it.
       float so[NT][4];
       float kf[2], vf[2];
+      uint32_t byte = 0;
       if constexpr (kE4M3) {
-        const uint32_t byte = lds_u8(kt + 2 * C::kTile + lane);
+        byte = lds_u8(kt + 2 * C::kTile + lane);
         const float mine = lane < 16 ? e8m0_to_float(byte) : e8m0_log2(byte);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
@@ -457,7 +490,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
           grow = grow || top[t][e] > m[t][e] + kGrow;
           if constexpr (kE4M3) {
             topo[t][e] = fmaxf(so[t][e], so[t][2 + e]);
-            grow = grow || topo[t][e] > mo[t][e] + kGrow;
+            grow = grow || topo[t][e] > mo[t][e] + (kGrow + kUp);
           }
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -475,13 +508,23 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
             };
             float f = raise(m[t][e], top[t][e]);
             l[t][e] *= f;
-            if constexpr (kE4M3) f = raise(mo[t][e], topo[t][e]);
+            if constexpr (kE4M3) f = raise(mo[t][e], topo[t][e] - kUp);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               acc[c][t][e] *= f;
               acc[c][t][2 + e] *= f;
             }
           }
+        if constexpr (kE4M3) {
+          float gap = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) gap = fmaxf(gap, mo[t][e] - m[t][e]);  // rows without a key: NaN, left out
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) gap = fmaxf(gap, __shfl_xor_sync(0xffffffffu, gap, o));
+          low = lane < 16 ? 0 : static_cast<int>(fmaxf(gap, -256.f) + kUp) + 127 - kScaleGap;
+        }
       }
       // P^T: the packed pairs are (key; rows 2 j, 2 j + 1) and are wanted as (row; keys 2 j, 2 j + 1)
       uint32_t pt[NT][2];
@@ -492,7 +535,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
         for (int e = 0; e < 4; ++e) {
           pw[e] = fast_exp2(sc[t][e] - (m[t][e & 1] == -INFINITY ? 0.f : m[t][e & 1]));
           l[t][e & 1] += pw[e];
-          // in f16: off by 2^-11 of itself, or 2^-25 of the row's largest
+          // in f16: off by 2^-11 of itself, or 2^-25 (see kScaleGap)
           if constexpr (kE4M3) pw[e] = fast_exp2(so[t][e] - (mo[t][e & 1] == -INFINITY ? 0.f : mo[t][e & 1]));
         }
 #pragma unroll
@@ -501,22 +544,40 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
                                         : pack_bf16(pw[2 * y], pw[2 * y + 1]));  // bf16: off by 2^-8 of itself at most
       }
       if constexpr (kE4M3) {
-        const int vr = (lane & 7) + (lane & 8);  // keys 0-7, 8-15 of a 16-channel piece, then of the next
+        if (__any_sync(0xffffffffu, static_cast<int>(byte) < low)) {  // of V's scales: lanes 16 and on
+          // What is left of P where f16 rounds it as a subnormal number, times 2^28, then what is left of
+          // that: each product's sum is added at its own scale. (A tile of rows at a time, for registers.)
+          auto left = [](float x) -> float {
+            return fabsf(x) < 0x1p-14f ? (x - __half2float(__float2half_rn(x))) * kLift : 0.f;
+          };
 #pragma unroll
-        for (int c = 0; c < C::kPieces; c += 2) {
-          uint32_t f[4];
-          ldsm4_trans(vt + piece_at<C::kRowBytes>(vr, c + (lane >> 4)), f);
+          for (int t = 0; t < NT; ++t) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            // bytes: even and odd channel of one key, then of the next; the even channels are the
-            // fragment's rows 0-7, the odd ones 8-15
-            uint32_t v[4];
-            e4m3x4_to_f16x2(__byte_perm(f[2 * y], 0, 0x3120), v[0], v[1]);
-            e4m3x4_to_f16x2(__byte_perm(f[2 * y + 1], 0, 0x3120), v[2], v[3]);
+            for (int e = 0; e < 4; ++e) so[t][e] = left(fast_exp2(so[t][e] - (mo[t][e & 1] == -INFINITY ? 0.f : mo[t][e & 1])));
+            float down = 1.f;
+#pragma unroll 1
+            while (__any_sync(0xffffffffu, so[t][0] != 0.f || so[t][1] != 0.f || so[t][2] != 0.f || so[t][3] != 0.f)) {
+              uint32_t rest[2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816h(acc[c + y][t], v, pt[t][0], pt[t][1]);
+              for (int y = 0; y < 2; ++y) rest[y] = transpose8x8(pack_f16(so[t][2 * y], so[t][2 * y + 1]));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) so[t][e] = left(so[t][e]);
+              down *= 1.f / kLift;
+              each_v<C::kRowBytes>(vt, lane, [&](int c, const uint32_t(&v)[4]) {
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816h(sum, v, rest[0], rest[1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[c][t][e] = fmaf(sum[e], down, acc[c][t][e]);
+              });
+            }
           }
         }
+      }
+      if constexpr (kE4M3) {
+        each_v<C::kRowBytes>(vt, lane, [&](int c, const uint32_t(&v)[4]) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma16816h(acc[c][t], v, pt[t][0], pt[t][1]);
+        });
       } else {
         const int vr = (lane & 7) + ((lane >> 4) << 3);  // channels 0-7, 8-15 of keys 0-7, then of keys 8-15
 #pragma unroll

@@ -433,7 +433,8 @@ size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
  * bf16 cache holds in V at a position of the sequence itself, or that code * 2^k becomes in bf16
  * (pages filled otherwise than by fcp_cache_write), may reach, in its channel, the new tokens of
  * the same sequence that come before it. Sums, maxima and the softmax's statistics are float32; P is
- * rounded to bf16 (f16 in the kernel for few rows of an e4m3 cache) for the product with V.
+ * rounded to bf16 (f16 in the kernel for few rows of an e4m3 cache: off by 2^-11 of itself, or
+ * 2^-22 of the row's largest weight) for the product with V.
  * Results do not depend on timing: no atomics are used. o and lse must not overlap the inputs.
  * workspace: fcp_paged_attn_workspace_bytes, 256-byte aligned, its contents need not be
  * kept or cleared; calls whose work may overlap need one each. Errors: FCP_ERR_INVALID (also

@@ -54,3 +54,24 @@ def test_a_nan_in_v_reaches_its_readers(fcp, at, b, c):
     else:
         assert o[:, :n][:, sees].isnan().all()
         assert torch.equal(o[:, :n][:, ~sees], want[0][:, :n][:, ~sees])
+
+
+# ---------------------------------------------------------------- V's scales far apart
+@pytest.mark.parametrize("new", [1, 2, 3, 8, 50], ids=lambda n: f"new{n}")
+@pytest.mark.parametrize("apart", [6, 11, 18, 24, 40, 90])
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_rows_of_v_beside_large_ones(fcp, new, apart, d):
+    """Every ninth row of V is 2^apart larger than the rest, and zero but for one channel: the other
+    channels are sums over the small rows alone, which must not be lost beside it."""
+    b = Batch([new, 1], [300, 77], hq=4, hkv=1, d=d, page=32, cache="e4m3", seed=apart)
+    t = U.make(b)
+    codes, byte = t["v_pages"].view(torch.uint8), t["v_scales"].view(torch.uint8)
+    large = torch.zeros_like(byte, dtype=torch.bool)
+    large[:, :, 4::9] = True
+    large &= byte != 255
+    byte.copy_(torch.where(large, 117 + apart // 2, torch.where(byte == 255, 255, byte - (apart + 1) // 2)).to(torch.uint8))
+    codes.masked_fill_(large[..., None] & (torch.arange(d, device="cuda") != 5), 0)
+    cache, batch = U.handles(fcp, b, t)
+    o, lse, before = attend(fcp, b, t, cache, batch)
+    cache.check_device_error()
+    U.check_attention(b, t, o, lse, *before)
