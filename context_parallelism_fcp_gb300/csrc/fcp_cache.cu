@@ -86,34 +86,56 @@ __device__ __forceinline__ void find_places(const PagedArgs& p, int t0, TokenPla
     if (step == 1 && j < p.n_seqs) lens[j] = load(p.lens + j);
   }
   __syncthreads();
+  const int t = t0 + threadIdx.x;
+  const bool mine = threadIdx.x < kMoveTokens && t < p.total_new;
+  auto shape = [&](int i, bool report) {
+    return step == 1 ? checked_shape(p, coarse[i], coarse[i + 1], lens[i], report) : seq_shape(p, i, report);
+  };
+  int i = 0;
+  SeqShape s{0, 0, 0};
+  if (mine) {
+    int lo = 0, hi = n_coarse;  // coarse[lo] <= t < coarse[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (coarse[mid] <= t) lo = mid; else hi = mid;
+    }
+    i = lo * step;
+    int e = min(i + step, p.n_seqs);
+    while (e - i > 1) {
+      const int mid = (i + e) >> 1;
+      if (load(p.cu + mid) <= t) i = mid; else e = mid;
+    }
+    if (i < p.n_seqs) s = shape(i, true);
+  }
+  const bool lost = mine && (s.n == 0 || t < s.a || t >= s.a + s.n);
+  if (__syncthreads_or(lost)) {
+    // Rows before the first sequence and behind the last, but also rows of a batch whose offsets fall
+    // back, in which the search may miss the sequence that owns one: every sequence is asked.
+    int* owner = reinterpret_cast<int*>(place);
+    if (threadIdx.x < kMoveTokens) owner[threadIdx.x] = -1;
+    __syncthreads();
+    for (int k = threadIdx.x; k < p.n_seqs; k += kMoveThreads) {
+      const SeqShape z = shape(k, false);
+      if (z.n > 0)
+        for (int x = max(z.a - t0, 0); x < min(z.a + z.n - t0, kMoveTokens); ++x) atomicMax(&owner[x], k);
+    }
+    __syncthreads();
+    if (lost) {
+      i = owner[threadIdx.x];
+      s = i >= 0 ? shape(i, false) : SeqShape{0, 0, 0};
+    }
+    __syncthreads();
+  }
   if (threadIdx.x < kMoveTokens) {
-    const int t = t0 + threadIdx.x;
     TokenPlace r{-1, 0};
-    if (t < p.total_new) {
-      int lo = 0, hi = n_coarse;  // coarse[lo] <= t < coarse[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (coarse[mid] <= t) lo = mid; else hi = mid;
-      }
-      int i = lo * step, e = min(i + step, p.n_seqs);
-      while (e - i > 1) {
-        const int mid = (i + e) >> 1;
-        if (load(p.cu + mid) <= t) i = mid; else e = mid;
-      }
-      if (i < p.n_seqs) {
-        const SeqShape s = step == 1 ? checked_shape(p, coarse[i], coarse[i + 1], lens[i], true) : seq_shape(p, i, true);
-        if (t >= s.a && t < s.a + s.n) {
-          const int pos = s.len - s.n + (t - s.a);
-          if (pos >= 0) {
-            const int page = load(p.table + static_cast<long long>(i) * p.max_pages + (pos >> p.page_shift));
-            if (page >= 0 && page < p.n_pages) {
-              r.page = page;
-              r.off = pos & ((1 << p.page_shift) - 1);
-            } else {
-              atomicCAS(p.status, 0, kErrCachePage);
-            }
-          }
-        }
+    const int pos = s.n > 0 ? s.len - s.n + (t - s.a) : -1;
+    if (pos >= 0) {
+      const int page = load(p.table + static_cast<long long>(i) * p.max_pages + (pos >> p.page_shift));
+      if (page >= 0 && page < p.n_pages) {
+        r.page = page;
+        r.off = pos & ((1 << p.page_shift) - 1);
+      } else {
+        atomicCAS(p.status, 0, kErrCachePage);
       }
     }
     place[threadIdx.x] = r;

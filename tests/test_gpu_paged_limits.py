@@ -1,7 +1,9 @@
 """The paged cache where its inputs are far from ordinary."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import paged as R
 from tests import paged_util as U
 from tests.paged_util import Batch
 from tests.test_gpu_paged import attend
@@ -75,3 +77,82 @@ def test_small_rows_of_v_beside_large_ones(fcp, new, apart, d):
     o, lse, before = attend(fcp, b, t, cache, batch)
     cache.check_device_error()
     U.check_attention(b, t, o, lse, *before)
+
+
+# ---------------------------------------------------------------- offsets that fall back
+BROKEN = [
+    # cu, total, the sequences that own rows
+    ([0, 2, 5, 1000, 8, 10], 10, [0, 1, 4]),
+    ([0, 9, 2, 4, 3], 8, [2]),
+    ([5, 7, 1, 3, 900, 7, 9], 9, [0, 2, 5]),
+    ([-4, 5, 7, 2, 2, 5, 99], 7, [1, 4]),
+]
+
+
+def _broken(c, cu, total, owners, many, seed=0):
+    """A batch of len(cu) - 1 sequences with these offsets; many: that many empty sequences more in front
+    and behind, so that offsets are searched in two steps."""
+    n = len(cu) - 1
+    new = [max(0, cu[i + 1] - cu[i]) if 0 <= cu[i] <= cu[i + 1] <= total else 0 for i in range(n)]
+    b = Batch([0] * many + new + [0] * many, [20 + i % 30 for i in range(n + 2 * many)], hq=2, hkv=2, cache=c, seed=seed)
+    t = U.make(b)
+    t["cu"] = torch.tensor([cu[0]] * many + cu + [cu[-1]] * many, dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(seed)
+    for x, h in (("q", b.hq), ("k", b.hkv), ("v", b.hkv)):
+        t[x] = torch.randn(h, total, b.d, generator=g).to(torch.bfloat16).cuda()
+    cache = fcp_cache(t)
+    return b, t, cache
+
+
+def fcp_cache(t):
+    import context_parallelism_fcp_gb300 as pkg
+
+    return pkg.PagedCache.wrap(t["k_pages"], t["v_pages"], t["k_scales"], t["v_scales"])
+
+
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+@pytest.mark.parametrize("many", [0, 700])
+@pytest.mark.parametrize("cu,total,owners", BROKEN, ids=lambda x: None)
+def test_rows_behind_a_bad_offset_are_written_and_read(fcp, cu, total, owners, many, c):
+    """A bad offset in front of a good sequence: its rows are found, and every other byte stays."""
+    b, t, cache = _broken(c, cu, total, owners, many)
+    batch = fcp.CacheBatch(t["cu"], t["lens"], t["table"], total, max_new=total)
+    table = t["table"].cpu().numpy()
+    place = {}  # packed row -> page, row of the page
+    for i in owners:
+        n = cu[i + 1] - cu[i]
+        for j in range(n):
+            pos = b.lens[many + i] - n + j
+            assert cu[i] + j not in place and pos >= 0
+            place[cu[i] + j] = int(table[many + i, pos // b.page]), pos % b.page
+    # read
+    k, v = torch.full_like(t["k"], 3.0), torch.full_like(t["v"], -3.0)
+    fcp.cache_read(cache, batch, k, v)
+    with pytest.raises(fcp.FcpError, match="0x50"):
+        cache.check_device_error()
+    for got, fill, x in ((k, 3.0, "k"), (v, -3.0, "v")):
+        stored = U.values(t[x + "_pages"], t[x + "_scales"])
+        want = np.full(got.shape, fill)
+        for row, (pg, off) in place.items():
+            want[:, row] = stored[pg, :, off]
+        assert np.array_equal(got.double().cpu().numpy(), want)
+    # write
+    names = [x for x in ("k_pages", "v_pages", "k_scales", "v_scales") if t[x] is not None]
+    before = {x: t[x].clone() for x in names}
+    fcp.cache_write(cache, batch, t["k"], t["v"])
+    with pytest.raises(fcp.FcpError, match="0x50"):
+        cache.check_device_error()
+    for x in "kv":
+        rows = t[x].cpu()
+        if c == "bf16":
+            want = before[x + "_pages"].view(torch.int16).cpu().clone()
+            for row, (pg, off) in place.items():
+                want[pg, :, off] = rows[:, row].view(torch.int16)
+            assert torch.equal(t[x + "_pages"].view(torch.int16).cpu(), want)
+        else:
+            want, byte = (before[x + y].view(torch.uint8).cpu().numpy().copy() for y in ("_pages", "_scales"))
+            for row, (pg, off) in place.items():
+                for h in range(b.hkv):
+                    want[pg, h, off], byte[pg, h, off] = R.quantise_row(rows[h, row].double().numpy())
+            assert np.array_equal(t[x + "_pages"].view(torch.uint8).cpu().numpy(), want)
+            assert np.array_equal(t[x + "_scales"].view(torch.uint8).cpu().numpy(), byte)
