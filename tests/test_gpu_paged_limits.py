@@ -156,3 +156,89 @@ def test_rows_behind_a_bad_offset_are_written_and_read(fcp, cu, total, owners, m
                     want[pg, h, off], byte[pg, h, off] = R.quantise_row(rows[h, row].double().numpy())
             assert np.array_equal(t[x + "_pages"].view(torch.uint8).cpu().numpy(), want)
             assert np.array_equal(t[x + "_scales"].view(torch.uint8).cpu().numpy(), byte)
+
+
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+@pytest.mark.parametrize("max_new", [1, 100], ids=["few", "chunk"])
+@pytest.mark.parametrize("cu,total,owners", BROKEN, ids=lambda x: None)
+def test_rows_behind_a_bad_offset_are_attended(fcp, cu, total, owners, max_new, c):
+    """The same batches' attention: the good sequences' rows are theirs alone, others stay."""
+    b, t, cache = _broken(c, cu, total, owners, 0)
+    batch = fcp.CacheBatch(t["cu"], t["lens"], t["table"], total, max_new=max_new)
+    b.pad = total - sum(b.new)  # the outputs have `total` rows
+    o, lse, before = attend(fcp, b, t, cache, batch)
+    with pytest.raises(fcp.FcpError, match="0x50"):
+        cache.check_device_error()
+    rest = torch.ones(total, dtype=torch.bool, device="cuda")
+    for i in owners:
+        a, e = cu[i], cu[i + 1]
+        rest[a:e] = False
+        one = Batch([e - a], [b.lens[i]], hq=b.hq, hkv=b.hkv, cache=c)
+        u = dict(t, table=t["table"][i:i + 1], q=t["q"][:, a:e])
+        U.check_attention(one, u, o[:, a:e], lse[:, a:e])
+    assert torch.equal(o[:, rest], before[0][:, rest]) and torch.equal(lse[:, rest], before[1][:, rest])
+
+
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page_id", [1 << 30, -1])
+def test_pages_outside_the_cache(fcp, page_id, c):
+    """Attention counts the keys of a page outside the cache as zeros, in K and in V; a write and a read
+    leave their rows out; the rest of the batch is what it was."""
+    b = Batch([3, 40, 2], [70, 80, 33], hq=4, hkv=2, cache=c, pad=2)
+    t = U.make(b)
+    bad = [(0, 1), (1, 4), (2, 2)]  # sequence, entry: the second holds new tokens of its own
+    held = dict(t)
+    for x in ("k_pages", "v_pages"):
+        held[x] = torch.cat([t[x].view(torch.uint8 if c == "e4m3" else torch.bfloat16),
+                             torch.zeros_like(t[x][:1].view(torch.uint8 if c == "e4m3" else torch.bfloat16))]).view(t[x].dtype)
+        if c == "e4m3":
+            y = x[0] + "_scales"
+            held[y] = torch.cat([t[y].view(torch.uint8), torch.full_like(t[y][:1].view(torch.uint8), 127)]).view(t[y].dtype)
+    zero = t["k_pages"].shape[0]  # a page of zeros that the oracle looks at in their place
+    table = t["table"].clone()
+    held["table"] = t["table"].clone()
+    for i, e in bad:
+        table[i, e] = page_id
+        held["table"][i, e] = zero
+    t["table"] = table
+    cache = fcp_cache(t)
+    for max_new in (1, 100):
+        batch = fcp.CacheBatch(t["cu"], t["lens"], t["table"], b.total, max_new=max_new)
+        o, lse, before = attend(fcp, b, t, cache, batch)
+        with pytest.raises(fcp.FcpError, match="0x51"):
+            cache.check_device_error()
+        U.check_attention(b, held, o, lse, *before)
+    places = [x for x in R.places(b.new, b.lens, table.cpu().numpy(), b.page) if 0 <= x[3] < zero]
+    assert 0 < len(places) < sum(b.new)
+    k, v = torch.full_like(t["k"], 3.0), torch.full_like(t["v"], -3.0)
+    fcp.cache_read(cache, batch, k, v)
+    with pytest.raises(fcp.FcpError, match="0x51"):
+        cache.check_device_error()
+    for got, fill, x in ((k, 3.0, "k"), (v, -3.0, "v")):
+        stored, want = U.values(t[x + "_pages"], t[x + "_scales"]), np.full(got.shape, fill)
+        for row, _, _, pg, off in places:
+            want[:, row] = stored[pg, :, off]
+        assert np.array_equal(got.double().cpu().numpy(), want)
+    names = [x for x in ("k_pages", "v_pages", "k_scales", "v_scales") if t[x] is not None]
+    before = {x: t[x].clone() for x in names}
+    fcp.cache_write(cache, batch, t["k"], t["v"])
+    with pytest.raises(fcp.FcpError, match="0x51"):
+        cache.check_device_error()
+    written = torch.zeros(t["k_pages"].shape[0], b.page, dtype=torch.bool)
+    for _, _, _, pg, off in places:
+        written[pg, off] = True
+    for x in names:
+        raw = lambda y: y.view(torch.int16 if y.element_size() == 2 else torch.uint8).transpose(1, 2).cpu()  # noqa: E731
+        now, old = raw(t[x]), raw(before[x])
+        assert torch.equal(now[~written], old[~written]), x
+    fcp.cache_read(cache, batch, k, v)
+    with pytest.raises(fcp.FcpError, match="0x51"):
+        cache.check_device_error()
+    for row, *_ in places:
+        if c == "bf16":
+            assert torch.equal(k[:, row], t["k"][:, row]) and torch.equal(v[:, row], t["v"][:, row])
+        else:
+            for got, x in ((k, t["k"]), (v, t["v"])):
+                for h in range(b.hkv):
+                    codes, byte = R.quantise_row(x[h, row].double().cpu().numpy())
+                    assert np.array_equal(got[h, row].double().cpu().numpy(), R.row_value(codes, byte))
