@@ -356,12 +356,12 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
-          if (v > 0) w.next(a);
+          if (v > 0) w.next(a, line, w1);
           int ga = 0, gb = 0;
           while ((more = more && w.i < a.c.n_seqs && w.f0 < w1)) {
             w.part(w0, w1, ga, gb);
             if (gb > ga) break;
-            w.next(a);  // the share has the group's overhead only
+            w.next(a, line, w1);  // the share has the group's overhead only
           }
           volatile Unit* dst = unit_slot + k;
           dst->valid = more ? 1 : 0;

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     while ((p.valid = w.i < a.c.n_seqs && w.f0 < w1)) {
       w.part(w0, w1, p.ga, p.gb);
       if (p.gb > p.ga) break;
-      w.next(a);  // the share has the group's overhead only
+      w.next(a, line, w1);  // the share has the group's overhead only
     }
     if (p.valid) {
       p.i = w.i;
@@ -328,8 +328,9 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
     // while Q and the first chunks are on their way, in the warp that has the fewest
     if (threadIdx.x == kFewThreads - 32) {
       Walk<P> w = walk;
-      w.next(a);
-      advance(w, sh, sh.begin(b), sh.begin(b + 1), shared_piece[turn ^ 1]);
+      const long long w1 = sh.begin(b + 1);
+      w.next(a, line, w1);
+      advance(w, sh, sh.begin(b), w1, shared_piece[turn ^ 1]);
     }
 
     // e4m3: Q's rows as f16 scaled by 2^(14 - e), e the largest exponent of the row; `back` takes the

@@ -242,3 +242,38 @@ def test_pages_outside_the_cache(fcp, page_id, c):
                 for h in range(b.hkv):
                     codes, byte = R.quantise_row(x[h, row].double().cpu().numpy())
                     assert np.array_equal(got[h, row].double().cpu().numpy(), R.row_value(codes, byte))
+
+
+# ---------------------------------------------------------------- idle sequences
+@pytest.mark.parametrize("c", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 40], ids=["few", "chunk"])
+def test_thousands_of_idle_sequences(fcp, c, new):
+    """Busy sequences before, between and behind 30000 idle ones each: right, and in a time that is not that
+    of reading them one after another in one thread (100 ns each: 3 ms)."""
+    gap = 30000
+    new_, lens = [new, 0, new, 0, new], [300, 0, 700, 0, 20 + new]
+    b = Batch(new_, lens, hq=4, hkv=2, d=128, cache=c, seed=new)
+    t = U.make(b)
+    busy = [0, gap + 1, 2 * gap + 2]
+    n = 2 * gap + 3
+    table = torch.full((n, t["table"].shape[1]), -7, dtype=torch.int32, device="cuda")
+    lens_all = torch.full((n,), 5, dtype=torch.int32, device="cuda")
+    count = torch.zeros(n, dtype=torch.int32, device="cuda")
+    for at, i in zip(busy, (0, 2, 4)):
+        table[at], lens_all[at], count[at] = t["table"][i], t["lens"][i], new
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), count.cumsum(0)]).int()
+    cache = fcp_cache(t)
+    batch = fcp.CacheBatch(cu, lens_all, table, b.total, max_new=new)
+    o, lse, before = attend(fcp, b, t, cache, batch)
+    cache.check_device_error()
+    U.check_attention(b, t, o, lse, *before)
+    att, times = fcp.PagedAttention(cache, b.hq), []
+    for _ in range(4):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+        torch.cuda.synchronize()
+        start.record()
+        att.forward(batch, t["q"], o, lse)
+        end.record()
+        torch.cuda.synchronize()
+        times.append(start.elapsed_time(end))
+    assert min(times) < 1.5, times
