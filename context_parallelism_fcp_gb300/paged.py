@@ -3,7 +3,10 @@
 ``PagedCache`` holds one layer's pages, ``CacheBatch`` says which rows of a packed batch belong
 to which cached sequence, and ``cache_write``, ``cache_read`` and ``paged_attn`` are the C calls
 of the same names. As in the rest of the package the arguments are checked and marshalled here
-and all the work is done by the library's kernels, on the caller's stream.
+and all the work is done by the library's kernels, on the caller's stream. That may be any stream: what a
+cache or an attention allocates stays theirs until the work of every stream that they were used on is done.
+(Tensors of the caller's follow torch's rule: one that is used on another stream than its own and then dropped
+is the caller's to record there. A graph's tensors and objects have to outlive it.)
 """
 from __future__ import annotations
 
@@ -38,7 +41,37 @@ def _want(t, dtype, shape, index: int, name: str) -> None:
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
 
 
-class PagedCache:
+class _Owner:
+    """An object with device memory of its own that calls on any stream may use. The allocator knows that
+    memory as the stream's that was current when the object was made: so the object waits there until what
+    that stream did with it before is done, and lets the allocator know of every other stream that uses it."""
+
+    _foreign = False
+
+    def _own(self, tensors, index: int) -> None:
+        self._tensors, self._index = tensors, index
+        self._streams = {torch._C._cuda_getCurrentRawStream(index)}
+        with torch.cuda.device(index):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+
+    def _note(self, raw: int, stream) -> None:
+        """Called for a stream that is not in _streams yet."""
+        self._streams.add(raw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.current_stream(self._index) if stream is None else None
+        if stream is None or (raw != 0 and stream.stream_id == raw):
+            self._foreign = True  # made elsewhere, and perhaps destroyed before this object
+            return
+        for t in self._tensors:
+            t.record_stream(stream)
+
+    def __del__(self):
+        if self._foreign and torch is not None and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.synchronize(self._index)
+
+
+class PagedCache(_Owner):
     """K and V of one layer in pages (fcp_cache). ``dtype`` is torch.bfloat16, or
     torch.float8_e4m3fn for a cache that quantises each row as it is written, with a
     power-of-two scale for each token and head. Pages start as zeros."""
@@ -54,7 +87,7 @@ class PagedCache:
             pages = [p.view(dtype) for p in pages]
             scales = [torch.full(shape[:3], 127, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
                       for _ in range(2)]
-        self._setup(*pages, *scales)
+        self._setup(*pages, *scales, made=[*pages, *(x for x in scales if x is not None)])
 
     @classmethod
     def wrap(cls, k_pages, v_pages, k_scales=None, v_scales=None) -> "PagedCache":
@@ -64,7 +97,7 @@ class PagedCache:
         self._setup(k_pages, v_pages, k_scales, v_scales)
         return self
 
-    def _setup(self, k_pages, v_pages, k_scales, v_scales):
+    def _setup(self, k_pages, v_pages, k_scales, v_scales, made=()):
         if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in _DTYPES:
             raise TypeError("k_pages must be a torch tensor of bfloat16 or float8_e4m3fn")
         if k_pages.dim() != 4:
@@ -86,8 +119,9 @@ class PagedCache:
             raise ValueError(f"head_dim must be 64 or 128, got {self.head_dim}")
         if self.page_size not in (16, 32, 64, 128, 256, 512, 1024, 2048, 4096):
             raise ValueError(f"page_size must be a power of two from 16 to 4096, got {self.page_size}")
-        self.dtype, self.device, self._index = k_pages.dtype, k_pages.device, k_pages.get_device()
+        self.dtype, self.device = k_pages.dtype, k_pages.device
         self.status = torch.zeros(64, dtype=torch.int32, device=self.device)
+        self._own([self.status, *made], k_pages.get_device())
         self._struct = _CacheStruct(
             k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr() if quantised else None,
             v_scales.data_ptr() if quantised else None, self.status.data_ptr(), self.n_pages, self.hkv,
@@ -136,7 +170,10 @@ def _move(fn, name, cache: PagedCache, batch: CacheBatch, k, v, stream) -> None:
     shape = (cache.hkv, batch.total_new, cache.head_dim)
     _want(k, torch.bfloat16, shape, index, "k")
     _want(v, torch.bfloat16, shape, index, "v")
-    status = fn(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), _here(index, stream))
+    raw = _here(index, stream)
+    if raw not in cache._streams:
+        cache._note(raw, stream)
+    status = fn(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), raw)
     if status:
         _check(status, name)
 
@@ -166,7 +203,7 @@ def paged_attn(cache: PagedCache, batch: CacheBatch, q, o, lse, workspace, causa
             q.shape[0], stream)
 
 
-def _attend(fn, cache, batch, q, o, lse, workspace, workspace_bytes, causal, hq, stream) -> None:
+def _attend(fn, cache, batch, q, o, lse, workspace, workspace_bytes, causal, hq, stream, owner=None) -> None:
     index = cache._index
     if batch._index != index:
         raise ValueError("the batch and the cache must be on one device")
@@ -174,13 +211,18 @@ def _attend(fn, cache, batch, q, o, lse, workspace, workspace_bytes, causal, hq,
     _want(q, torch.bfloat16, shape, index, "q")
     _want(o, torch.bfloat16, shape, index, "o")
     _want(lse, torch.float32, shape[:2], index, "lse")
+    raw = _here(index, stream)
+    if raw not in cache._streams:
+        cache._note(raw, stream)
+    if owner is not None and raw not in owner._streams:
+        owner._note(raw, stream)
     status = fn(cache._ref, batch._ref, q.data_ptr(), hq, causal, o.data_ptr(), lse.data_ptr(), workspace,
-                workspace_bytes, _here(index, stream))
+                workspace_bytes, raw)
     if status:
         _check(status, "fcp_paged_attn")
 
 
-class PagedAttention:
+class PagedAttention(_Owner):
     """paged_attn with a workspace of its own, for one cache. Calls that may overlap on the GPU
     (other streams, replays of captured graphs) need one PagedAttention each."""
 
@@ -190,6 +232,7 @@ class PagedAttention:
         self.cache, self.hq, self.causal = cache, int(hq), bool(causal)
         self.workspace = torch.empty(int(lib().fcp_paged_attn_workspace_bytes(cache.head_dim)), dtype=torch.uint8,
                                      device=cache.device)
+        self._own([self.workspace], cache._index)
         self._call = lib().fcp_paged_attn, cache
         self._last = self.workspace.data_ptr(), self.workspace.nbytes, 1 if causal else 0, self.hq
 
@@ -203,5 +246,5 @@ class PagedAttention:
             with nullcontext() if stream is None else torch.cuda.stream(stream):
                 o = torch.empty_like(q) if o is None else o
                 lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse is None else lse
-        _attend(*self._call, batch, q, o, lse, *self._last, stream)
+        _attend(*self._call, batch, q, o, lse, *self._last, stream, self)
         return o, lse

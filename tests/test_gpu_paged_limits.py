@@ -277,3 +277,95 @@ def test_thousands_of_idle_sequences(fcp, c, new):
         torch.cuda.synchronize()
         times.append(start.elapsed_time(end))
     assert min(times) < 1.5, times
+
+
+# ---------------------------------------------------------------- streams
+def _busy(stream, seconds=0.05):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(2e9 * seconds))
+
+
+@pytest.mark.parametrize("kind", ["stream", "current", "handle", "external"])
+def test_objects_dropped_while_another_stream_works(fcp, kind):
+    """A cache and an attention made on one stream, used on another and dropped at once: their memory is not
+    handed out while the work is under way."""
+    b = Batch([1, 2], [3000, 700], hq=8, hkv=2, d=128)
+    t = U.make(b)
+    cache, batch = U.handles(fcp, b, t)
+    want = fcp.PagedAttention(cache, b.hq).forward(batch, t["q"])
+    o, lse = torch.zeros_like(t["q"]), torch.zeros(b.hq, b.total, device="cuda")
+    cache = fcp.PagedCache(*t["k_pages"].shape[:1], b.page, b.hkv, b.d)
+    cache.k_pages.copy_(t["k_pages"])
+    cache.v_pages.copy_(t["v_pages"])
+    att = fcp.PagedAttention(cache, b.hq)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    other = torch.cuda.ExternalStream(side.cuda_stream) if kind == "external" else side
+    _busy(side)
+    if kind == "current":
+        with torch.cuda.stream(side):
+            att.forward(batch, t["q"], o, lse)
+    else:
+        att.forward(batch, t["q"], o, lse, stream=side.cuda_stream if kind == "handle" else other)
+    mine = {x.data_ptr() for x in (att.workspace, cache.status, cache.k_pages, cache.v_pages)}
+    n, pages = att.workspace.numel(), cache.k_pages.numel()
+    del cache, att
+    over = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    over += [torch.empty(pages, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    over += [torch.empty(64, dtype=torch.int32, device="cuda") for _ in range(8)]
+    if not side.query():
+        assert not mine & {x.data_ptr() for x in over}
+    else:  # an object used on a stream of unknown life waits for the device when it is dropped
+        assert kind in ("handle", "external")
+    for x in over:
+        x.view(torch.uint8).fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_objects_made_on_a_busy_stream(fcp):
+    """Memory that the first stream has yet to write (a dropped tensor's, a new cache's zeros) is not used by
+    another stream before that is done."""
+    b = Batch([1, 2], [3000, 700], hq=8, hkv=2, d=128, page=64)
+    t = U.make(b)
+    cache, batch = U.handles(fcp, b, t)
+    want = fcp.PagedAttention(cache, b.hq).forward(batch, t["q"])
+    whole = fcp.CacheBatch(torch.tensor([0, 3000, 3700], dtype=torch.int32).cuda(), t["lens"], t["table"], 3700, max_new=3000)
+    k, v = (torch.empty(2, 3700, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    fcp.cache_read(cache, whole, k, v)
+    o, lse = torch.zeros_like(t["q"]), torch.zeros(b.hq, b.total, device="cuda")
+    n = fcp.lib().fcp_paged_attn_workspace_bytes(b.d)
+    torch.cuda.synchronize()
+    first, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    dropped = torch.empty(n, dtype=torch.uint8, device="cuda")
+    _busy(first)
+    dropped.fill_(255)
+    del dropped
+    other = fcp.PagedCache(cache.n_pages, b.page, b.hkv, b.d)
+    att = fcp.PagedAttention(other, b.hq)
+    with torch.cuda.stream(side):
+        fcp.cache_write(other, whole, k, v)
+        att.forward(batch, t["q"], o, lse)
+    torch.cuda.synchronize()
+    other.check_device_error()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_objects_made_inside_a_capture(fcp):
+    """Nothing in making a cache or an attention stops a capture, and a graph replays with them."""
+    b = Batch([1, 40], [300, 70], hq=4, hkv=2, d=64)
+    t = U.make(b)
+    cache, batch = U.handles(fcp, b, t)
+    want = fcp.PagedAttention(cache, b.hq).forward(batch, t["q"])
+    o, lse = torch.zeros_like(t["q"]), torch.zeros(b.hq, b.total, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = fcp.PagedCache.wrap(t["k_pages"], t["v_pages"])
+        att = fcp.PagedAttention(again, b.hq)
+        att.forward(batch, t["q"], o, lse)
+    for _ in range(2):
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    again.check_device_error()
