@@ -20,7 +20,7 @@ from typing import Optional, Sequence, Tuple
 
 import numpy as np
 
-__all__ = [
+_NAMES = [
     "FcpError",
     "Plan",
     "lib",
@@ -35,16 +35,12 @@ __all__ = [
     "block_attn_bwd_tiles_banded",
     "reshuffle",
     "FcpAttention",
-    "PagedCache",
-    "CacheBatch",
-    "cache_write",
-    "cache_read",
-    "paged_attn",
-    "PagedAttention",
     "MASK_FULL",
     "MASK_CAUSAL_DIAG",
     "EXPORTED_SYMBOLS",
 ]
+# of paged.py, which needs torch; importing the package (its host plan) does not
+_PAGED_NAMES = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention"]
 
 MASK_FULL = 0
 MASK_CAUSAL_DIAG = 1
@@ -622,9 +618,18 @@ class FcpAttention:
 
 
 def __getattr__(name):
-    # the paged cache needs torch, which importing the package (its host plan) does not
-    if name in ("PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention"):
+    if name == "__all__":  # what a star import takes: without torch, what works without it
+        try:
+            import torch  # noqa: F401
+        except ImportError:
+            return list(_NAMES)
+        return _NAMES + _PAGED_NAMES
+    if name in _PAGED_NAMES:
         from . import paged
 
         return getattr(paged, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), "__all__", *_PAGED_NAMES})
