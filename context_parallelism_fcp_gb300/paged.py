@@ -102,6 +102,8 @@ class PagedCache(_Owner):
             raise TypeError("k_pages must be a torch tensor of bfloat16 or float8_e4m3fn")
         if k_pages.dim() != 4:
             raise ValueError("k_pages must have shape [n_pages, Hkv, page_size, D]")
+        if k_pages.shape[1] == 0:
+            raise ValueError("k_pages must have a KV head at least")
         _need(k_pages, k_pages.dtype, None, "k_pages")
         _need(v_pages, k_pages.dtype, k_pages.shape, "v_pages")
         quantised = k_pages.dtype != torch.bfloat16

@@ -39,3 +39,14 @@ def test_a_star_import_takes_the_cache(fcp):
     exec("from context_parallelism_fcp_gb300 import *", names)
     assert names["PagedCache"] is fcp.PagedCache and names["Plan"] is fcp.Plan
     assert set(fcp.__all__) <= set(dir(fcp))
+
+
+@pytest.mark.parametrize("shape", [(2, 0, 16, 64), (0, 0, 16, 64)])
+def test_a_cache_without_heads_is_refused(fcp, shape):
+    import torch
+
+    pages = torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="KV head"):
+        fcp.PagedCache.wrap(pages, pages.clone())
+    with pytest.raises(ValueError, match="KV head"):
+        fcp.PagedCache(shape[0], shape[2], shape[1], shape[3], device="cpu")
