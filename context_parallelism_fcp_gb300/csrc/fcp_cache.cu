@@ -67,6 +67,7 @@ namespace {
 constexpr int kMoveThreads = 256;
 constexpr int kMoveTokens = 32;   // packed rows of a block
 constexpr int kCoarse = 1024;     // row offsets kept in shared memory
+constexpr int kEnough = 8;        // blocks of an SM: all that its threads allow
 
 // The cache row (page * page_size + offset, to which a head adds its stride) of each of the
 // block's tokens; -1 for rows behind the last sequence, rows before their sequence's first
@@ -285,21 +286,24 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
   }
 }
 
-// The launch overlaps the kernel before it in the stream where there is enough work that this
+// The launch overlaps the kernel before it in the stream where its blocks fill the GPU, so that this
 // is worth the call's extra microsecond and a half on the host.
 template <int D, bool kRead>
 fcp_status launch_move(const PagedArgs& p, int dtype, void* k, void* v, cudaStream_t s) {
   const unsigned bx = static_cast<unsigned>((p.total_new + kMoveTokens - 1) / kMoveTokens);
   // all heads stay in one block while that leaves enough blocks for the GPU (4 sequences of up to
   // 16384 tokens written: 17.0 us; with a quarter of the heads to a block 32.2)
+  int dev = 0, n_sm = 0;
+  if (const fcp_status st = this_device(&dev, &n_sm); st != FCP_OK) return st;
+  auto fills = [&](int heads) { return 2ll * bx * ((p.hkv + heads - 1) / heads) >= kEnough * n_sm; };
   int heads = p.hkv;
-  while (heads > 1 && 2ll * bx * ((p.hkv + heads - 1) / heads) < 1216) heads = (heads + 1) / 2;
+  while (heads > 1 && !fills(heads)) heads = (heads + 1) / 2;
   const dim3 grid(bx, static_cast<unsigned>((p.hkv + heads - 1) / heads), 2);
   uint4* pk = static_cast<uint4*>(k);
   uint4* pv = static_cast<uint4*>(v);
   auto* kernel = dtype == FCP_CACHE_E4M3 ? move_kernel<D, true, kRead> : move_kernel<D, false, kRead>;
   const char* where = kRead ? "cache read launch" : "cache write launch";
-  if (2ll * bx * grid.y >= 1216) return launch_overlapped(kernel, grid, kMoveThreads, 0, s, where, p, pk, pv, heads);
+  if (fills(heads)) return launch_overlapped(kernel, grid, kMoveThreads, 0, s, where, p, pk, pv, heads);
   kernel<<<grid, kMoveThreads, 0, s>>>(p, pk, pv, heads);
   FCP_CUDA_TRY(cudaGetLastError(), where);
   return FCP_OK;

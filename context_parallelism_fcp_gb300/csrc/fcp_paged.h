@@ -97,6 +97,19 @@ inline fcp_status launch_overlapped(void (*kernel)(Params...), dim3 grid, int th
   return FCP_OK;
 }
 
+// The current device and its number of SMs, which does not change.
+inline fcp_status this_device(int* dev, int* n_sm) {
+  static std::atomic<int> known[64];
+  FCP_CUDA_TRY(cudaGetDevice(dev), "paged cache device");
+  if (*dev < 0 || *dev >= 64) return FCP_ERR_UNSUPPORTED;
+  *n_sm = known[*dev].load(std::memory_order_relaxed);
+  if (*n_sm == 0) {
+    FCP_CUDA_TRY(cudaDeviceGetAttribute(n_sm, cudaDevAttrMultiProcessorCount, *dev), "paged cache SM count");
+    known[*dev].store(*n_sm, std::memory_order_relaxed);
+  }
+  return FCP_OK;
+}
+
 // cudaFuncSetAttribute for a kernel's dynamic shared memory, once for each device.
 template <class Kernel>
 inline fcp_status allow_smem(Kernel kernel, int bytes, int device, std::atomic<uint64_t>& done, const char* where) {

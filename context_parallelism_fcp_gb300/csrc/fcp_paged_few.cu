@@ -662,19 +662,6 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(con
   }
 }
 
-// The current device and its number of SMs, which does not change.
-fcp_status this_device(int* dev, int* n_sm) {
-  static std::atomic<int> known[64];
-  FCP_CUDA_TRY(cudaGetDevice(dev), "paged attention device");
-  if (*dev < 0 || *dev >= 64) return FCP_ERR_UNSUPPORTED;
-  *n_sm = known[*dev].load(std::memory_order_relaxed);
-  if (*n_sm == 0) {
-    FCP_CUDA_TRY(cudaDeviceGetAttribute(n_sm, cudaDevAttrMultiProcessorCount, *dev), "paged attention SM count");
-    known[*dev].store(*n_sm, std::memory_order_relaxed);
-  }
-  return FCP_OK;
-}
-
 template <int D, bool kE4M3, int NT>
 fcp_status launch_few(AttnArgs a, void* workspace, int dev, int n_sm, int max_new, cudaStream_t s) {
   using C = FewCfg<D, kE4M3, NT>;
