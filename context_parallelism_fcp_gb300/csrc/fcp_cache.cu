@@ -89,9 +89,6 @@ __device__ __forceinline__ void find_places(const PagedArgs& p, int t0, TokenPla
   __syncthreads();
   const int t = t0 + threadIdx.x;
   const bool mine = threadIdx.x < kMoveTokens && t < p.total_new;
-  auto shape = [&](int i, bool report) {
-    return step == 1 ? checked_shape(p, coarse[i], coarse[i + 1], lens[i], report) : seq_shape(p, i, report);
-  };
   int i = 0;
   SeqShape s{0, 0, 0};
   if (mine) {
@@ -106,7 +103,7 @@ __device__ __forceinline__ void find_places(const PagedArgs& p, int t0, TokenPla
       const int mid = (i + e) >> 1;
       if (load(p.cu + mid) <= t) i = mid; else e = mid;
     }
-    if (i < p.n_seqs) s = shape(i, true);
+    if (i < p.n_seqs) s = step == 1 ? checked_shape(p, coarse[i], coarse[i + 1], lens[i], true) : seq_shape(p, i, true);
   }
   const bool lost = mine && (s.n == 0 || t < s.a || t >= s.a + s.n);
   if (__syncthreads_or(lost)) {
@@ -115,15 +112,23 @@ __device__ __forceinline__ void find_places(const PagedArgs& p, int t0, TokenPla
     int* owner = reinterpret_cast<int*>(place);
     if (threadIdx.x < kMoveTokens) owner[threadIdx.x] = -1;
     __syncthreads();
-    for (int k = threadIdx.x; k < p.n_seqs; k += kMoveThreads) {
-      const SeqShape z = shape(k, false);
-      if (z.n > 0)
-        for (int x = max(z.a - t0, 0); x < min(z.a + z.n - t0, kMoveTokens); ++x) atomicMax(&owner[x], k);
+    for (int base = 0; base < p.n_seqs; base += kCoarse - 1) {
+      if (step > 1) {
+        __syncthreads();
+        for (int j = threadIdx.x; j < kCoarse; j += kMoveThreads) coarse[j] = load(p.cu + min(base + j, p.n_seqs));
+        __syncthreads();
+      }
+      for (int j = threadIdx.x; j < min(kCoarse - 1, p.n_seqs - base); j += kMoveThreads) {
+        if (coarse[j] >= t0 + kMoveTokens || coarse[j + 1] <= t0) continue;
+        const SeqShape z = seq_shape(p, base + j, false);
+        if (z.n > 0)
+          for (int x = max(z.a - t0, 0); x < min(z.a + z.n - t0, kMoveTokens); ++x) atomicMax(&owner[x], base + j);
+      }
     }
     __syncthreads();
     if (lost) {
       i = owner[threadIdx.x];
-      s = i >= 0 ? shape(i, false) : SeqShape{0, 0, 0};
+      s = i >= 0 ? seq_shape(p, i, false) : SeqShape{0, 0, 0};
     }
     __syncthreads();
   }
