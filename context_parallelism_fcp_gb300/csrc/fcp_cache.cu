@@ -10,8 +10,8 @@
 // Both directions are bound by HBM: 2 * T * Hkv rows in and out, nothing reused. A warp moves whole
 // rows, D / 8 lanes to a row, 16 bytes of bf16 to a lane; a block takes 32 tokens of all heads, whose
 // places are looked up once. Measured, D = 128: 27000 new tokens of 8 heads written into an e4m3
-// cache in 32.1 us (5240 GB/s, 77% of a copy's rate; the third round of blocks is a quarter full),
-// 169000 of 4 heads in 90 us (5780 GB/s), 35000 tokens of 8 heads read in 36.7 us (5830 GB/s); bf16
+// cache in 32.2 us (5220 GB/s, 77% of a copy's rate; the third round of blocks is a quarter full),
+// 169000 of 4 heads in 90 us (5780 GB/s), 35000 tokens of 8 heads read in 37 us (5800 GB/s); bf16
 // caches 6300 (write) to 7000 GB/s (read).
 // Writing e4m3 was bound by integer instructions (33.3 and 101 us) until pointers stepped along and
 // the clamp of the largest scale became a branch of its own.

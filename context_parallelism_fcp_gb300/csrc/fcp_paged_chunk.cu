@@ -20,9 +20,10 @@
 // Bound by the chain of each key tile, S -> softmax -> P -> PV, as the forward is: tensor memory has
 // no room for a second S of a tile; an e4m3 cache adds the loaders' instructions to the softmax's.
 // Measured (64 query, 8 KV heads, D = 128, alone): 2048 new tokens over 32768 keys 1330 us from a bf16
-// cache (1600 TFLOP/s) and 1735 us from an e4m3 one (1228), 8192 over 8192 750 and 959 us, 16 chunks
-// of 512 with nothing before them 156 and 189 us (a quarter of it writes o). Call after call the first
-// two are 1440 and 1880 us: blocks then land on other SMs, and the slowest decides.
+// cache (1600 TFLOP/s) and 1710 us from an e4m3 one (1245), 8192 over 8192 735 and 965 us, 16 chunks
+// of 512 with nothing before them 156 and 192 us (a quarter of it writes o; what a unit costs beside
+// its one to four key tiles is most of the rest). Call after call the first two are 1440 to 1520 and
+// 1880 us: blocks then land on other SMs, and the slowest decides.
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1 (thread = row = TMEM lane); 8: the walk along the
 // block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 only): loaders.

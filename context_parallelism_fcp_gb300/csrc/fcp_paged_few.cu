@@ -34,8 +34,10 @@
 // Measured (8 KV heads, D = 128): 128 e4m3 sequences of up to 8192 tokens, 8 query heads a KV head,
 // 150 us (5870 GB/s, 87% of a copy's rate); two bf16 sequences of 131072, 155 us (6900 GB/s, all of
 // it); 32 bf16 sequences of up to 4096 with 4 drafted tokens, 4 query heads a KV head, 39 us (5170
-// GB/s, 76%; the beginnings and ends of pieces are the rest). 10 sequences of up to 1000 take 9 us,
-// of which the lengths, the first rows and the merge are a dependent chain of memory latencies.
+// GB/s, 76%; the beginnings and ends of pieces are the rest), and 38 us from an e4m3 cache, whose half
+// as many bytes cost a conversion and two exponentials a weight (with 2 and 8 query heads a KV head 26.7
+// and 57.6 us). 10 sequences of up to 1000 take 9 us, of which the lengths, the first rows and the merge
+// are a dependent chain of memory latencies.
 #include <algorithm>
 #include <cmath>
 
@@ -55,8 +57,7 @@ constexpr float kUp = 7.0f;                 // e4m3: P starts at 2^7 and grows t
 // 2^gap below that of the largest is 2^(gap - 25 - kUp) of the largest weight. Up to this gap (2^-22)
 // that is left so; beyond it the rest of P counts too (which it has to: with gaps of 2^18 and more,
 // channels where the large row is zero were off by tens of times the rounding of P and o, or zero).
-// The test for it costs single tokens up to 1%, 32 x 4 tokens of 2, 4 and 8 heads 26.2 to 27.6, 38.1
-// to 38.6 and 58.5 to 57.6 us.
+// The test for it costs single tokens up to 1%, 32 x 4 tokens of 2 and 4 heads 2%, of 8 nothing.
 constexpr int kScaleGap = 10;
 constexpr float kLift = 0x1p28f;
 // Blocks to an SM and the shared memory of a block's stages, for NT tiles of 8 rows. bf16 is at

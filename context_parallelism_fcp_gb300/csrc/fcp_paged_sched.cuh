@@ -35,7 +35,8 @@ struct AttnArgs {
   const __nv_bfloat16* q;
   // Little work at most: the call after this one may start while the merge runs. (4 sequences of up
   // to 333 keys, call after call: 8.6 us instead of 10.4; with 128 of up to 8192 the next call's
-  // early blocks were in the way: 180 us instead of 171.)
+  // early blocks were in the way: 180 us instead of 171.) The host knows no lengths, only how many
+  // positions the block table has room for.
   int32_t small;
 };
 
