@@ -11,6 +11,7 @@ is the caller's to record there. A graph's tensors and objects have to outlive i
 from __future__ import annotations
 
 import ctypes
+import sys
 from contextlib import nullcontext
 from typing import Optional, Tuple
 
@@ -67,7 +68,7 @@ class _Owner:
             t.record_stream(stream)
 
     def __del__(self):
-        if self._foreign and torch is not None and not torch.cuda.is_current_stream_capturing():
+        if self._foreign and not sys.is_finalizing() and not torch.cuda.is_current_stream_capturing():
             torch.cuda.synchronize(self._index)
 
 

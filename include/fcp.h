@@ -363,10 +363,11 @@ fcp_status fcp_reshuffle(const fcp_plan* plan, const void* d_plan, const void* s
  *                      positions of a sequence (they would read as NaN or as 480)
  * all contiguous and 16-byte aligned. page_size is a power of two, 16 to 4096; D is 64 or 128.
  * status is one int32 on the device (16-byte aligned, zero at first), the error word of every
- * call that uses the cache; read and clear it with fcp_device_error. 0x50: a sequence's offsets or length do
- * not fit the batch (its rows are left as they were; a row that two sequences then claim is either's); 0x51: a block-table entry that was needed
- * lies outside [0, n_pages) (a write or read leaves its row out, attention counts its keys as
- * zeros). Neither stops the rest of the batch, and nothing outside the buffers is touched.
+ * call that uses the cache; read and clear it with fcp_device_error. 0x50: a sequence's offsets
+ * or length do not fit the batch (its rows are left as they were; a row that two others claim is
+ * either's); 0x51: a block-table entry that was needed lies outside [0, n_pages) (a write or read
+ * leaves its row out, attention counts its keys as zeros). Neither stops the rest of the batch,
+ * and nothing outside the buffers is touched.
  * 0x60 to 0x6f: a wait inside the attention ran out of its 2 seconds, 0x01: its shared memory
  * was misaligned; o and lse are then incomplete.
  *
