@@ -103,7 +103,8 @@ class _View(ctypes.Structure):
 
 class _CacheStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scales", "v_scales", "status")] + [
-        (n, ctypes.c_int32) for n in ("n_pages", "hkv", "page_size", "head_dim", "dtype", "reserved")]
+        (n, ctypes.c_int32) for n in ("n_pages", "hkv", "page_size", "head_dim", "dtype", "reserved")] + [
+        (n, ctypes.c_float) for n in ("k_unit", "v_unit")]
 
 
 class _CacheBatchStruct(ctypes.Structure):

@@ -1,5 +1,5 @@
 // Writing rows of K and V into the pages of a paged cache (quantising them where the cache is
-// e4m3), and reading them back as bf16.
+// e4m3 or e2m1), and reading them back as bf16.
 //
 // Row r = (token, KV head) with channels x: an e4m3 cache stores k = the smallest integer
 // >= -126 with max|x| <= 448 * 2^k, and the codes e4m3(x * 2^-k), rounded to nearest even: the
@@ -16,18 +16,25 @@
 // Writing e4m3 was bound by integer instructions (33.3 and 101 us) until pointers stepped along and
 // the clamp of the largest scale became a branch of its own.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "fcp_paged.h"
 
 namespace fcp {
 
+static bool good_unit(float u) {
+  int e = 0;
+  return u > 0.f && std::isfinite(u) && std::frexp(u, &e) == 0.5f && e >= -59 && e <= 61;
+}
+
 fcp_status paged_args(const fcp_cache* c, const fcp_cache_batch* b, PagedArgs* out) {
   if (c == nullptr || b == nullptr || out == nullptr) return FCP_ERR_INVALID;
   if (c->n_pages < 0 || c->hkv <= 0 || c->page_size <= 0 || b->n_seqs < 0 || b->max_pages < 0 || b->total_new < 0 ||
       b->max_new < 0)
     return FCP_ERR_INVALID;
-  if (c->dtype != FCP_CACHE_BF16 && c->dtype != FCP_CACHE_E4M3) return FCP_ERR_INVALID;
+  if (c->dtype != FCP_CACHE_BF16 && c->dtype != FCP_CACHE_E4M3 && c->dtype != FCP_CACHE_E2M1) return FCP_ERR_INVALID;
+  if (c->dtype == FCP_CACHE_E2M1 && !(good_unit(c->k_unit) && good_unit(c->v_unit))) return FCP_ERR_INVALID;
   if (c->head_dim != 64 && c->head_dim != 128) return FCP_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return FCP_ERR_UNSUPPORTED;
   if (static_cast<long long>(b->max_pages) * c->page_size > 1ll << 30) return FCP_ERR_UNSUPPORTED;
@@ -37,7 +44,7 @@ fcp_status paged_args(const fcp_cache* c, const fcp_cache_batch* b, PagedArgs* o
   if (!aligned4(b->cu_new) || !aligned4(b->lens) || !aligned4(b->block_table)) return FCP_ERR_INVALID;
   if (c->n_pages > 0) {
     if (!c->k_pages || !c->v_pages || !aligned16(c->k_pages) || !aligned16(c->v_pages)) return FCP_ERR_INVALID;
-    if (c->dtype == FCP_CACHE_E4M3 &&
+    if (c->dtype != FCP_CACHE_BF16 &&
         (!c->k_scales || !c->v_scales || !aligned16(c->k_scales) || !aligned16(c->v_scales)))
       return FCP_ERR_INVALID;
   }
@@ -57,6 +64,8 @@ fcp_status paged_args(const fcp_cache* c, const fcp_cache_batch* b, PagedArgs* o
   p.k_scales = c->k_scales;
   p.v_scales = c->v_scales;
   p.status = c->status;
+  p.k_unit = c->dtype == FCP_CACHE_E2M1 ? c->k_unit : 1.f;
+  p.v_unit = c->dtype == FCP_CACHE_E2M1 ? c->v_unit : 1.f;
   if (c->n_pages == 0) p.k_pages = p.v_pages = p.k_scales = p.v_scales = reinterpret_cast<uint8_t*>(c->status);
   *out = p;
   return FCP_OK;
@@ -192,10 +201,43 @@ __device__ __forceinline__ uint2 quantise(const uint4 x, uint32_t& scale_byte) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// Quantise the 8 channels of this lane to e2m1, with one e4m3 scale for them and its neighbour's 8:
+// 8 codes and the scale's byte. (Division by 6 and by the scale as products, rounded to 12 bits and to
+// 2^-13: quotients that lie on a border between two codes become that border exactly, and others are
+// at least 2^-9 of themselves away from one, since x has 8 significant bits and a border times a scale
+// at most 7. So this rounds as the quotients themselves would.)
+__device__ __forceinline__ uint32_t quantise4(const uint4 x, float per_unit, uint32_t& scale_byte) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t two = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+  two = max_u16x2(two, __shfl_xor_sync(0xffffffffu, two, 1));
+  const uint32_t top = max(two & 0xffffu, two >> 16);
+  const float sixth = __uint_as_float(top << 16) * per_unit * (1.f / 6.f);
+  const float s = __uint_as_float((__float_as_uint(sixth) + 0x800u) & ~0xfffu);
+  const uint32_t byte = max(static_cast<uint32_t>(__nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3)), 1u);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(e4m3_to_float(byte)));
+  inv *= per_unit;
+  constexpr float kRound = 1536.f;  // 1.5 * 2^10: sums near it are multiples of 2^-13
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 y = dev::ffma2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u), inv, inv, kRound, kRound);
+    y = dev::fadd2(y.x, y.y, -kRound, -kRound);
+    asm("{\n.reg .b8 b;\n.reg .b16 h;\ncvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\nmov.b16 h, {b, 0};\ncvt.u32.u16 %0, h;\n}"
+        : "=r"(c[i])
+        : "f"(y.y), "f"(y.x));
+  }
+  const bool finite = top < 0x7f80u;
+  scale_byte = finite ? byte : 0x7fu;
+  return finite ? __byte_perm(__byte_perm(c[0], c[1], 0x3240), __byte_perm(c[2], c[3], 0x3240), 0x5410) : 0u;
+}
+
 // grid (ceil(T / 32), ceil(Hkv / heads per block), 2: K or V)
-template <int D, bool kE4M3, bool kRead>
+template <int D, int kKind, bool kRead>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, uint4* k, uint4* v,
                                                             int heads) {
+  constexpr bool kE4M3 = kKind == FCP_CACHE_E4M3, kE2M1 = kKind == FCP_CACHE_E2M1;
+  constexpr int kScales = kE2M1 ? D / 16 : 1;      // scales of a row
   constexpr int LPR = D / 8;                       // lanes to a row
   constexpr int kPass = kMoveThreads / LPR;        // rows of one pass over the block
   constexpr int kPasses = kMoveTokens / kPass;     // passes to a head
@@ -209,7 +251,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
   // Rows of one head after another: everything steps by a constant. A thread's loads of kHeads heads
   // go out together, then they are converted and stored.
   constexpr int kHeads = 4 / kPasses;
-  using Cell = typename std::conditional<kE4M3, uint2, uint4>::type;  // 8 channels in a page
+  using Cell = std::conditional_t<kE2M1, uint32_t, std::conditional_t<kE4M3, uint2, uint4>>;  // 8 channels in a page
   const long long page_step = 1ll << p.page_shift, row_step = static_cast<long long>(p.total_new) * LPR;
   uint4* mine[kPasses];
   uint4 x[kHeads][kPasses];
@@ -241,8 +283,9 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
     at[i] = r.page >= 0;
     const long long row = at[i] ? page_row(p, r.page, h0) + r.off : 0;
     cells[i] = reinterpret_cast<Cell*>(blockIdx.z ? p.v_pages : p.k_pages) + row * LPR + l;
-    scales[i] = (blockIdx.z ? p.v_scales : p.k_scales) + row;
+    scales[i] = (blockIdx.z ? p.v_scales : p.k_scales) + row * kScales + (kE2M1 ? l / 2 : 0);
   }
+  const float unit = blockIdx.z ? p.v_unit : p.k_unit, per_unit = 1.f / unit;  // exact: powers of two
   for (int h = h0; h < h1; h += kHeads) {
     if constexpr (!kRead) {
       if (h > h0) load_rows(h);
@@ -259,6 +302,9 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
             x[y][i].x = c.x;
             x[y][i].y = c.y;
             byte[y][i] = scales[i][y * page_step];
+          } else if constexpr (kE2M1) {
+            x[y][i].x = cells[i][y * page_step * LPR];
+            byte[y][i] = scales[i][y * page_step * kScales];
           } else {
             x[y][i] = cells[i][y * page_step * LPR];
           }
@@ -271,12 +317,19 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
         const bool on = at[i] && h + y < h1;
         if constexpr (kRead) {
           if constexpr (kE4M3) x[y][i] = scaled8(make_uint2(x[y][i].x, x[y][i].y), e8m0_to_float(byte[y][i]));
+          if constexpr (kE2M1) x[y][i] = scaled8(x[y][i].x, e4m3_to_float(byte[y][i]) * unit);
           if (on) __stcs(mine[i] + y * row_step, x[y][i]);
         } else if constexpr (kE4M3) {
           const uint2 codes = quantise<LPR>(x[y][i], byte[y][i]);
           if (on) {
             cells[i][y * page_step * LPR] = codes;
             if (l == 0) scales[i][y * page_step] = static_cast<uint8_t>(byte[y][i]);
+          }
+        } else if constexpr (kE2M1) {
+          const uint32_t codes = quantise4(x[y][i], per_unit, byte[y][i]);
+          if (on) {
+            cells[i][y * page_step * LPR] = codes;
+            if ((l & 1) == 0) scales[i][y * page_step * kScales] = static_cast<uint8_t>(byte[y][i]);
           }
         } else if (on) {
           cells[i][y * page_step * LPR] = x[y][i];
@@ -286,7 +339,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedArgs p, u
     for (int i = 0; i < kPasses; ++i) {
       mine[i] += kHeads * row_step;
       cells[i] += kHeads * page_step * LPR;
-      scales[i] += kHeads * page_step;
+      scales[i] += kHeads * page_step * kScales;
     }
   }
 }
@@ -306,7 +359,9 @@ fcp_status launch_move(const PagedArgs& p, int dtype, void* k, void* v, cudaStre
   const dim3 grid(bx, static_cast<unsigned>((p.hkv + heads - 1) / heads), 2);
   uint4* pk = static_cast<uint4*>(k);
   uint4* pv = static_cast<uint4*>(v);
-  auto* kernel = dtype == FCP_CACHE_E4M3 ? move_kernel<D, true, kRead> : move_kernel<D, false, kRead>;
+  auto* kernel = dtype == FCP_CACHE_E2M1   ? move_kernel<D, FCP_CACHE_E2M1, kRead>
+                 : dtype == FCP_CACHE_E4M3 ? move_kernel<D, FCP_CACHE_E4M3, kRead>
+                                           : move_kernel<D, FCP_CACHE_BF16, kRead>;
   const char* where = kRead ? "cache read launch" : "cache write launch";
   if (fills(heads)) return launch_overlapped(kernel, grid, kMoveThreads, 0, s, where, p, pk, pv, heads);
   kernel<<<grid, kMoveThreads, 0, s>>>(p, pk, pv, heads);

@@ -1,10 +1,12 @@
-// Shared host/device definitions of the paged key/value cache: argument checks, the e8m0 and
-// e4m3 conversions, and a sequence's place in a batch.
+// Shared host/device definitions of the paged key/value cache: argument checks, the e8m0,
+// e4m3 and e2m1 conversions, and a sequence's place in a batch.
 //
 // A cache row is one (token, KV head): D channels of K or of V. Rows live in pages
 // [n_pages, Hkv, page_size, D], so the rows of one page and head are contiguous. In an e4m3
 // cache a row carries a power-of-two scale 2^k kept as the byte k + 127 (e8m0; 255 is NaN):
-// scaling by it is exact, so a row is rounded once when it is written and never again.
+// scaling by it is exact, so a row is rounded once when it is written and never again. A 4-bit cache
+// has an e4m3 scale s for each 16 channels and a power of two for the whole cache: a code has 2
+// significant bits and s has 4, so code * s is exact in f16 (at most 2688, multiples of 2^-10) and bf16.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,6 +43,7 @@ struct PagedArgs {
   uint8_t* k_scales;
   uint8_t* v_scales;
   int32_t* status;
+  float k_unit, v_unit;  // of a 4-bit cache; 1 otherwise
 };
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -64,6 +67,11 @@ __device__ __forceinline__ int load(const int32_t* p) {
 __device__ __forceinline__ uint32_t load(const uint8_t* p) {
   uint32_t x;
   asm volatile("ld.global.u8 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint32_t load(const uint16_t* p) {
+  uint32_t x;
+  asm volatile("{\n.reg .b16 h;\nld.global.b16 h, [%1];\ncvt.u32.u16 %0, h;\n}" : "=r"(x) : "l"(p));
   return x;
 }
 __device__ __forceinline__ uint2 load(const uint2* p) {
@@ -158,6 +166,21 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& lo, uin
       : "r"(four));
 }
 
+// Eight e2m1 codes as four f16x2 of neighbouring codes, exactly.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t eight, uint32_t (&r)[4]) {
+  asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %4;\ncvt.rn.f16x2.e2m1x2 %0, a;\ncvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\ncvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(eight));
+}
+
+// An e4m3 scale as float32.
+__device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
+  uint32_t lo, hi;
+  e4m3x4_to_f16x2(byte, lo, hi);
+  return __low2float(*reinterpret_cast<const __half2*>(&lo));
+}
+
 // 8 codes times their row's scale as 8 bf16 channels: the product with a power of two is exact in
 // float32, and exact in bf16 while it is a normal number there.
 __device__ __forceinline__ uint4 scaled8(const uint2 x, float scale) {
@@ -168,6 +191,19 @@ __device__ __forceinline__ uint4 scaled8(const uint2 x, float scale) {
   for (int i = 0; i < 4; ++i) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
     const float2 y = dev::fmul2(v.x, v.y, scale, scale);
+    r[i] = dev::pack_bf16(y.x, y.y);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// 8 e2m1 codes times a factor (a scale and the cache's unit) as 8 bf16 channels: exact as above.
+__device__ __forceinline__ uint4 scaled8(uint32_t codes, float factor) {
+  uint32_t h[4], r[4];
+  e2m1x8_to_f16x2(codes, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    const float2 y = dev::fmul2(v.x, v.y, factor, factor);
     r[i] = dev::pack_bf16(y.x, y.y);
   }
   return make_uint4(r[0], r[1], r[2], r[3]);

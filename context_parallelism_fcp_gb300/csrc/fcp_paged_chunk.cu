@@ -31,6 +31,7 @@
 // 256 + 128 t + D).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fcp_paged_sched.cuh"
 
@@ -40,10 +41,11 @@ namespace {
 using namespace dev;
 
 constexpr int kLoaders = 6;  // warps
-template <bool kE4M3>
-constexpr int kThreads = 32 * (10 + (kE4M3 ? kLoaders : 0));
+template <int kKind>
+constexpr int kThreads = 32 * (10 + (kKind != FCP_CACHE_BF16 ? kLoaders : 0));
 constexpr int kPanelBytes = kTileM * 128;  // 128 rows x 64 bf16 channels
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr float kUp = 7.0f;                 // e2m1: P starts at 2^7 and grows to 2^15, the top of f16
 constexpr int kQBox = 16;                   // tokens of a TMA load of Q for tiles of several heads
 // Registers a thread with the loader warps: the launch gives 128, and the softmax warps take
 // what the others leave (they hold a row of 128 scores).
@@ -64,7 +66,8 @@ enum : int {
   B_DRAIN = 20,
   B_TFULL = 21,   // 2 slots: the next unit is published
   B_TEMPTY = 23,  // 2 slots: the MMA, softmax and loader warps have read it
-  B_COUNT = 25
+  B_QREADY = 25,  // e2m1, per tile: Q is f16
+  B_COUNT = 27
 };
 
 // A block's piece of a group: key tiles [kt0, kt1) of unit u.
@@ -91,8 +94,10 @@ struct Cfg {
   static constexpr int kSmemBytes = kEnd > 118 * 1024 ? kEnd : 118 * 1024;
   static_assert(kStage % 16 == 0, "16-byte aligned staging");
   static_assert(kSmemBytes <= 232448, "shared memory per block");
-  static constexpr uint32_t kIdescS = idesc_bf16(kTileM, kTileN, false, false);
-  static constexpr uint32_t kIdescPV = idesc_bf16(kTileM, D, false, true);
+  template <int kKind>
+  static constexpr uint32_t kIdescS = (kKind == FCP_CACHE_E2M1 ? idesc_f16 : idesc_bf16)(kTileM, kTileN, false, false);
+  template <int kKind>
+  static constexpr uint32_t kIdescPV = (kKind == FCP_CACHE_E2M1 ? idesc_f16 : idesc_bf16)(kTileM, D, false, true);
 };
 
 // 8 codes times 2^-120 as bf16: a code's exponent and mantissa moved to bf16's fields, four codes
@@ -115,12 +120,52 @@ __device__ __forceinline__ void times(uint32_t (&r)[4], uint32_t f) {
   }
 }
 
-template <int D, bool kE4M3>
-__global__ void __launch_bounds__(kThreads<kE4M3>, 1)
+__device__ __forceinline__ uint32_t times_f16(uint32_t x, uint32_t f) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Row r of a tile of Q in shared memory from bf16 to f16 in place, scaled by 2^(14 - e) with e the row's
+// largest exponent; returns 2^(e - 14). A lane begins at its own 16 bytes of a row, so that neighbours
+// are on different banks.
+template <int D>
+__device__ __forceinline__ float q_to_f16(uint8_t* tile, int r) {
+  uint32_t top = 0;
+  auto piece = [&](int c) -> uint4* {
+    return reinterpret_cast<uint4*>(tile + (c >> 3) * kPanelBytes + r * 128 + (((c + r) & 7) << 4));
+  };
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *piece(c);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  }
+  const int up = min(126, 141 - static_cast<int>(top >> 7));  // of rows past 2^-112
+  const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *piece(c);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = pack_f16(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+    *piece(c) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+}
+
+template <int D, int kKind>
+__global__ void __launch_bounds__(kThreads<kKind>, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ16,
                  const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
-  constexpr int kThreads = fcp::kThreads<kE4M3>;
+  constexpr int kThreads = fcp::kThreads<kKind>;
+  constexpr bool kLoad = kKind != FCP_CACHE_BF16, kE2M1 = kKind == FCP_CACHE_E2M1;
   using C = Cfg<D>;
   using P = ChunkRows;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -183,12 +228,13 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   };
 
   if (threadIdx.x == 0) {
+    constexpr int kFull = kE2M1 ? 4 : (kLoad ? 8 : 1);
     mbar_init(bar(B_QFULL), 1);
     mbar_init(bar(B_QEMPTY), 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_KFULL + s), kE4M3 ? 8 : 1);  // one arrival per 16 rows, or the copies' bytes
+      mbar_init(bar(B_KFULL + s), kFull);  // one arrival per group of rows, or the copies' bytes
       mbar_init(bar(B_KEMPTY + s), 1);
-      mbar_init(bar(B_VFULL + s), kE4M3 ? 8 : 1);
+      mbar_init(bar(B_VFULL + s), kFull);
       mbar_init(bar(B_VEMPTY + s), 1);
       mbar_init(bar(B_SFULL + s), 1);
       mbar_init(bar(B_PFULL + 2 * s), 4);  // one arrival per softmax warp of the tile
@@ -196,7 +242,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       mbar_init(bar(B_ODONE + s), 1);
       mbar_init(bar(B_OFREE + s), 4);
       mbar_init(bar(B_TFULL + s), 1);
-      mbar_init(bar(B_TEMPTY + s), 9 + (kE4M3 ? kLoaders : 0));
+      mbar_init(bar(B_TEMPTY + s), 9 + (kLoad ? kLoaders : 0));
+      mbar_init(bar(B_QREADY + s), 4);
     }
     mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0;
@@ -213,7 +260,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 8) {
-    if constexpr (kE4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if constexpr (kLoad) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp >= 10) {
       // ---------------------------------------------------------- loaders (e4m3)
       // The work is 16-row groups, each in one page: K's eight of a tile, V's eight, the next tile's.
@@ -242,6 +289,94 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       bool ok = true;
       int J0 = 0;                            // key tiles before this unit
       int g1 = order, g2 = g1 + step();      // the group held, and the next
+      if constexpr (kE2M1) {
+        // Groups of 32 rows, in two pages where those are of 16: K's four of a tile, V's four. A lane has
+        // 32 codes, 16 bytes, of rows r0 + kStep4 x; eight lanes store at a time, of four rows and two
+        // neighbouring pieces, which the swizzle puts on different banks. A code is exact in f16, and so
+        // is its product with its scale: two operations for two codes, where bf16 would take five.
+        constexpr int kStep4 = D == 128 ? 8 : 16, kLoads4 = 32 / kStep4, kScales = D / 16;
+        const int c4 = D == 128 ? (lane & 1) | ((lane >> 2) & 2) : lane & 1;
+        const int row0 = D == 128 ? ((lane >> 1) & 3) | ((lane >> 2) & 4) : lane >> 1;
+        for (int v = 0; ok; ++v) {
+          const Unit t = next_unit(v, kErrPagedWait + 1);
+          if (t.valid <= 0) break;
+          const int* table = a.c.table + static_cast<long long>(t.i) * a.c.max_pages;
+          const int g_end = (J0 + t.kt1 - t.kt0) * 8;
+          auto first_key = [&](int g) -> int { return (t.kt0 + (g >> 3) - J0) * kTileN + 32 * (g & 3); };
+          auto lookup = [&](int g, int half) -> int {  // of 16 rows of group g; -1: nothing to read
+            const int key = first_key(g) + 16 * half;
+            return g < g_end && key < t.len ? load(table + (key >> a.c.page_shift)) : -1;
+          };
+          uint4 raw[kLoads4];
+          uint32_t two[kLoads4];  // the scales of a row's 32 codes; zeros where there is no row
+          auto fetch = [&](int g, int page_a, int page_b) {
+            const int key0 = first_key(g);
+            const bool is_v = (g & 4) != 0;
+            const uint8_t* codes = is_v ? a.c.v_pages : a.c.k_pages;
+            const uint8_t* scales = is_v ? a.c.v_scales : a.c.k_scales;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int key = key0 + 16 * half, page = half ? page_b : page_a;
+              const bool in = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.n_pages);
+              if (!in && g < g_end && key < t.len) atomicCAS(err, 0, kErrCachePage);
+              const long long row = (in ? page_row(a.c, page, t.h) + (key & page_mask) : 0) + row0;
+              const int held = in ? t.len - key - row0 : 0;  // rows row0 + kStep4 x with kStep4 x below it are there
+#pragma unroll
+              for (int y = 0; y < kLoads4 / 2; ++y) {
+                const int x = half * (kLoads4 / 2) + y;
+                two[x] = 0u;
+                raw[x] = make_uint4(0u, 0u, 0u, 0u);
+                if (kStep4 * y < held) {
+                  raw[x] = load(reinterpret_cast<const uint4*>(codes + (row + kStep4 * y) * (D / 2) + 16 * c4));
+                  two[x] = load(reinterpret_cast<const uint16_t*>(scales + (row + kStep4 * y) * kScales + 2 * c4));
+                }
+              }
+            }
+          };
+          fetch(g1, lookup(g1, 0), lookup(g1, 1));
+          int page_a = lookup(g2, 0), page_b = lookup(g2, 1);
+          while (g1 < g_end) {
+            const int J = g1 >> 3, s = J & 1;  // the block's key tile
+            const bool is_v = (g1 & 4) != 0;
+            ok = mbar_wait(bar((is_v ? B_VEMPTY : B_KEMPTY) + s), ((J >> 1) & 1) ^ 1, abort_flag, err, kErrPagedWait + 2);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t* dst = smem + (is_v ? C::kV : C::kK) + s * C::kTileBytes;
+#pragma unroll
+            for (int x = 0; x < kLoads4; ++x) {
+              if (is_v) {  // a NaN scale of V becomes zero, and its key is kept
+                const bool n0 = (two[x] & 0x7fu) == 0x7fu, n1 = (two[x] & 0x7f00u) == 0x7f00u;
+                if (n0 || n1) {
+                  atomicMin(nan_key + (v & 3), first_key(g1) + row0 + kStep4 * x);
+                  two[x] &= (n0 ? 0u : 0xffu) | (n1 ? 0u : 0xff00u);
+                }
+              }
+              uint32_t both, none;
+              e4m3x4_to_f16x2(two[x], both, none);
+              const uint32_t f[2] = {__byte_perm(both, 0, 0x1010), __byte_perm(both, 0, 0x3232)};
+              const uint32_t word[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+              const int r = 32 * (g1 & 3) + row0 + kStep4 * x;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                uint32_t h[4];
+                e2m1x8_to_f16x2(word[y], h);
+                const int q = 4 * c4 + y;
+                *reinterpret_cast<uint4*>(dst + (q >> 3) * kPanelBytes + r * 128 + (((q ^ r) & 7) << 4)) =
+                    make_uint4(times_f16(h[0], f[y >> 1]), times_f16(h[1], f[y >> 1]), times_f16(h[2], f[y >> 1]),
+                               times_f16(h[3], f[y >> 1]));
+              }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive_warp(bar((is_v ? B_VFULL : B_KFULL) + s));
+            fetch(g2, page_a, page_b);
+            g1 = g2;
+            g2 += step();
+            page_a = lookup(g2, 0);
+            page_b = lookup(g2, 1);
+          }
+          J0 += t.kt1 - t.kt0;
+        }
+      } else
       for (int v = 0; ok; ++v) {
         const Unit t = next_unit(v, kErrPagedWait + 1);
         if (t.valid <= 0) break;
@@ -340,7 +475,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       if (lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmQ16);
-        if constexpr (!kE4M3) {
+        if constexpr (!kLoad) {
           tma_prefetch_desc(&tmK);
           tma_prefetch_desc(&tmV);
         }
@@ -366,7 +501,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           }
           volatile Unit* dst = unit_slot + k;
           dst->valid = more ? 1 : 0;
-          if constexpr (kE4M3) nan_key[v & 3] = INT32_MAX;
+          if constexpr (kLoad) nan_key[v & 3] = INT32_MAX;
           if (more) {
             dst->i = w.i;
             dst->a = w.s.a;
@@ -409,7 +544,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         bar(B_QFULL), p * 64, seq.a + tok, h * a.group + head);
         }
         last_q = v;
-        if constexpr (!kE4M3) {
+        if constexpr (!kLoad) {
           // A tile's pages, one to a lane; the next tile's are looked up while this one's loads go
           // out. Keys past the sequence and pages outside the cache take a box behind the last page,
           // which reads as zeros.
@@ -470,7 +605,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = (kk >> 2) * kPanelBytes + (kk & 3) * 32;
-          mma_ss_w(tmem + t * 128, sdesc_sw128(qbase + o, 16, 1024), sdesc_sw128(kbase + o, 16, 1024), C::kIdescS, kk > 0);
+          mma_ss_w(tmem + t * 128, sdesc_sw128(qbase + o, 16, 1024), sdesc_sw128(kbase + o, 16, 1024), C::template kIdescS<kKind>, kk > 0);
         }
       };
       // tiles processed so far by each of the two softmax groups, and units: their barriers'
@@ -487,7 +622,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           for (int k4 = 0; k4 < 4; ++k4) {
             const int kk = 4 * half + k4;
             mma_ts_w(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, sdesc_sw128(vbase + kk * 2048, kPanelBytes, 1024),
-                     C::kIdescPV, (acc || kk > 0));
+                     C::template kIdescPV<kKind>, (acc || kk > 0));
           }
         }
         return true;
@@ -498,7 +633,12 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         const Unit T = next_unit(v, kErrPagedWait + 6);
         if (T.valid <= 0) break;
         const int nt = P::tiles_of(SeqShape{T.a, T.n, T.len}, a.group, T.u);
-        ok = wwait(bar(B_QFULL), v & 1, kErrPagedWait + 7);
+        if constexpr (kE2M1) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) ok = ok && (t >= nt || wwait(bar(B_QREADY + t), ut[t] & 1, kErrPagedWait + 7));
+        } else {
+          ok = wwait(bar(B_QFULL), v & 1, kErrPagedWait + 7);
+        }
         if (!ok) break;
         tc_fence_after();
         // PV of key tile J - 1 (the unit's jl - 1) for tile t; the first overwrites O_t, which the
@@ -507,7 +647,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           const int ps = (J - 1) & 1;
           if (t == 0) {
             if (!wwait(bar(B_VFULL + ps), ((J - 1) >> 1) & 1, kErrPagedWait + 8)) return false;
-            if constexpr (!kE4M3) {
+            if constexpr (!kLoad) {
               // rows of the tile past the sequence, in its last page, become zeros
               const int held = T.len - (T.kt0 + jl - 1) * kTileN;
               if (held < kTileN) {
@@ -566,7 +706,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax (warps 0-7)
-    if constexpr (kE4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    if constexpr (kLoad) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -580,6 +720,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       const SeqShape seq{T.a, T.n, T.len};
       const ChunkRows::Shape z(seq, a.group);
       const int x = 2 * T.u + t;
+      if constexpr (kE2M1) {  // also for a unit of one tile, so that no phase is missed
+        ok = mbar_wait(bar(B_QFULL), v & 1, abort_flag, err, kErrPagedWait + 7);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
       if (x >= z.tiles) continue;  // a unit of one tile
       const ChunkRows::Tile tile = z.tile(x, a.group);
       int tok, head;
@@ -587,6 +732,13 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       const bool idle = !__any_sync(0xffffffffu, mine);  // a warp without a row keeps the barriers only
       // first key that this row does not see; rows that are not stored follow the fast path
       const int lim_row = !mine ? INT32_MAX : (a.causal ? max(0, T.len - T.n + tok + 1) : T.len);
+      float scale = a.scale_log2;
+      if constexpr (kE2M1) {
+        if (!idle) scale *= q_to_f16<D>(smem + C::kQ + t * C::kTileBytes, r);
+        fence_proxy_async_smem();
+        mbar_arrive_warp(bar(B_QREADY + t));
+      }
+      // what the row's weights are relative to: its maximum, in an e2m1 cache's f16 less kUp
       float m_used = -INFINITY;
       float l = 0.f;
       int jl = 0;
@@ -619,7 +771,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           mc[c] = fmaxf(mc[c], __uint_as_float(sv[32 * c + 31]));
         }
         const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-        const float m_new = fmaxf(m_used, mx * a.scale_log2);
+        const float m_new = fmaxf(m_used, kE2M1 ? fmaf(mx, scale, -kUp) : mx * scale);
         float alpha = 1.f;
         const bool grow = m_new > m_used + kRescaleThreshold;
         if (grow) {
@@ -627,7 +779,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
           m_used = m_new;
         }
         const float mb = (m_used == -INFINITY) ? 0.f : m_used;
-        // P (rounded to bf16: off by 2^-8 of itself at most) in two halves of 64 keys, each handed
+        // P (rounded to bf16: off by 2^-8 of itself at most; e2m1: to f16, by 2^-11 of itself or 2^-32 of
+        // the row's largest) in two halves of 64 keys, each handed
         // to the MMA warp as soon as it is stored
         float rowsum = 0.f;
 #pragma unroll
@@ -639,11 +792,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int i0 = 32 * c + 2 * e;
-              const float2 y = ffma2(__uint_as_float(sv[i0]), __uint_as_float(sv[i0 + 1]), a.scale_log2, a.scale_log2,
+              const float2 y = ffma2(__uint_as_float(sv[i0]), __uint_as_float(sv[i0 + 1]), scale, scale,
                                      -mb, -mb);
               const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
               acc2 = fadd2(acc2.x, acc2.y, p0, p1);
-              pk[e] = pack_bf16(p0, p1);
+              pk[e] = kE2M1 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
             }
             tmem_st16(s_addr + c * 16, pk);
           }
@@ -687,11 +840,13 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
       }
       float inv = T.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
       // every V of the unit has been loaded: its last PV is complete
-      const bool nan = kE4M3 && *const_cast<volatile int*>(nan_key + (v & 3)) < lim_row;
+      if constexpr (kE2M1) inv *= a.c.v_unit;
+      const bool nan = kLoad && *const_cast<volatile int*>(nan_key + (v & 3)) < lim_row;
       if (nan) inv = __uint_as_float(0x7fc00000u);
       // The warp's rows go through a shared block of 32 rows x 128 bytes (16-byte slots XOR-swizzled
       // by row), 64 bf16 or 32 float32 channels at a time, so that stores write whole row segments:
       // lane l writes slot l % 8 of rows l / 8 + 4 i
+      auto unit = [&](uint32_t y) -> uint32_t { return __float_as_uint(__uint_as_float(y) * a.c.v_unit); };
       uint8_t* stg = smem + C::kStage + warp * 4096;
       const int wrow = (warp & 3) * 32, sub = lane >> 3, e8 = lane & 7;
 #pragma unroll 1
@@ -708,7 +863,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<uint4*>(stg + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+                kE2M1 ? make_uint4(unit(ov[4 * e]), unit(ov[4 * e + 1]), unit(ov[4 * e + 2]), unit(ov[4 * e + 3]))
+                      : make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
           if (nan) {
 #pragma unroll 1
             for (int e = 0; e < 8; ++e)
@@ -763,13 +919,13 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
   }
 }
 
-template <int D, bool kE4M3>
+template <int D, int kKind>
 fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaStream_t s) {
   using C = Cfg<D>;
   CUtensorMap mq, mq16, mk = {}, mv = {};
   if (const fcp_status st = make_bf16_map(&mq, a.q, hq, a.c.total_new, D, kTileM); st != FCP_OK) return st;
   if (const fcp_status st = make_bf16_map(&mq16, a.q, hq, a.c.total_new, D, kQBox); st != FCP_OK) return st;
-  if constexpr (!kE4M3) {
+  if constexpr (kKind == FCP_CACHE_BF16) {
     // pages and heads are the maps' outer dimension; a box is a page's rows, at most a tile
     const long long outer = static_cast<long long>(a.c.n_pages) * a.c.hkv;
     if (outer + a.c.hkv > INT32_MAX) return FCP_ERR_UNSUPPORTED;
@@ -784,10 +940,10 @@ fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaSt
   const int blocks = std::max(2, std::min(n_sm, kMaxChunkBlocks) & ~1);
   set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
   static std::atomic<uint64_t> allowed{0};
-  if (const fcp_status st = allow_smem(chunk_kernel<D, kE4M3>, C::kSmemBytes, dev, allowed, "paged chunk smem attribute");
+  if (const fcp_status st = allow_smem(chunk_kernel<D, kKind>, C::kSmemBytes, dev, allowed, "paged chunk smem attribute");
       st != FCP_OK)
     return st;
-  if (const fcp_status st = launch_overlapped<kE4M3 ? 1 : 2>(chunk_kernel<D, kE4M3>, dim3(blocks), kThreads<kE4M3>, C::kSmemBytes, s,
+  if (const fcp_status st = launch_overlapped<kKind == FCP_CACHE_BF16 ? 2 : 1>(chunk_kernel<D, kKind>, dim3(blocks), kThreads<kKind>, C::kSmemBytes, s,
                                               "paged chunk launch", mq, mq16, mk, mv, a);
       st != FCP_OK)
     return st;
@@ -798,9 +954,13 @@ fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaSt
 
 fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int dev, int n_sm,
                               cudaStream_t s) {
-  if (dtype == FCP_CACHE_E4M3)
-    return d == 128 ? launch<128, true>(a, workspace, dev, n_sm, hq, s) : launch<64, true>(a, workspace, dev, n_sm, hq, s);
-  return d == 128 ? launch<128, false>(a, workspace, dev, n_sm, hq, s) : launch<64, false>(a, workspace, dev, n_sm, hq, s);
+  const auto run = [&](auto kind) {
+    constexpr int kKind = decltype(kind)::value;
+    return d == 128 ? launch<128, kKind>(a, workspace, dev, n_sm, hq, s) : launch<64, kKind>(a, workspace, dev, n_sm, hq, s);
+  };
+  if (dtype == FCP_CACHE_E2M1) return run(std::integral_constant<int, FCP_CACHE_E2M1>());
+  if (dtype == FCP_CACHE_E4M3) return run(std::integral_constant<int, FCP_CACHE_E4M3>());
+  return run(std::integral_constant<int, FCP_CACHE_BF16>());
 }
 
 }  // namespace fcp

@@ -11,6 +11,7 @@ is the caller's to record there. A graph's tensors and objects have to outlive i
 from __future__ import annotations
 
 import ctypes
+import math
 import sys
 from contextlib import nullcontext
 from typing import Optional, Tuple
@@ -21,7 +22,8 @@ from . import _CacheBatchStruct, _CacheStruct, _check, _need, _stream, device_er
 
 __all__ = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention"]
 
-_DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+_E2M1 = torch.float4_e2m1fn_x2  # two codes to an element
+_DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, _E2M1: 2}
 
 
 def _here(index: int, stream) -> int:
@@ -73,43 +75,54 @@ class _Owner:
 
 
 class PagedCache(_Owner):
-    """K and V of one layer in pages (fcp_cache). ``dtype`` is torch.bfloat16, or
-    torch.float8_e4m3fn for a cache that quantises each row as it is written, with a
-    power-of-two scale for each token and head. Pages start as zeros."""
+    """K and V of one layer in pages (fcp_cache). ``dtype`` is torch.bfloat16, or a smaller one
+    whose rows are quantised as they are written: torch.float8_e4m3fn with a power-of-two scale for
+    each token and head, or torch.float4_e2m1fn_x2 (two channels to an element) with an e4m3 scale
+    for every 16 channels, in units of ``k_unit`` for K and ``v_unit`` for V (powers of two; 16
+    channels may reach 2688 units, and lose bits below 0.09 units). Pages start as zeros."""
 
-    def __init__(self, n_pages: int, page_size: int, hkv: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
+    def __init__(self, n_pages: int, page_size: int, hkv: int, head_dim: int, dtype=torch.bfloat16, device="cuda",
+                 k_unit: float = 1.0, v_unit: float = 1.0):
         if dtype not in _DTYPES:
-            raise TypeError(f"dtype must be torch.bfloat16 or torch.float8_e4m3fn, got {dtype}")
-        shape = (int(n_pages), int(hkv), int(page_size), int(head_dim))
+            raise TypeError(f"dtype must be torch.bfloat16, torch.float8_e4m3fn or torch.float4_e2m1fn_x2, got {dtype}")
+        rows, head_dim = (int(n_pages), int(hkv), int(page_size)), int(head_dim)
+        if dtype == _E2M1 and head_dim not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+        shape = (*rows, head_dim // 2 if dtype == _E2M1 else head_dim)
         pages = [torch.zeros(shape, dtype=torch.uint8 if dtype != torch.bfloat16 else dtype, device=device)
                  for _ in range(2)]
         scales = [None, None]
         if dtype != torch.bfloat16:
             pages = [p.view(dtype) for p in pages]
-            scales = [torch.full(shape[:3], 127, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
-                      for _ in range(2)]
-        self._setup(*pages, *scales, made=[*pages, *(x for x in scales if x is not None)])
+            kind, one, size = ((torch.float8_e4m3fn, 0x38, (*rows, head_dim // 16)) if dtype == _E2M1
+                               else (torch.float8_e8m0fnu, 127, rows))
+            scales = [torch.full(size, one, dtype=torch.uint8, device=device).view(kind) for _ in range(2)]
+        self._setup(*pages, *scales, k_unit, v_unit, made=[*pages, *(x for x in scales if x is not None)])
 
     @classmethod
-    def wrap(cls, k_pages, v_pages, k_scales=None, v_scales=None) -> "PagedCache":
-        """A cache over pages that exist already ([n_pages, Hkv, page_size, D], and for e4m3 pages
-        the e8m0 scales [n_pages, Hkv, page_size])."""
+    def wrap(cls, k_pages, v_pages, k_scales=None, v_scales=None, k_unit: float = 1.0,
+             v_unit: float = 1.0) -> "PagedCache":
+        """A cache over pages that exist already: [n_pages, Hkv, page_size, D], for e4m3 pages with the
+        e8m0 scales [n_pages, Hkv, page_size]; or e2m1 pages [n_pages, Hkv, page_size, D / 2] with the
+        e4m3 scales [n_pages, Hkv, page_size, D / 16]."""
         self = cls.__new__(cls)
-        self._setup(k_pages, v_pages, k_scales, v_scales)
+        self._setup(k_pages, v_pages, k_scales, v_scales, k_unit, v_unit)
         return self
 
-    def _setup(self, k_pages, v_pages, k_scales, v_scales, made=()):
+    def _setup(self, k_pages, v_pages, k_scales, v_scales, k_unit, v_unit, made=()):
         if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in _DTYPES:
-            raise TypeError("k_pages must be a torch tensor of bfloat16 or float8_e4m3fn")
+            raise TypeError("k_pages must be a torch tensor of bfloat16, float8_e4m3fn or float4_e2m1fn_x2")
         if k_pages.dim() != 4:
             raise ValueError("k_pages must have shape [n_pages, Hkv, page_size, D]")
         if k_pages.shape[1] == 0:
             raise ValueError("k_pages must have a KV head at least")
         _need(k_pages, k_pages.dtype, None, "k_pages")
         _need(v_pages, k_pages.dtype, k_pages.shape, "v_pages")
-        quantised = k_pages.dtype != torch.bfloat16
+        quantised, packed = k_pages.dtype != torch.bfloat16, k_pages.dtype == _E2M1
         for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            if quantised:
+            if packed:
+                _need(t, torch.float8_e4m3fn, (*k_pages.shape[:3], k_pages.shape[3] // 8), name)
+            elif quantised:
                 _need(t, torch.float8_e8m0fnu, k_pages.shape[:3], name)
             elif t is not None:
                 raise ValueError(f"{name}: a bf16 cache has no scales")
@@ -118,6 +131,14 @@ class PagedCache(_Owner):
             raise ValueError("the cache's tensors must be on one device")
         self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
         self.n_pages, self.hkv, self.page_size, self.head_dim = (int(x) for x in k_pages.shape)
+        if packed:
+            self.head_dim *= 2
+        self.k_unit, self.v_unit = float(k_unit), float(v_unit)
+        for name, u in (("k_unit", self.k_unit), ("v_unit", self.v_unit)):
+            if not packed and u != 1.0:
+                raise ValueError(f"{name}: only a 4-bit cache has units")
+            if not 2.0 ** -60 <= u <= 2.0 ** 60 or math.frexp(u)[0] != 0.5:
+                raise ValueError(f"{name} must be a power of two from 2^-60 to 2^60, got {u}")
         if self.head_dim not in (64, 128):
             raise ValueError(f"head_dim must be 64 or 128, got {self.head_dim}")
         if self.page_size not in (16, 32, 64, 128, 256, 512, 1024, 2048, 4096):
@@ -128,7 +149,7 @@ class PagedCache(_Owner):
         self._struct = _CacheStruct(
             k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr() if quantised else None,
             v_scales.data_ptr() if quantised else None, self.status.data_ptr(), self.n_pages, self.hkv,
-            self.page_size, self.head_dim, _DTYPES[self.dtype], 0)
+            self.page_size, self.head_dim, _DTYPES[self.dtype], 0, self.k_unit, self.v_unit)
         self._ref = ctypes.byref(self._struct)
 
     def check_device_error(self, stream=None) -> None:
@@ -183,7 +204,7 @@ def _move(fn, name, cache: PagedCache, batch: CacheBatch, k, v, stream) -> None:
 
 def cache_write(cache: PagedCache, batch: CacheBatch, k, v, stream=None) -> None:
     """Write the new tokens' K and V (bf16 [Hkv, total_new, D]) into their pages, quantising them
-    where the cache is e4m3 (fcp_cache_write)."""
+    where the cache is e4m3 or e2m1 (fcp_cache_write)."""
     _move(lib().fcp_cache_write, "fcp_cache_write", cache, batch, k, v, stream)
 
 

@@ -361,6 +361,13 @@ fcp_status fcp_reshuffle(const fcp_plan* plan, const void* d_plan, const void* s
  *                      stands for code * 2^(byte - 127); byte 255 makes it NaN. Codes 0x7f and
  *                      0xff are never written and must not be in pages filled otherwise, at
  *                      positions of a sequence (they would read as NaN or as 480)
+ * or in 4 bits:
+ *   k_pages, v_pages   [n_pages, Hkv, page_size, D / 2] bytes of two e2m1 codes, the even channel in
+ *                      the low half
+ *   k_scales, v_scales [n_pages, Hkv, page_size, D / 16] e4m3: a code stands for code * scale * unit,
+ *                      with k_unit for K and v_unit for V, powers of two that the cache's maker
+ *                      chooses: sixteen channels up to 2688 units are held to 4 bits, and below
+ *                      0.09 units with less. Scales must not be negative; NaN makes its channels NaN
  * all contiguous and 16-byte aligned. page_size is a power of two, 16 to 4096; D is 64 or 128.
  * status is one int32 on the device (16-byte aligned, zero at first), the error word of every
  * call that uses the cache; read and clear it with fcp_device_error. 0x50: a sequence's offsets
@@ -382,7 +389,7 @@ fcp_status fcp_reshuffle(const fcp_plan* plan, const void* d_plan, const void* s
  * most; it only chooses the kernel (a wrong value costs time, never correctness). Several
  * sequences may share pages for reading; two rows written to one place in one call leave one
  * of them, or a mixture of both, there. */
-typedef enum { FCP_CACHE_BF16 = 0, FCP_CACHE_E4M3 = 1 } fcp_cache_dtype;
+typedef enum { FCP_CACHE_BF16 = 0, FCP_CACHE_E4M3 = 1, FCP_CACHE_E2M1 = 2 } fcp_cache_dtype;
 
 typedef struct {
   void* k_pages;
@@ -391,6 +398,7 @@ typedef struct {
   uint8_t* v_scales;
   int32_t* status;
   int32_t n_pages, hkv, page_size, head_dim, dtype, reserved;
+  float k_unit, v_unit; /* of a 4-bit cache, from 2^-60 to 2^60; not looked at otherwise */
 } fcp_cache;
 
 typedef struct {
@@ -404,9 +412,13 @@ typedef struct {
  * quantises each row: with k the smallest integer >= -126 such that max|x| <= 448 * 2^k (k = 0
  * for a row of zeros), the codes are x * 2^-k rounded to nearest even (at most 240 where k = 120:
  * 256 * 2^120 is past bf16's range) and the scale byte is k + 127; a row that holds an
- * infinity or NaN gets byte 255 and codes of zero. New tokens whose position is negative
+ * infinity or NaN gets byte 255 and codes of zero. A 4-bit cache takes for each 16 channels the
+ * scale max|x| / (6 * unit) rounded to e4m3 (to nearest, even codes at ties; 448 at most and 2^-9 at
+ * least) and the codes nearest to x / (scale * unit) (even ones at ties; 6 at most); channels with an
+ * infinity or NaN among them get scale NaN and codes of zero. New tokens whose position is negative
  * (n_i > lens[i]) are left out. Errors: FCP_ERR_INVALID (nulls,
- * negative sizes, misaligned or missing buffers, an unknown dtype), FCP_ERR_UNSUPPORTED (D,
+ * negative sizes, misaligned or missing buffers, an unknown dtype, a unit that is no power of two
+ * in its range), FCP_ERR_UNSUPPORTED (D,
  * page_size, more than 65536 sequences, 2^30 new tokens or 2^30 positions in a block table's
  * row), FCP_ERR_CUDA. */
 fcp_status fcp_cache_write(const fcp_cache* cache, const fcp_cache_batch* batch, const void* k, const void* v,
@@ -414,8 +426,9 @@ fcp_status fcp_cache_write(const fcp_cache* cache, const fcp_cache_batch* batch,
 
 /* The inverse: read the same rows of the cache back into bf16 k and v [Hkv, total_new, D]. A
  * batch with n_i = lens[i] reads whole sequences, packed as fcp_block_attn_fwd takes them.
- * Exact for a bf16 cache, and for an e4m3 one whose value code * 2^k is a normal bf16 number;
- * writing what was read stores the same values again. Errors as fcp_cache_write. */
+ * Exact for a bf16 cache, and for an e4m3 or 4-bit one whose value is a normal bf16 number;
+ * writing what was read stores the same values again (in a 4-bit cache where the scale is 2^-6 at
+ * least). Errors as fcp_cache_write. */
 fcp_status fcp_cache_read(const fcp_cache* cache, const fcp_cache_batch* batch, void* k, void* v, void* stream);
 
 /* Bytes of fcp_paged_attn's workspace: partial results of the groups that are split over
