@@ -40,7 +40,7 @@ _NAMES = [
     "EXPORTED_SYMBOLS",
 ]
 # of paged.py, which needs torch; importing the package (its host plan) does not
-_PAGED_NAMES = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention"]
+_PAGED_NAMES = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention", "PagePool"]
 
 MASK_FULL = 0
 MASK_CAUSAL_DIAG = 1
@@ -112,6 +112,11 @@ class _CacheBatchStruct(ctypes.Structure):
         (n, ctypes.c_int32) for n in ("n_seqs", "max_pages", "total_new", "max_new")]
 
 
+class _PagePoolStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("free_pages", "n_free", "lens", "block_table", "status")] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_seqs", "max_pages")]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -154,6 +159,8 @@ _SIGNATURES = {
     "fcp_paged_attn_workspace_bytes": (_SZ, [_I32]),
     "fcp_paged_attn": (_ST, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_CacheBatchStruct), _P, _I32, _I32, _P, _P, _P,
                              _SZ, _P]),
+    "fcp_pool_release": (_ST, [ctypes.POINTER(_PagePoolStruct), _P, _P]),
+    "fcp_pool_admit": (_ST, [ctypes.POINTER(_PagePoolStruct), _P, _I32, _P, _P, _P, _P, _P]),
     "fcp_selftest_bounded_wait": (_ST, [_P, _P]),
     "fcp_device_error": (_ST, [_P, ctypes.POINTER(_I32), _P]),
     "fcp_plan_free": (None, [_P]),

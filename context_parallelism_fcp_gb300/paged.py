@@ -1,8 +1,8 @@
-"""The paged key/value cache of include/fcp.h and the attention that reads it.
+"""The paged key/value cache of include/fcp.h, the pages of its sequences, and the attention that reads it.
 
 ``PagedCache`` holds one layer's pages, ``CacheBatch`` says which rows of a packed batch belong
 to which cached sequence, and ``cache_write``, ``cache_read`` and ``paged_attn`` are the C calls
-of the same names. As in the rest of the package the arguments are checked and marshalled here
+of the same names. ``PagePool`` gives pages to sequences and takes them back, on the GPU. As in the rest of the package the arguments are checked and marshalled here
 and all the work is done by the library's kernels, on the caller's stream. That may be any stream: what a
 cache or an attention allocates stays theirs until the work of every stream that they were used on is done.
 (Tensors of the caller's follow torch's rule: one that is used on another stream than its own and then dropped
@@ -18,9 +18,9 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _CacheBatchStruct, _CacheStruct, _check, _need, _stream, device_error, FcpError, lib
+from . import _CacheBatchStruct, _CacheStruct, _PagePoolStruct, _check, _need, _stream, device_error, FcpError, lib
 
-__all__ = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention"]
+__all__ = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention", "PagePool"]
 
 _E2M1 = torch.float4_e2m1fn_x2  # two codes to an element
 _DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, _E2M1: 2}
@@ -272,3 +272,104 @@ class PagedAttention(_Owner):
                 lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse is None else lse
         _attend(*self._call, batch, q, o, lse, *self._last, stream, self)
         return o, lse
+
+
+class PagePool(_Owner):
+    """The pages of up to ``n_seqs`` sequences, kept on the GPU (fcp_page_pool): a stack of free pages,
+    the sequences' lengths and the block table that CacheBatch takes, all int32 CUDA tensors. One pool
+    serves the caches of all layers. Calls change these in place: those on one pool must not overlap."""
+
+    def __init__(self, n_pages: int, page_size: int, n_seqs: int, max_pages: int, device="cuda"):
+        ints = dict(dtype=torch.int32, device=device)
+        made = [torch.arange(int(n_pages) - 1, -1, -1, **ints), torch.full((1,), int(n_pages), **ints),
+                torch.zeros(int(n_seqs), **ints), torch.full((int(n_seqs), int(max_pages)), -1, **ints)]
+        self._setup(*made, page_size, None, None, made)
+
+    @classmethod
+    def wrap(cls, free_pages, n_free, lens, block_table, page_size: int, cu_new=None, granted=None) -> "PagePool":
+        """A pool over tensors that exist already: the first n_free[0] of free_pages [n_pages] are the
+        pages that no sequence has."""
+        self = cls.__new__(cls)
+        self._setup(free_pages, n_free, lens, block_table, page_size, cu_new, granted, [])
+        return self
+
+    def _setup(self, free_pages, n_free, lens, block_table, page_size, cu_new, granted, made):
+        _need(lens, torch.int32, None, "lens")
+        if lens.dim() != 1:
+            raise ValueError("lens must have shape [n_seqs]")
+        n = lens.shape[0]
+        _need(free_pages, torch.int32, None, "free_pages")
+        if free_pages.dim() != 1:
+            raise ValueError("free_pages must have shape [n_pages]")
+        _need(n_free, torch.int32, (1,), "n_free")
+        _need(block_table, torch.int32, None, "block_table")
+        if block_table.dim() != 2 or block_table.shape[0] != n:
+            raise ValueError(f"block_table must have shape [{n}, max_pages], got {tuple(block_table.shape)}")
+        if page_size not in (16, 32, 64, 128, 256, 512, 1024, 2048, 4096):
+            raise ValueError(f"page_size must be a power of two from 16 to 4096, got {page_size}")
+        made = list(made)
+        if cu_new is None:
+            made.append(cu_new := torch.zeros(n + 1, dtype=torch.int32, device=lens.device))
+        if granted is None:
+            made.append(granted := torch.zeros(n, dtype=torch.int32, device=lens.device))
+        _need(cu_new, torch.int32, (n + 1,), "cu_new")
+        _need(granted, torch.int32, (n,), "granted")
+        if any(t.device != lens.device for t in (free_pages, n_free, block_table, cu_new, granted)):
+            raise ValueError("the pool's tensors must be on one device")
+        self.free_pages, self.n_free, self.lens, self.block_table = free_pages, n_free, lens, block_table
+        self.cu_new, self.granted, self.n_seqs, self.page_size = cu_new, granted, n, int(page_size)
+        self.status = torch.zeros(64, dtype=torch.int32, device=lens.device)
+        self._own([self.status, *made], lens.get_device())
+        self._struct = _PagePoolStruct(free_pages.data_ptr(), n_free.data_ptr(), lens.data_ptr(), block_table.data_ptr(),
+                                       self.status.data_ptr(), free_pages.shape[0], self.page_size, n, block_table.shape[1])
+        self._ref = ctypes.byref(self._struct)
+        self._outs = cu_new.data_ptr(), granted.data_ptr()
+
+    def _launch(self, stream) -> int:
+        if torch._C._cuda_getDevice() != self._index:
+            raise ValueError(f"the pool is on cuda:{self._index}, the current device is cuda:{torch._C._cuda_getDevice()}")
+        raw = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream(stream)
+        if raw not in self._streams:
+            self._note(raw, stream)
+        return raw
+
+    def release(self, keep, stream=None) -> None:
+        """Cut sequence i back to ``keep[i]`` tokens (int32 CUDA tensor; negative: leave it, 0: it ends);
+        pages behind it become free (fcp_pool_release)."""
+        _want(keep, torch.int32, (self.n_seqs,), self._index, "keep")
+        status = lib().fcp_pool_release(self._ref, keep.data_ptr(), self._launch(stream))
+        if status:
+            _check(status, "fcp_pool_release")
+
+    def admit(self, new, positions=None, slots=None, total_new: Optional[int] = None, stream=None) -> None:
+        """Make room for ``new[i]`` more tokens of each sequence (int32 CUDA tensor), first come first
+        served (fcp_pool_admit): ``granted[i]`` says how many it got (all or none), ``lens``,
+        ``cu_new`` and ``block_table`` include them. ``positions`` (int32) and ``slots`` (int64), both
+        [total_new] and optional, get each packed row's position and page * page_size + row of the page;
+        -1 for rows of no sequence. ``total_new`` is needed where neither is given."""
+        if total_new is None:
+            rows = positions if positions is not None else slots
+            if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+                raise ValueError("total_new is needed, or positions or slots of shape [total_new]")
+            total_new = rows.shape[0]
+        _want(new, torch.int32, (self.n_seqs,), self._index, "new")
+        if positions is not None:
+            _want(positions, torch.int32, (total_new,), self._index, "positions")
+        if slots is not None:
+            _want(slots, torch.int64, (total_new,), self._index, "slots")
+        status = lib().fcp_pool_admit(self._ref, new.data_ptr(), total_new, *self._outs,
+                                      positions.data_ptr() if positions is not None else None,
+                                      slots.data_ptr() if slots is not None else None, self._launch(stream))
+        if status:
+            _check(status, "fcp_pool_admit")
+
+    def batch(self, total_new: int, max_new: int) -> CacheBatch:
+        """The CacheBatch of the tokens that were admitted last: it reads this pool's tensors, so one
+        serves every step of ``total_new`` packed rows."""
+        return CacheBatch(self.cu_new, self.lens, self.block_table, total_new, max_new)
+
+    def check_device_error(self, stream=None) -> None:
+        """Synchronise and raise if a call found the pool's state broken (see fcp_page_pool)."""
+        code = device_error(self.status, stream)
+        if code:
+            raise FcpError(6, "page pool", f"error word 0x{code:x}")

@@ -457,6 +457,46 @@ size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
 fcp_status fcp_paged_attn(const fcp_cache* cache, const fcp_cache_batch* batch, const void* q, int32_t hq,
                           int32_t causal, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Pages for a paged cache's sequences, kept on the device (no counterpart on the pages). free_pages
+ * [n_pages] is a stack: its first *n_free entries are the pages that no sequence has, the last of them
+ * its top. lens[i] and row i of block_table are those of an fcp_cache_batch; entries past a
+ * sequence's pages are not looked at. One pool serves the caches of all layers. All arrays are on the
+ * device, so a captured graph replays with whatever they hold then; the calls change lens, block_table,
+ * free_pages and *n_free in place, so two calls on a pool must not overlap, and pages that several
+ * sequences share must not be released here while another has them.
+ * status is int32[4] on the device (16-byte aligned, zero at first): word 0 the error word (read and
+ * clear it with fcp_device_error), the others the calls' own. 0x50: a length that does not fit its row,
+ * a negative number of new tokens, a stack height outside [0, n_pages], or a release that would pass
+ * n_pages (that sequence, or the call's whole release, is left out); 0x51: a page id outside
+ * [0, n_pages) in what was released or taken. */
+typedef struct {
+  int32_t* free_pages;  /* [n_pages] */
+  int32_t* n_free;      /* [1] */
+  int32_t* lens;        /* [n_seqs] */
+  int32_t* block_table; /* [n_seqs, max_pages] */
+  int32_t* status;
+  int32_t n_pages, page_size, n_seqs, max_pages;
+} fcp_page_pool;
+
+/* Cut sequences back: lens[i] becomes min(lens[i], keep[i]) (as it is for a negative keep[i]; 0 ends a
+ * sequence), and the pages behind it go on the stack in the order sequence, page; their entries of
+ * the block table become -1. Errors: FCP_ERR_INVALID (nulls, negative sizes, misaligned arrays),
+ * FCP_ERR_UNSUPPORTED (page_size, more than 65536 sequences or 2^30 positions in a row),
+ * FCP_ERR_CUDA. */
+fcp_status fcp_pool_release(const fcp_page_pool* pool, const int32_t* keep, void* stream);
+
+/* Make room for new_tokens[i] more tokens of each sequence, first come first served: pages are taken
+ * from the stack's top in the order sequence, page, and packed rows (total_new of them in all) are
+ * given out in the same order. A sequence gets all its tokens or none: none where its row of the block
+ * table has no room, and once pages or rows have not sufficed for a sequence, the ones behind it that
+ * need a page, or a row, get none either. Writes granted[i], cu_new [n_seqs + 1] (an
+ * fcp_cache_batch's), lens[i] (with the new tokens), the block table's new entries, and for each
+ * packed row its position in its sequence and its slot page * page_size + position % page_size, -1 for
+ * rows behind the last sequence. positions and slots [total_new] may be null; granted must not be
+ * new_tokens. Errors as fcp_pool_release, and more than 2^30 rows FCP_ERR_UNSUPPORTED. */
+fcp_status fcp_pool_admit(const fcp_page_pool* pool, const int32_t* new_tokens, int32_t total_new, int32_t* cu_new,
+                          int32_t* granted, int32_t* positions, int64_t* slots, void* stream);
+
 /* Synchronise `stream`, copy the device plan's error word to *code (0 = none; else the
  * kernel and wait that gave up) and clear it. Returns FCP_ERR_DEVICE if it was set. */
 fcp_status fcp_device_error(const void* d_plan, int32_t* code, void* stream);
