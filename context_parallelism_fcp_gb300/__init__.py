@@ -39,8 +39,9 @@ _NAMES = [
     "MASK_CAUSAL_DIAG",
     "EXPORTED_SYMBOLS",
 ]
-# of paged.py, which needs torch; importing the package (its host plan) does not
-_PAGED_NAMES = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention", "PagePool"]
+# of paged.py and rotary.py, which need torch; importing the package (its host plan) does not
+_PAGED_NAMES = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention", "PagePool", "Rotary",
+                "rotary_apply", "rotary_backward", "rotary_write"]
 
 MASK_FULL = 0
 MASK_CAUSAL_DIAG = 1
@@ -112,6 +113,11 @@ class _CacheBatchStruct(ctypes.Structure):
         (n, ctypes.c_int32) for n in ("n_seqs", "max_pages", "total_new", "max_new")]
 
 
+class _RotaryStruct(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("magnitude", ctypes.c_float), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
 class _PagePoolStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("free_pages", "n_free", "lens", "block_table", "status")] + [
         (n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_seqs", "max_pages")]
@@ -159,6 +165,9 @@ _SIGNATURES = {
     "fcp_paged_attn_workspace_bytes": (_SZ, [_I32]),
     "fcp_paged_attn": (_ST, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_CacheBatchStruct), _P, _I32, _I32, _P, _P, _P,
                              _SZ, _P]),
+    "fcp_rotary_apply": (_ST, [ctypes.POINTER(_RotaryStruct), _P, _I32, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _P]),
+    "fcp_rotary_write": (_ST, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_CacheBatchStruct),
+                               ctypes.POINTER(_RotaryStruct), _P, _P, _I32, _P, _P, _P]),
     "fcp_pool_release": (_ST, [ctypes.POINTER(_PagePoolStruct), _P, _P]),
     "fcp_pool_admit": (_ST, [ctypes.POINTER(_PagePoolStruct), _P, _I32, _P, _P, _P, _P, _P]),
     "fcp_selftest_bounded_wait": (_ST, [_P, _P]),
@@ -521,13 +530,15 @@ class FcpAttention:
     plan is scheduled as the block-level pipeline with coalesce degree c (Plan.schedule) and
     the forward launches one execution stage at a time before the merge. ``bwd_band`` sets the
     backward's query bands (Plan.set_bwd_band; None keeps the plan's own choice); the
-    workspace holds their dK/dV sums, so a plan with bands runs its backward banded."""
+    workspace holds their dK/dV sums, so a plan with bands runs its backward banded. With
+    ``rotary`` (a Rotary) q and k are turned by their positions in their sequences before the
+    attention, in the backward again, and dq and dk (rounded to bf16) are turned back."""
 
     def __init__(self, seqlens: Sequence[int], block_size: int, causal: bool, n_workers: int, hq: int, hkv: int,
                  head_dim: int, token_cap: Optional[int] = None, coalesce: int = 1, device="cuda",
-                 backward: bool = True, pipeline: Optional[int] = None, bwd_band: Optional[int] = None):
+                 backward: bool = True, pipeline: Optional[int] = None, bwd_band: Optional[int] = None, rotary=None):
         self._recipe = (int(block_size), bool(causal), int(n_workers), token_cap, int(coalesce), pipeline, bwd_band)
-        self._setup(self._make_plan(seqlens), hq, hkv, head_dim, device, backward)
+        self._setup(self._make_plan(seqlens), hq, hkv, head_dim, device, backward, rotary)
 
     def _make_plan(self, seqlens) -> "Plan":
         block_size, causal, n_workers, token_cap, coalesce, pipeline, bwd_band = self._recipe
@@ -559,17 +570,30 @@ class FcpAttention:
             raise ValueError("the new batch has a different number of pipeline stages")
         plan.upload(self.d_plan, stream)
         self.plan = plan
+        if self.rotary is not None:
+            import torch
+
+            if stream is not None and not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream(stream), device=self.device)
+            with torch.cuda.stream(stream):
+                self.positions.copy_(self._packed_positions())
 
     @classmethod
     def from_plan(cls, plan: "Plan", hq: int, hkv: int, head_dim: int, device="cuda",
-                  backward: bool = True) -> "FcpAttention":
+                  backward: bool = True, rotary=None) -> "FcpAttention":
         """Wrap an already distributed plan (e.g. Plan.ring(...))."""
         self = cls.__new__(cls)
         self._recipe = None
-        self._setup(plan, hq, hkv, head_dim, device, backward)
+        self._setup(plan, hq, hkv, head_dim, device, backward, rotary)
         return self
 
-    def _setup(self, plan, hq, hkv, head_dim, device, backward):
+    def _packed_positions(self):
+        import torch
+
+        return torch.from_numpy(np.concatenate([np.arange(int(n), dtype=np.int32) for n in self.plan.seqlens] or
+                                               [np.zeros(0, np.int32)]))
+
+    def _setup(self, plan, hq, hkv, head_dim, device, backward, rotary=None):
         import torch
 
         self.plan = plan
@@ -592,6 +616,20 @@ class FcpAttention:
             # with query bands, room for their float32 dK/dV sums, so that the backward runs banded
             ws = self.plan.workspace_bytes(hq, head_dim) + self.plan.band_workspace_bytes(hkv, head_dim)
             self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
+        self.rotary = rotary
+        if rotary is not None:
+            if rotary.rotary_dim > head_dim:
+                raise ValueError(f"rotary_dim {rotary.rotary_dim} is larger than head_dim {head_dim}")
+            self.positions = self._packed_positions().to(self.device)
+            self._turned = [torch.empty((h, self.T, head_dim), dtype=torch.bfloat16, device=self.device)
+                            for h in (hq, hkv)]
+
+    def _turn(self, q, k, stream):
+        if self.rotary is None:
+            return q, k
+        from .rotary import rotary_apply
+
+        return rotary_apply(self.rotary, q, k, self.positions, *self._turned, stream=stream)
 
     def forward(self, q, k, v, o=None, lse=None, stream=None):
         import torch
@@ -600,6 +638,7 @@ class FcpAttention:
             o = torch.empty((self.hq, self.T, self.head_dim), dtype=torch.bfloat16, device=self.device)
         if lse is None:
             lse = torch.empty((self.hq, self.T), dtype=torch.float32, device=self.device)
+        q, k = self._turn(q, k, stream)
         if self.n_stages > 1:
             for st in range(self.n_stages):
                 block_attn_fwd_stage(self.plan, self.d_plan, st, q, k, v, self.part_o, self.part_lse, stream)
@@ -616,7 +655,12 @@ class FcpAttention:
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
+        q, k = self._turn(q, k, stream)
         block_attn_bwd(self.plan, self.d_plan, q, k, v, o, dout, lse, dq, dk, dv, self.workspace, stream)
+        if self.rotary is not None:
+            from .rotary import rotary_backward
+
+            rotary_backward(self.rotary, dq, dk, self.positions, dq, dk, stream=stream)
         return dq, dk, dv
 
     def check_device_error(self, stream=None) -> None:
@@ -633,9 +677,9 @@ def __getattr__(name):
             return list(_NAMES)
         return _NAMES + _PAGED_NAMES
     if name in _PAGED_NAMES:
-        from . import paged
+        from . import paged, rotary
 
-        return getattr(paged, name)
+        return getattr(paged if hasattr(paged, name) else rotary, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -26,22 +26,22 @@ _E2M1 = torch.float4_e2m1fn_x2  # two codes to an element
 _DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, _E2M1: 2}
 
 
-def _here(index: int, stream) -> int:
+def _here(index: int, stream, what: str = "cache") -> int:
     """The stream to launch on. Kernels run on the current device, so that is where the tensors
     have to be."""
     if torch._C._cuda_getDevice() != index:
-        raise ValueError(f"the cache is on cuda:{index}, the current device is cuda:{torch._C._cuda_getDevice()}")
+        raise ValueError(f"the {what} is on cuda:{index}, the current device is cuda:{torch._C._cuda_getDevice()}")
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
 
 
-def _want(t, dtype, shape, index: int, name: str) -> None:
+def _want(t, dtype, shape, index: int, name: str, what: str = "cache") -> None:
     """_need and the device, with a step's few microseconds in mind: what is right passes quickly."""
     if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous()):
         return
     _need(t, dtype, shape, name)
     if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
+        raise ValueError(f"{name} is on {t.device}, the {what} on cuda:{index}")
 
 
 class _Owner:
@@ -326,9 +326,7 @@ class PagePool(_Owner):
         self._outs = cu_new.data_ptr(), granted.data_ptr()
 
     def _launch(self, stream) -> int:
-        if torch._C._cuda_getDevice() != self._index:
-            raise ValueError(f"the pool is on cuda:{self._index}, the current device is cuda:{torch._C._cuda_getDevice()}")
-        raw = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream(stream)
+        raw = _here(self._index, stream, "pool")
         if raw not in self._streams:
             self._note(raw, stream)
         return raw
@@ -336,7 +334,7 @@ class PagePool(_Owner):
     def release(self, keep, stream=None) -> None:
         """Cut sequence i back to ``keep[i]`` tokens (int32 CUDA tensor; negative: leave it, 0: it ends);
         pages behind it become free (fcp_pool_release)."""
-        _want(keep, torch.int32, (self.n_seqs,), self._index, "keep")
+        _want(keep, torch.int32, (self.n_seqs,), self._index, "keep", "pool")
         status = lib().fcp_pool_release(self._ref, keep.data_ptr(), self._launch(stream))
         if status:
             _check(status, "fcp_pool_release")
@@ -352,11 +350,11 @@ class PagePool(_Owner):
             if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
                 raise ValueError("total_new is needed, or positions or slots of shape [total_new]")
             total_new = rows.shape[0]
-        _want(new, torch.int32, (self.n_seqs,), self._index, "new")
+        _want(new, torch.int32, (self.n_seqs,), self._index, "new", "pool")
         if positions is not None:
-            _want(positions, torch.int32, (total_new,), self._index, "positions")
+            _want(positions, torch.int32, (total_new,), self._index, "positions", "pool")
         if slots is not None:
-            _want(slots, torch.int64, (total_new,), self._index, "slots")
+            _want(slots, torch.int64, (total_new,), self._index, "slots", "pool")
         status = lib().fcp_pool_admit(self._ref, new.data_ptr(), total_new, *self._outs,
                                       positions.data_ptr() if positions is not None else None,
                                       slots.data_ptr() if slots is not None else None, self._launch(stream))

@@ -457,6 +457,36 @@ size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
 fcp_status fcp_paged_attn(const fcp_cache* cache, const fcp_cache_batch* batch, const void* q, int32_t hq,
                           int32_t causal, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Rotary positions (no counterpart on the pages). The first rotary_dim channels of a row make pairs,
+ * channel i with rotary_dim / 2 + i, or (interleaved != 0) 2 i with 2 i + 1; at position p pair i
+ * becomes m (a cos x - b sin x, b cos x + a sin x) with x = 2 pi p turns[i] 2^-64 and m = magnitude; the
+ * other channels go as they are. turns [rotary_dim / 2] is on the device: a frequency of f radians a
+ * position is the integer nearest to f / (2 pi) * 2^64, which keeps x right to 2^-32 of a turn at every
+ * int32 position. rotary_dim is a multiple of 16, up to D. Products are float32, rounded to bf16
+ * once. */
+typedef struct {
+  const uint64_t* turns;
+  float magnitude;
+  int32_t rotary_dim, interleaved;
+} fcp_rotary;
+
+/* Turn q [Hq, total, D] and k [Hkv, total, D] (bf16) into q_out and k_out, which may be q and k
+ * themselves; either may have no heads (and no buffers). positions [total] int32 on the device, of
+ * any sign. backward != 0: the gradients of q and k from those of q_out and k_out, which is the turn the
+ * other way, times the same m. Errors: FCP_ERR_INVALID (nulls, negative sizes, misaligned buffers,
+ * rotary_dim outside 1 .. D, a magnitude that is not positive and finite), FCP_ERR_UNSUPPORTED (D other
+ * than 64 and 128, rotary_dim no multiple of 16, more than 2^30 rows or 65535 heads), FCP_ERR_CUDA. */
+fcp_status fcp_rotary_apply(const fcp_rotary* rotary, const int32_t* positions, int32_t total, const void* q,
+                            void* q_out, int32_t hq, const void* k, void* k_out, int32_t hkv, int32_t head_dim,
+                            int32_t backward, void* stream);
+
+/* The same for a batch's new tokens at their positions in their sequences, with the turned k, rounded
+ * to bf16, and v written to the cache as by fcp_cache_write: what fcp_rotary_apply and fcp_cache_write do
+ * in two calls, bit for bit. q_out may be q; its rows of no sequence, and of negative positions, are
+ * left as they were; hq may be 0. k and v are not changed. Errors as these two calls'. */
+fcp_status fcp_rotary_write(const fcp_cache* cache, const fcp_cache_batch* batch, const fcp_rotary* rotary,
+                            const void* q, void* q_out, int32_t hq, const void* k, const void* v, void* stream);
+
 /* Pages for a paged cache's sequences, kept on the device (no counterpart on the pages). free_pages
  * [n_pages] is a stack: its first *n_free entries are the pages that no sequence has, the last of them
  * its top. lens[i] and row i of block_table are those of an fcp_cache_batch; entries past a
