@@ -22,9 +22,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libfcp.so")
 
 SOURCES = ["fcp_plan.cpp", "fcp_solver.cpp", "fcp_validate.cpp", "fcp_fwd.cu", "fcp_bwd.cu", "fcp_bwd_tile.cu", "fcp_merge.cu",
-           "fcp_cache.cu", "fcp_pool.cu", "fcp_rotary.cu", "fcp_paged_few.cu", "fcp_paged_chunk.cu"]
+           "fcp_cache.cu", "fcp_pool.cu", "fcp_rotary.cu", "fcp_paged_few.cu", "fcp_paged_few4.cu", "fcp_paged_chunk.cu"]
 HEADERS = ["fcp_internal.h", "fcp_cuda_util.h", "fcp_sm100.cuh", "fcp_paged.h",
-           "fcp_paged_sched.cuh", "fcp_move.cuh"]
+           "fcp_paged_sched.cuh", "fcp_paged_few.cuh", "fcp_move.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-I", INCLUDE,
           "-I", CSRC]

@@ -1,5 +1,5 @@
 // Attention of few new rows for each cached sequence (single tokens, drafted tokens) over a
-// paged cache, and the entry point of the attention over a paged cache.
+// paged cache in bf16 or e4m3, and the entry point of the attention over a paged cache.
 //
 // For a KV head the rows are (new token, query head) pairs, 8, 16 or 32 to a unit, so every query
 // head of the group and every drafted token shares one pass over the keys: HBM traffic is the
@@ -40,20 +40,15 @@
 // are a dependent chain of memory latencies.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
-#include "fcp_paged_sched.cuh"
+#include "fcp_paged_few.cuh"
 
 namespace fcp {
 namespace {
 
 using namespace dev;
+using namespace few;
 
-constexpr int kWarps = 4;
-constexpr int kFewThreads = kWarps * 32;
-constexpr int kChunk = 16;                  // keys of a stage
-constexpr float kGrow = 8.0f;               // a row maximum is raised when it grows by over 2^8
-constexpr float kUp = 7.0f;                 // e4m3: P starts at 2^7 and grows to 2^15, the top of f16
 // e4m3: below 2^-14 P's rounding to f16 is off by up to 2^-25, which for a key whose V has a scale
 // 2^gap below that of the largest is 2^(gap - 25 - kUp) of the largest weight. Up to this gap (2^-22)
 // that is left so; beyond it the rest of P counts too (which it has to: with gaps of 2^18 and more,
@@ -64,99 +59,20 @@ constexpr float kLift = 0x1p28f;
 // Blocks to an SM and the shared memory of a block's stages, for NT tiles of 8 rows. bf16 is at
 // HBM's rate with two; the e4m3 conversion leaves more latency to hide, as far as the registers
 // go: 128, 168 and 255 a thread.
-template <int kKind, int NT>
-constexpr int kPerSm = kKind == FCP_CACHE_BF16 ? 2 : (NT == 1 ? 4 : (NT == 2 ? 3 : 2));
+template <bool kE4M3, int NT>
+constexpr int kPerSm = !kE4M3 ? 2 : (NT == 1 ? 4 : (NT == 2 ? 3 : 2));
 
-template <int D, int kKind, int NT>
+template <int D, bool kE4M3, int NT>
 struct FewCfg {
-  static constexpr int kStageBudget = (kPerSm<kKind, NT> == 4 ? 50 : (kPerSm<kKind, NT> == 3 ? 67 : 97)) * 1024;
-  static constexpr int kRowBytes = kKind == FCP_CACHE_E2M1 ? D / 2 : (kKind == FCP_CACHE_E4M3 ? D : 2 * D);
-  static constexpr int kScaleBytes = kKind == FCP_CACHE_E2M1 ? D / 16 : (kKind == FCP_CACHE_E4M3 ? 1 : 0);  // of a row
+  static constexpr int kStageBudget = (kPerSm<kE4M3, NT> == 4 ? 50 : (kPerSm<kE4M3, NT> == 3 ? 67 : 97)) * 1024;
+  static constexpr int kRowBytes = kE4M3 ? D : 2 * D;
   static constexpr int kPieces = kRowBytes / 16;               // 16-byte pieces of a row
   static constexpr int kTile = kChunk * kRowBytes;             // K or V of a chunk
-  static constexpr int kStage = 2 * kTile + 2 * kChunk * kScaleBytes;  // K, V, their scales
+  static constexpr int kStage = 2 * kTile + (kE4M3 ? 32 : 0);  // + 16 K scales, 16 V scales
   static constexpr int kStagesRaw = kStageBudget / (kWarps * kStage);
   static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
   static constexpr int kWarpBytes = kStages * kStage;
 };
-
-// Where piece c of row r lies in a tile. Rows of 128 bytes and more: 8 rows of one piece, and
-// pieces 0-3 of two neighbouring rows, fall on different banks; rows of 64 bytes share a line
-// of banks two by two, rows of 32 four by four.
-template <int kRowBytes>
-__device__ __forceinline__ int piece_at(int r, int c) {
-  if constexpr (kRowBytes == 32) return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
-  else if constexpr (kRowBytes == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  else return r * kRowBytes + ((c ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16_or_zeros(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-// The first `bytes` of 16, and zeros.
-__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int n>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
-}
-__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint32_t v;
-  asm volatile("{\n.reg .b16 h;\nld.shared.b16 h, [%1];\ncvt.u32.u16 %0, h;\n}" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 in, float32 out
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// the same in f16
-__device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The 8x8 matrix of 16-bit elements that the warp holds, transposed.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
 
 // f(c, fragment) for each 16 channels of a chunk's V in e4m3, as the first operand in f16.
 template <int kRowBytes, class F>
@@ -178,72 +94,9 @@ __device__ __forceinline__ void each_v(uint32_t vt, int lane, F f) {
   }
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Four e2m1 codes of each of two keys (the low and the high half), with the keys' scales as f16: the same
-// code of both keys in one register.
-__device__ __forceinline__ void e2m1_pairs(uint32_t x, uint32_t scale, uint32_t (&r)[4]) {
-  uint32_t h[4];
-  e2m1x8_to_f16x2(x, h);
-  r[0] = mul_f16x2(__byte_perm(h[0], h[2], 0x5410), scale);
-  r[1] = mul_f16x2(__byte_perm(h[0], h[2], 0x7632), scale);
-  r[2] = mul_f16x2(__byte_perm(h[1], h[3], 0x5410), scale);
-  r[3] = mul_f16x2(__byte_perm(h[1], h[3], 0x7632), scale);
-}
-
-// f(c, fragment) for each 16 channels of a chunk's V in e2m1, as the first operand in f16: lane (i8, j)
-// has channels 32 (c / 2) + 4 i8 + 2 (c % 2) and the next, as the fragment's rows i8 and 8 + i8.
-template <int D, class F>
-__device__ __forceinline__ void each_v4(uint32_t vt, uint32_t scales, int lane, F f) {
-  constexpr int kRowBytes = D / 2, kSegments = D / 32;
-  const int vr = (lane & 7) + (lane & 8), j = lane & 3;
-  const bool odd = (lane >> 4) != 0;  // channels 16-31 of a segment of 32
-  uint32_t sc[2][kSegments];          // scales of keys 2 j and 2 j + 1 (and those + 8)
-#pragma unroll
-  for (int y = 0; y < 2; ++y) {
-    const uint32_t at = scales + (8 * y + 2 * j) * (D / 16);
-    if constexpr (D == 128) {
-      const uint4 w = lds16(at);
-      const uint32_t sel = odd ? 0x7531u : 0x6420u;
-      const uint32_t k0 = __byte_perm(w.x, w.y, sel), k1 = __byte_perm(w.z, w.w, sel);
-      e4m3x4_to_f16x2(__byte_perm(k0, k1, 0x5140), sc[y][0], sc[y][1]);
-      e4m3x4_to_f16x2(__byte_perm(k0, k1, 0x7362), sc[y][2], sc[y][3]);
-    } else {
-      const uint2 w = lds8(at);
-      e4m3x4_to_f16x2(__byte_perm(w.x, w.y, odd ? 0x7351u : 0x6240u), sc[y][0], sc[y][1]);
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < kSegments; g += 2) {
-    uint32_t x[4];
-    ldsm4_trans(vt + piece_at<kRowBytes>(vr, g + (lane >> 4)), x);
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      uint32_t lo[4], hi[4];
-      e2m1_pairs(x[2 * y], sc[0][g + y], lo);
-      e2m1_pairs(x[2 * y + 1], sc[1][g + y], hi);
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const uint32_t v[4] = {lo[2 * z], lo[2 * z + 1], hi[2 * z], hi[2 * z + 1]};
-        f(2 * (g + y) + z, v);
-      }
-    }
-  }
-}
-
-struct Piece {
-  int valid, i, h, u, a, n, len, end, ga, gb, slot;
-};
-
-template <int D, int kKind, int NT>
-__global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(const AttnArgs a) {
-  constexpr bool kE4M3 = kKind == FCP_CACHE_E4M3, kE2M1 = kKind == FCP_CACHE_E2M1;
-  constexpr bool kF16 = kE4M3 || kE2M1;  // the products' type
-  constexpr float kM = kE2M1 ? kUp : 0.f;  // a row's maximum less this is what its weights are relative to
-  using C = FewCfg<D, kKind, NT>;
+template <int D, bool kE4M3, int NT>
+__global__ void __launch_bounds__(kFewThreads, kPerSm<kE4M3, NT>) few_kernel(const AttnArgs a) {
+  using C = FewCfg<D, kE4M3, NT>;
   using P = FewRows<8 * NT>;
   constexpr int kRows = P::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -332,17 +185,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
       const bool on = row(8 * (kSharedQ ? warp : t) + i8, tok, head);
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (static_cast<long long>(p.h * a.group + (on ? head : 0)) * a.c.total_new + s.a + (on ? tok : 0)) * D);
-      if constexpr (kE2M1) {
-        // lane j has D / 4 neighbouring channels, 8 of them in two products
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          const uint4 v = on ? load(src + (D / 32) * j + w) : make_uint4(0, 0, 0, 0);
-          q[t][2 * w][0] = v.x;
-          q[t][2 * w][1] = v.y;
-          q[t][2 * w + 1][0] = v.z;
-          q[t][2 * w + 1][1] = v.w;
-        }
-      } else if constexpr (kE4M3) {
+      if constexpr (kE4M3) {
         // 64 channels: lane j has channels 16 j .. 16 j + 15, in products 0-3 of the 64
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
@@ -405,15 +248,6 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
           if (lane < 2)
             cp_async16_or_zeros(dst + 2 * C::kTile + 16 * lane, (lane ? a.c.v_scales : a.c.k_scales) + r0, ok);
         }
-        if constexpr (kE2M1) {  // rows behind the last key have scales of zero
-          constexpr int kHalf = kChunk * C::kScaleBytes / 16;
-          if (lane < 2 * kHalf) {
-            const int at16 = 16 * (lane % kHalf);
-            const int bytes = ok ? min(max((s.len - key) * C::kScaleBytes - at16, 0), 16) : 0;
-            cp_async16_part(dst + 2 * C::kTile + 16 * lane,
-                            (lane < kHalf ? a.c.k_scales : a.c.v_scales) + (bytes > 0 ? r0 * C::kScaleBytes + at16 : 0), bytes);
-          }
-        }
       }
       cp_commit();
       ++n_issued;
@@ -429,13 +263,13 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
       advance(w, sh, sh.begin(b), w1, shared_piece[turn ^ 1]);
     }
 
-    // e4m3 and e2m1: Q's rows as f16 scaled by 2^(14 - e), e the largest exponent of the row; `back` takes the
+    // e4m3: Q's rows as f16 scaled by 2^(14 - e), e the largest exponent of the row; `back` takes the
     // scores of row i8 of a tile to log2 units.
     float back[kSharedQ ? 1 : NT];
 #pragma unroll
     for (int t = 0; t < (kSharedQ ? 1 : NT); ++t) {
       back[t] = a.scale_log2;
-      if constexpr (kF16) {
+      if constexpr (kE4M3) {
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
@@ -473,7 +307,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
         const bool on = row(8 * t + 2 * j + e, tok, head);
         lim[t][e] = !on || !a.causal ? s.len : s.len - s.n + tok + 1;
         if constexpr (kSharedQ) factor[t][e] = shared_back[8 * t + 2 * j + e];
-        else factor[t][e] = kF16 ? __shfl_sync(0xffffffffu, back[t], 4 * (2 * j + e)) : a.scale_log2;
+        else factor[t][e] = kE4M3 ? __shfl_sync(0xffffffffu, back[t], 4 * (2 * j + e)) : a.scale_log2;
       }
     auto q_of = [&](int t, int c) -> uint2 {
       if constexpr (kSharedQ) return shared_q[t][c][lane];
@@ -512,46 +346,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[t][e] = 0.f;
-      if constexpr (kE2M1) {
-        uint32_t raw[2][D / 32], ks[2][2];  // of keys i8 and 8 + i8: 8 codes to a word; scales of the words' halves
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t at = kt + 2 * C::kTile + (8 * y + i8) * C::kScaleBytes;
-          uint32_t two, none;
-          if constexpr (D == 128) {
-            const uint4 v = lds16(kt + piece_at<C::kRowBytes>(8 * y + i8, j));
-            raw[y][0] = v.x;
-            raw[y][1] = v.y;
-            raw[y][2] = v.z;
-            raw[y][3] = v.w;
-            e4m3x4_to_f16x2(lds_u16(at + 2 * j), two, none);
-            ks[y][0] = __byte_perm(two, 0, 0x1010);
-            ks[y][1] = __byte_perm(two, 0, 0x3232);
-          } else {
-            const uint2 v = lds8(kt + piece_at<C::kRowBytes>(8 * y + i8, j >> 1) + 8 * (j & 1));
-            raw[y][0] = v.x;
-            raw[y][1] = v.y;
-            e4m3x4_to_f16x2(lds_u8(at + j), two, none);
-            ks[y][0] = ks[y][1] = __byte_perm(two, 0, 0x1010);
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          uint32_t f0[4], f1[4];
-          e2m1x8_to_f16x2(raw[0][w], f0);
-          e2m1x8_to_f16x2(raw[1][w], f1);
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const uint32_t f[4] = {mul_f16x2(f0[2 * z], ks[0][w >> 1]), mul_f16x2(f1[2 * z], ks[1][w >> 1]),
-                                   mul_f16x2(f0[2 * z + 1], ks[0][w >> 1]), mul_f16x2(f1[2 * z + 1], ks[1][w >> 1])};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint2 y = q_of(t, 2 * w + z);
-              mma16816h(sc[t], f, y.x, y.y);
-            }
-          }
-        }
-      } else if constexpr (kE4M3) {
+      if constexpr (kE4M3) {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           const uint4 v0 = lds16(kt + piece_at<C::kRowBytes>(i8, 4 * c + j));
@@ -614,33 +409,6 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (key + 8 * (e >> 1) + i8 >= lim[t][e & 1]) sc[t][e] = so[t][e] = -INFINITY;
-        if constexpr (kE2M1) {
-          // a NaN scale of V must not meet the zero weights of rows that do not see it: zeros take its place,
-          // and the channels of the rows that do see it become NaN here
-          constexpr int kGroups = D / 16;
-          const uint32_t vs = vt + C::kTile + kChunk * C::kScaleBytes;
-          uint32_t four = 0;
-          if (lane < kChunk * kGroups / 4)
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(four) : "r"(vs + 4 * lane) : "memory");
-          if (__any_sync(0xffffffffu, (((four & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u)) {
-#pragma unroll 1
-            for (int x = kChunk * kGroups - 1; x >= 0; --x) {  // key x / kGroups, group x % kGroups
-              if ((lds_u8(vs + x) & 0x7fu) != 0x7fu) continue;
-              __syncwarp();
-              if (lane == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(vs + x), "r"(0) : "memory");
-              const int g = x % kGroups;
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c)
-                if (g == 2 * (c >> 1) + (lane >> 4))
-#pragma unroll
-                  for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      if (key + x / kGroups < lim[t][e & 1]) acc[c][t][e] = __uint_as_float(0x7fc00000u);
-            }
-            __syncwarp();
-          }
-        }
       }
       // raise the running maxima only when some row's grew by more than 2^8: P stays below 2^8
       bool grow = false;
@@ -650,7 +418,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           top[t][e] = fmaxf(sc[t][e], sc[t][2 + e]);
-          grow = grow || top[t][e] > m[t][e] + (kGrow + kM);
+          grow = grow || top[t][e] > m[t][e] + kGrow;
           if constexpr (kE4M3) {
             topo[t][e] = fmaxf(so[t][e], so[t][2 + e]);
             grow = grow || topo[t][e] > mo[t][e] + (kGrow + kUp);
@@ -669,7 +437,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
               at = to;
               return f;
             };
-            float f = raise(m[t][e], top[t][e] - kM);
+            float f = raise(m[t][e], top[t][e]);
             l[t][e] *= f;
             if constexpr (kE4M3) f = raise(mo[t][e], topo[t][e] - kUp);
 #pragma unroll
@@ -703,7 +471,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          pt[t][y] = transpose8x8(kF16 ? pack_f16(pw[2 * y], pw[2 * y + 1])
+          pt[t][y] = transpose8x8(kE4M3 ? pack_f16(pw[2 * y], pw[2 * y + 1])
                                         : pack_bf16(pw[2 * y], pw[2 * y + 1]));  // bf16: off by 2^-8 of itself at most
       }
       if constexpr (kE4M3) {
@@ -736,12 +504,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
           }
         }
       }
-      if constexpr (kE2M1) {
-        each_v4<D>(vt, vt + C::kTile + kChunk * C::kScaleBytes, lane, [&](int c, const uint32_t(&v)[4]) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816h(acc[c][t], v, pt[t][0], pt[t][1]);
-        });
-      } else if constexpr (kE4M3) {
+      if constexpr (kE4M3) {
         each_v<C::kRowBytes>(vt, lane, [&](int c, const uint32_t(&v)[4]) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) mma16816h(acc[c][t], v, pt[t][0], pt[t][1]);
@@ -781,14 +544,11 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
         float f = mx == -INFINITY ? 0.f : fast_exp2(m[t][e] - mx);
         if (i8 == 0) warp_l[warp][r] = l[t][e] * f;
         if constexpr (kE4M3) f = mx == -INFINITY ? 0.f : fast_exp2(mo[t][e] - mx);  // acc's own reference
-        if constexpr (kE2M1) f *= a.c.v_unit;
         float* dst = sums + (static_cast<size_t>(warp) * kRows + r) * kSumRow;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           const float x0 = acc[c][t][e] * f, x1 = acc[c][t][2 + e] * f;
-          if constexpr (kE2M1) {  // see each_v4
-            *reinterpret_cast<float2*>(dst + 32 * (c >> 1) + 4 * i8 + 2 * (c & 1)) = make_float2(x0, x1);
-          } else if constexpr (kE4M3) {  // channels 2 i8 and 2 i8 + 1 of the 16
+          if constexpr (kE4M3) {  // channels 2 i8 and 2 i8 + 1 of the 16
             *reinterpret_cast<float2*>(dst + 16 * c + 2 * i8) = make_float2(x0, x1);
           } else {
             dst[16 * c + i8] = x0;
@@ -832,18 +592,18 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<kKind, NT>) few_kernel(con
   }
 }
 
-template <int D, int kKind, int NT>
+template <int D, bool kE4M3, int NT>
 fcp_status launch_few(AttnArgs a, void* workspace, int dev, int n_sm, int max_new, cudaStream_t s) {
-  using C = FewCfg<D, kKind, NT>;
+  using C = FewCfg<D, kE4M3, NT>;
   using P = FewRows<8 * NT>;
   constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * (D + 4) * 4);
-  const int blocks = std::min(kPerSm<kKind, NT> * n_sm, kMaxBlocks);
+  const int blocks = std::min(kPerSm<kE4M3, NT> * n_sm, kMaxBlocks);
   set_workspace<P>(a, workspace, D, kMaxBlocks);
   static std::atomic<uint64_t> allowed{0};
-  if (const fcp_status st = allow_smem(few_kernel<D, kKind, NT>, kSmem, dev, allowed, "paged attention smem attribute");
+  if (const fcp_status st = allow_smem(few_kernel<D, kE4M3, NT>, kSmem, dev, allowed, "paged attention smem attribute");
       st != FCP_OK)
     return st;
-  if (const fcp_status st = launch_overlapped(few_kernel<D, kKind, NT>, dim3(blocks), kFewThreads, kSmem, s,
+  if (const fcp_status st = launch_overlapped(few_kernel<D, kE4M3, NT>, dim3(blocks), kFewThreads, kSmem, s,
                                               "paged attention launch", a);
       st != FCP_OK)
     return st;
@@ -865,15 +625,12 @@ fcp_status launch_attn(const AttnArgs& a, int dtype, int hq, int max_new, void* 
   // 20.8 from an e4m3 cache and 16.6 instead of 19.6 from a bf16 one, 60 rows 21.4 instead of 18.5,
   // 64 rows of long sequences 37.4 instead of 36.7, 128 rows far more.)
   if (rows > 32) return launch_paged_chunk(a, dtype, D, hq, workspace, dev, n_sm, s);
-  const auto launch = [&](auto kind) {
-    constexpr int kKind = decltype(kind)::value;
-    return rows <= 8    ? launch_few<D, kKind, 1>(a, workspace, dev, n_sm, max_new, s)
-           : rows <= 16 ? launch_few<D, kKind, 2>(a, workspace, dev, n_sm, max_new, s)
-                        : launch_few<D, kKind, 4>(a, workspace, dev, n_sm, max_new, s);
-  };
-  if (dtype == FCP_CACHE_E2M1) return launch(std::integral_constant<int, FCP_CACHE_E2M1>());
-  if (dtype == FCP_CACHE_E4M3) return launch(std::integral_constant<int, FCP_CACHE_E4M3>());
-  return launch(std::integral_constant<int, FCP_CACHE_BF16>());
+  if (dtype == FCP_CACHE_E2M1) return launch_paged_few4(a, D, static_cast<int>(rows), workspace, dev, n_sm, max_new, s);
+  const bool e = dtype == FCP_CACHE_E4M3;
+  auto* launch = rows <= 8    ? (e ? launch_few<D, true, 1> : launch_few<D, false, 1>)
+                 : rows <= 16 ? (e ? launch_few<D, true, 2> : launch_few<D, false, 2>)
+                              : (e ? launch_few<D, true, 4> : launch_few<D, false, 4>);
+  return launch(a, workspace, dev, n_sm, max_new, s);
 }
 
 }  // namespace

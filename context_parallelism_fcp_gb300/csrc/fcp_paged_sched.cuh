@@ -499,6 +499,8 @@ inline fcp_status launch_merge(const AttnArgs& a, int blocks, int slices, cudaSt
   return launch_overlapped(paged_merge_kernel<P, D>, dim3(blocks, slices), 32 * kMergeWarps, 0, s, "paged merge launch", a);
 }
 
+fcp_status launch_paged_few4(const AttnArgs& a, int d, int rows, void* workspace, int dev, int n_sm, int max_new,
+                             cudaStream_t s);
 fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int dev, int n_sm,
                               cudaStream_t s);
 
