@@ -22,17 +22,18 @@ using namespace dev;
 using namespace few;
 
 template <int NT>
-constexpr int kPerSm = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // blocks to an SM, as their registers allow
+constexpr int kPerSm = NT == 1 ? 3 : 2;  // blocks to an SM
+template <int NT>
+using Rows = FewRows<8 * NT, 3>;
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int kBudget = (kPerSm<NT> == 4 ? 50 : (kPerSm<NT> == 3 ? 67 : 97)) * 1024;  // of shared memory
   static constexpr int kRowBytes = D / 2, kScales = D / 16;  // of a row of K or V
   static constexpr int kPieces = kRowBytes / 16;             // 16-byte pieces of a row
-  // A stage is two chunks, whose overhead is shared; up to two tiles of rows do both at a time, for more
-  // independent instructions (four have no registers for that).
+  // A stage is two chunks, whose overhead is shared and which are done together, for more independent
+  // instructions.
   static constexpr int kKeys = 2 * kChunk;
-  static constexpr int kAtOnce = NT <= 2 ? 2 : 1;
   static constexpr int kTile = kKeys * kRowBytes;                  // K or V of a stage
   static constexpr int kScaleTile = kKeys * kScales;
   static constexpr int kStage = 2 * (kTile + kScaleTile);          // K, V, their scales
@@ -124,7 +125,7 @@ __device__ __forceinline__ void each_v(uint32_t vt, uint32_t scales, int lane, F
 template <int D, int NT>
 __global__ void __launch_bounds__(kFewThreads, kPerSm<NT>) few4_kernel(const AttnArgs a) {
   using C = Cfg<D, NT>;
-  using P = FewRows<8 * NT>;
+  using P = Rows<NT>;
   constexpr int kRows = P::kRows, kKeys = C::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Line<kFewThreads> line;
@@ -373,143 +374,136 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<NT>) few4_kernel(const Att
       const uint32_t kt = stages + stage * C::kStage, vt = kt + C::kTile;
       const uint32_t ks = vt + C::kTile, vs = ks + C::kScaleTile;
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
-      constexpr int kAt = C::kAtOnce;
+      float sc[2][NT][4];  // S^T: element 2 y + e is key `key` + 16 u + 8 y + i8, row 8 t + 2 j + e
 #pragma unroll
-      for (int u0 = 0; u0 < 2; u0 += kAt) {
-        const int first = key + kChunk * u0;
-        float sc[kAt][NT][4];  // S^T: element 2 y + e is key first + 16 u + 8 y + i8, row 8 t + 2 j + e
+      for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int u = 0; u < kAt; ++u) {
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[u][t][e] = 0.f;
+        const int r = kChunk * u + i8;
+        uint32_t raw[2][D / 32], scale[2];  // of keys r and r + 8: 8 codes to a word; scales of the words' halves
+        if constexpr (D == 128) {
+          const uint4 v0 = lds16(kt + piece_at<C::kRowBytes>(r, j)), v1 = lds16(kt + piece_at<C::kRowBytes>(r + 8, j));
+          raw[0][0] = v0.x, raw[0][1] = v0.y, raw[0][2] = v0.z, raw[0][3] = v0.w;
+          raw[1][0] = v1.x, raw[1][1] = v1.y, raw[1][2] = v1.z, raw[1][3] = v1.w;
+          const uint32_t s0 = lds_u16(ks + r * 8 + 2 * j), s1 = lds_u16(ks + (r + 8) * 8 + 2 * j);
+          e4m3x4_to_f16x2(__byte_perm(s0, s1, 0x5410), scale[0], scale[1]);
+        } else {
+          const uint2 v0 = lds8(kt + piece_at<C::kRowBytes>(r, j >> 1) + 8 * (j & 1));
+          const uint2 v1 = lds8(kt + piece_at<C::kRowBytes>(r + 8, j >> 1) + 8 * (j & 1));
+          raw[0][0] = v0.x, raw[0][1] = v0.y;
+          raw[1][0] = v1.x, raw[1][1] = v1.y;
+          const uint32_t s0 = lds_u8(ks + r * 4 + j), s1 = lds_u8(ks + (r + 8) * 4 + j);
+          e4m3x4_to_f16x2(__byte_perm(s0, s1, 0x4400), scale[0], scale[1]);
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t f0[4], f1[4];
+          e2m1x8_to_f16x2(raw[0][w], f0);
+          e2m1x8_to_f16x2(raw[1][w], f1);
+          const uint32_t x0 = half_of(scale[0], w >> 1), x1 = half_of(scale[1], w >> 1);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const uint32_t f[4] = {mul_f16x2(f0[2 * z], x0), mul_f16x2(f1[2 * z], x1), mul_f16x2(f0[2 * z + 1], x0),
+                                   mul_f16x2(f1[2 * z + 1], x1)};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint2 y = q_of(t, 2 * w + z);
+              mma16816h(sc[u][t], f, y.x, y.y);
+            }
+          }
+        }
+      }
+      if (key + kKeys > lim_min) {  // some row does not see all of this
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[u][t][e] = 0.f;
-          const int r = kChunk * (u0 + u) + i8;
-          uint32_t raw[2][D / 32], scale[2];  // of keys r and r + 8: 8 codes to a word; scales of the words' halves
-          if constexpr (D == 128) {
-            const uint4 v0 = lds16(kt + piece_at<C::kRowBytes>(r, j)), v1 = lds16(kt + piece_at<C::kRowBytes>(r + 8, j));
-            raw[0][0] = v0.x, raw[0][1] = v0.y, raw[0][2] = v0.z, raw[0][3] = v0.w;
-            raw[1][0] = v1.x, raw[1][1] = v1.y, raw[1][2] = v1.z, raw[1][3] = v1.w;
-            const uint32_t s0 = lds_u16(ks + r * 8 + 2 * j), s1 = lds_u16(ks + (r + 8) * 8 + 2 * j);
-            e4m3x4_to_f16x2(__byte_perm(s0, s1, 0x5410), scale[0], scale[1]);
-          } else {
-            const uint2 v0 = lds8(kt + piece_at<C::kRowBytes>(r, j >> 1) + 8 * (j & 1));
-            const uint2 v1 = lds8(kt + piece_at<C::kRowBytes>(r + 8, j >> 1) + 8 * (j & 1));
-            raw[0][0] = v0.x, raw[0][1] = v0.y;
-            raw[1][0] = v1.x, raw[1][1] = v1.y;
-            const uint32_t s0 = lds_u8(ks + r * 4 + j), s1 = lds_u8(ks + (r + 8) * 4 + j);
-            e4m3x4_to_f16x2(__byte_perm(s0, s1, 0x4400), scale[0], scale[1]);
-          }
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            uint32_t f0[4], f1[4];
-            e2m1x8_to_f16x2(raw[0][w], f0);
-            e2m1x8_to_f16x2(raw[1][w], f1);
-            const uint32_t x0 = half_of(scale[0], w >> 1), x1 = half_of(scale[1], w >> 1);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t f[4] = {mul_f16x2(f0[2 * z], x0), mul_f16x2(f1[2 * z], x1), mul_f16x2(f0[2 * z + 1], x0),
-                                     mul_f16x2(f1[2 * z + 1], x1)};
-#pragma unroll
-              for (int t = 0; t < NT; ++t) {
-                const uint2 y = q_of(t, 2 * w + z);
-                mma16816h(sc[u][t], f, y.x, y.y);
-              }
-            }
-          }
+            for (int e = 0; e < 4; ++e)
+              if (key + kChunk * u + 8 * (e >> 1) + i8 >= lim[t][e & 1]) sc[u][t][e] = -INFINITY;
+        // A NaN scale of V must not meet the zero weights of rows that do not see it: zeros take its place,
+        // and the channels of the rows that do see it become NaN here.
+        constexpr int kCount = kKeys * C::kScales;
+        bool nan = false;
+        for (int x = 4 * lane; x < kCount; x += 128) {
+          const uint32_t four = lds4(vs + x);
+          nan = nan || (((four & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
         }
-        if (first + kChunk * kAt > lim_min) {  // some row does not see all of this
-#pragma unroll
-          for (int u = 0; u < kAt; ++u)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (first + kChunk * u + 8 * (e >> 1) + i8 >= lim[t][e & 1]) sc[u][t][e] = -INFINITY;
-          // A NaN scale of V must not meet the zero weights of rows that do not see it: zeros take its place,
-          // and the channels of the rows that do see it become NaN here.
-          constexpr int kCount = kAt * kChunk * C::kScales;
-          const uint32_t mine = vs + kChunk * C::kScales * u0;
-          bool nan = false;
-          for (int x = 4 * lane; x < kCount; x += 128) {
-            const uint32_t four = lds4(mine + x);
-            nan = nan || (((four & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
-          }
-          if (__any_sync(0xffffffffu, nan)) {
+        if (__any_sync(0xffffffffu, nan)) {
 #pragma unroll 1
-            for (int x = 0; x < kCount; ++x) {  // key x / kScales, group x % kScales
-              if ((lds_u8(mine + x) & 0x7fu) != 0x7fu) continue;
-              __syncwarp();
-              if (lane == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(mine + x), "r"(0) : "memory");
-              const int g = x % C::kScales;
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c)
-                if (g == 2 * (c >> 1) + (lane >> 4))
-#pragma unroll
-                  for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      if (first + x / C::kScales < lim[t][e & 1]) acc[c][t][e] = __uint_as_float(0x7fc00000u);
-            }
+          for (int x = 0; x < kCount; ++x) {  // key x / kScales, group x % kScales
+            if ((lds_u8(vs + x) & 0x7fu) != 0x7fu) continue;
             __syncwarp();
+            if (lane == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(vs + x), "r"(0) : "memory");
+            const int g = x % C::kScales;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+              if (g == 2 * (c >> 1) + (lane >> 4))
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if (key + x / C::kScales < lim[t][e & 1]) acc[c][t][e] = __uint_as_float(0x7fc00000u);
           }
+          __syncwarp();
         }
-        // raise the running maxima only when some row's grew by more than 2^8
-        bool grow = false;
-        float top[NT][2];
+      }
+      // raise the running maxima only when some row's grew by more than 2^8
+      bool grow = false;
+      float top[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[t][e] = max3f(fmaxf(sc[0][t][e], sc[0][t][2 + e]), sc[1][t][e], sc[1][t][2 + e]);
+          top[t][e] *= factor[t][e];
+          grow = grow || top[t][e] > m[t][e] + (kGrow + kUp);
+        }
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            top[t][e] = fmaxf(sc[0][t][e], sc[0][t][2 + e]);
-            if constexpr (kAt == 2) top[t][e] = fmaxf(top[t][e], fmaxf(sc[kAt - 1][t][e], sc[kAt - 1][t][2 + e]));
-            top[t][e] *= factor[t][e];
-            grow = grow || top[t][e] > m[t][e] + (kGrow + kUp);
+            float to = top[t][e] - kUp;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+            to = fmaxf(to, m[t][e]);
+            const float f = to == -INFINITY ? 1.f : fast_exp2(m[t][e] - to);
+            m[t][e] = to;
+            less[t][e] = to == -INFINITY ? 0.f : -to;
+            l[t][e] *= f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              acc[c][t][e] *= f;
+              acc[c][t][2 + e] *= f;
+            }
           }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float to = top[t][e] - kUp;
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
-              to = fmaxf(to, m[t][e]);
-              const float f = to == -INFINITY ? 1.f : fast_exp2(m[t][e] - to);
-              m[t][e] = to;
-              less[t][e] = to == -INFINITY ? 0.f : -to;
-              l[t][e] *= f;
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                acc[c][t][e] *= f;
-                acc[c][t][2 + e] *= f;
-              }
-            }
-        }
-        // P^T: the packed pairs are (key; rows 2 j, 2 j + 1) and are wanted as (row; keys 2 j, 2 j + 1). In f16:
-        // off by 2^-11 of itself, or 2^-25 where the row's largest weight is 2^7 at least.
-        uint32_t pt[kAt][NT][2];
-#pragma unroll
-        for (int u = 0; u < kAt; ++u)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float2 x = ffma2(sc[u][t][2 * y], sc[u][t][2 * y + 1], factor[t][0], factor[t][1], less[t][0], less[t][1]);
-              const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-              const float2 sum = fadd2(l[t][0], l[t][1], p0, p1);
-              l[t][0] = sum.x;
-              l[t][1] = sum.y;
-              pt[u][t][y] = transpose8x8(pack_f16(p0, p1));
-            }
-#pragma unroll
-        for (int u = 0; u < kAt; ++u)
-          each_v<D>(vt + kChunk * (u0 + u) * C::kRowBytes, vs + kChunk * (u0 + u) * C::kScales, lane,
-                    [&](int c, const uint32_t(&v)[4]) {
-#pragma unroll
-                      for (int t = 0; t < NT; ++t) mma16816h(acc[c][t], v, pt[u][t][0], pt[u][t][1]);
-                    });
       }
+      // P^T: the packed pairs are (key; rows 2 j, 2 j + 1) and are wanted as (row; keys 2 j, 2 j + 1). In f16:
+      // off by 2^-11 of itself, or 2^-25 where the row's largest weight is 2^7 at least.
+      uint32_t pt[2][NT][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float2 x = ffma2(sc[u][t][2 * y], sc[u][t][2 * y + 1], factor[t][0], factor[t][1], less[t][0], less[t][1]);
+            const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+            const float2 sum = fadd2(l[t][0], l[t][1], p0, p1);
+            l[t][0] = sum.x;
+            l[t][1] = sum.y;
+            pt[u][t][y] = transpose8x8(pack_f16(p0, p1));
+          }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        each_v<D>(vt + kChunk * u * C::kRowBytes, vs + kChunk * u * C::kScales, lane,
+                  [&](int c, const uint32_t(&v)[4]) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma16816h(acc[c][t], v, pt[u][t][0], pt[u][t][1]);
+                  });
     }
     cp_wait<0>();
 
@@ -580,7 +574,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<NT>) few4_kernel(const Att
 template <int D, int NT>
 fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int max_new, cudaStream_t s) {
   using C = Cfg<D, NT>;
-  using P = FewRows<8 * NT>;
+  using P = Rows<NT>;
   constexpr int kSmem = std::max(kWarps * C::kWarpBytes, kWarps * P::kRows * (D + 4) * 4);
   const int blocks = std::min(kPerSm<NT> * n_sm, kMaxBlocks);
   set_workspace<P>(a, workspace, D, kMaxBlocks);

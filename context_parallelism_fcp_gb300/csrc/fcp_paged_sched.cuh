@@ -55,7 +55,7 @@ __device__ __forceinline__ int granules_of(int end) { return max(1, (end + kGran
 // Units of a policy: units(s, group) and granules(s, group, unit, causal).
 //
 // Few rows: row r of a KV head is (new token r / group, head r % group); a unit is kRows of them.
-template <int kRowsPerUnit>
+template <int kRowsPerUnit, int kOverheadGranules = 1>
 struct FewRows {
   static constexpr int kRows = kRowsPerUnit;
   // A block's share is two granules at least: finer pieces cost more in the merge than they save (40
@@ -63,7 +63,7 @@ struct FewRows {
   // 1000, 4 KV heads: 13.7, 11.0, 11.5).
   static constexpr int kLeastShare = 2;
   static constexpr int kWarpPieces = 8;  // of a row, up to which the merge gives a row to a warp
-  static constexpr int kOverhead = 1;
+  static constexpr int kOverhead = kOverheadGranules;
   static __device__ __forceinline__ int units(const SeqShape& s, int group) {
     return static_cast<int>((static_cast<long long>(s.n) * group + kRows - 1) / kRows);
   }
