@@ -679,7 +679,9 @@ def __getattr__(name):
     if name in _PAGED_NAMES:
         from . import paged, rotary
 
-        return getattr(paged if hasattr(paged, name) else rotary, name)
+        for module in (paged, rotary):  # found at once from now on
+            globals().update((x, getattr(module, x)) for x in module.__all__)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

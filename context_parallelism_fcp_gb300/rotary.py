@@ -114,41 +114,49 @@ class Rotary(_Owner):
         self._ref = ctypes.byref(self._struct)
 
 
+def _outlike(x, stream):
+    """A tensor like x, as memory of the stream that the call runs on."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=x.device)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(x)
+
+
 def _apply(rotary: Rotary, q, k, positions, q_out, k_out, stream, backward: int):
     index = rotary._index
-    if q is None and k is None:
-        raise ValueError("there is neither q nor k")
-    one = q if q is not None else k
-    if not isinstance(one, torch.Tensor) or one.dim() != 3:
-        raise ValueError("q and k must be tensors [heads, T, D]")
     raw = _here(index, stream, "frequencies")
+    one = k if q is None else q
+    if not isinstance(one, torch.Tensor) or one.dim() != 3 or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 3)):
+        raise ValueError("q and k must be tensors [heads, T, D], one of them at least")
     _, T, D = one.shape
-    _want(positions, torch.int32, (T,), index, "positions")
-    outs, args = [], []
-    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
-        heads = 0
-        if x is not None:
-            if not isinstance(x, torch.Tensor) or x.dim() != 3:
-                raise ValueError("q and k must be tensors [heads, T, D]")
-            heads = x.shape[0]
-            _want(x, torch.bfloat16, (heads, T, D), index, name)
-            if out is None:
-                if stream is not None and not isinstance(stream, torch.cuda.Stream):
-                    stream = torch.cuda.ExternalStream(raw, device=x.device)
-                with torch.cuda.stream(stream):
-                    out = torch.empty_like(x)
-            else:
-                _want(out, torch.bfloat16, (heads, T, D), index, name + "_out")
-        elif out is not None:
-            raise ValueError(f"{name}_out without {name}")
-        outs.append(out)
-        args += [x.data_ptr() if heads else None, out.data_ptr() if heads else None, heads]
+    _want(positions, torch.int32, (T,), index, "positions", "frequencies")
+    hq = hkv = 0
+    if q is not None:
+        hq, shape = q.shape[0], q.shape
+        _want(q, torch.bfloat16, shape, index, "q", "frequencies")
+        if q_out is None:
+            q_out = _outlike(q, stream)
+        else:
+            _want(q_out, torch.bfloat16, shape, index, "q_out", "frequencies")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        hkv, shape = k.shape[0], (k.shape[0], T, D)
+        _want(k, torch.bfloat16, shape, index, "k", "frequencies")
+        if k_out is None:
+            k_out = _outlike(k, stream)
+        else:
+            _want(k_out, torch.bfloat16, shape, index, "k_out", "frequencies")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     if raw not in rotary._streams:
         rotary._note(raw, stream)
-    status = lib().fcp_rotary_apply(rotary._ref, positions.data_ptr(), T, *args, D, backward, raw)
+    status = lib().fcp_rotary_apply(rotary._ref, positions.data_ptr(), T, q.data_ptr() if hq else None,
+                                    q_out.data_ptr() if hq else None, hq, k.data_ptr() if hkv else None,
+                                    k_out.data_ptr() if hkv else None, hkv, D, backward, raw)
     if status:
         _check(status, "fcp_rotary_apply")
-    return tuple(outs)
+    return q_out, k_out
 
 
 def rotary_apply(rotary: Rotary, q, k, positions, q_out=None, k_out=None, stream=None):
@@ -182,10 +190,7 @@ def rotary_write(cache: PagedCache, batch: CacheBatch, rotary: Rotary, q, k, v, 
         hq = q.shape[0]
         _want(q, torch.bfloat16, (hq, *shape[1:]), index, "q")
         if q_out is None:
-            if stream is not None and not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(raw, device=q.device)
-            with torch.cuda.stream(stream):
-                q_out = torch.empty_like(q)
+            q_out = _outlike(q, stream)
         else:
             _want(q_out, torch.bfloat16, (hq, *shape[1:]), index, "q_out")
     elif q_out is not None:
