@@ -1,8 +1,8 @@
 """Rotary positions on the GPU against their float64 definition (oracle/rotary.py).
 
-Tolerance: the angle is right to 2^-32 of a turn and rounded to float32 (2^-25 half turns at most:
-2^-23.3 radians), cos and sin to two units (2^-23), and the factor, two products and a sum round to float32
-(2^-24 of the pair's size each); together below 2^-21 m (|a| + |b|). The result is rounded to bf16 once:
+Tolerance: the angle is right to 2^-32 of a turn (2^-29 radians), m cos and m sin to two units (2^-22.9 m at
+most), and two products and a sum round to float32 (2^-24 of the pair's size each); together below
+2^-21 m (|a| + |b|). The result is rounded to bf16 once:
 2^-8 of itself."""
 import numpy as np
 import pytest
