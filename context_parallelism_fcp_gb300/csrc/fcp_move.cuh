@@ -168,11 +168,4 @@ __device__ __forceinline__ uint32_t quantise4(const uint4 x, uint32_t top, float
   return finite ? __byte_perm(__byte_perm(c[0], c[1], 0x3240), __byte_perm(c[2], c[3], 0x3240), 0x5410) : 0u;
 }
 
-// The same for the 8 channels of this lane; its neighbour has the other 8.
-__device__ __forceinline__ uint32_t quantise4(const uint4 x, float per_unit, uint32_t& scale_byte) {
-  uint32_t two = top_pair(x);
-  two = max_u16x2(two, __shfl_xor_sync(0xffffffffu, two, 1));
-  return quantise4(x, max(two & 0xffffu, two >> 16), per_unit, scale_byte);
-}
-
 }  // namespace fcp

@@ -133,7 +133,7 @@ struct Marks {
   int b[kThreads];      // the stack's entries that those before it take
 };
 
-// grid (ceil(T / 1024))
+// A block does every gridDim.x-th 1024 rows.
 __global__ void __launch_bounds__(kThreads) admit_kernel(const PoolArgs p, const int32_t* new_tokens, int total_new,
                                                          int32_t* cu, int32_t* granted, int32_t* positions,
                                                          long long* slots) {
@@ -187,22 +187,10 @@ __global__ void __launch_bounds__(kThreads) admit_kernel(const PoolArgs p, const
       f(i, len, x, x > 0 ? pages : 0, row0, pg0);
     });
   };
-  const long long b0 = static_cast<long long>(blockIdx.x) * kThreads;
-  m.seq[tid] = -1;
-  __syncthreads();
   long long rows = 0, taken = 0;
-  each([&](int i, int len, int x, int pages, long long row0, long long pg0) {
-    if (x > 0) {
-      rows = row0 + x;
-      if (pages > 0) taken = pg0 + pages;
-      if (row0 < b0 + kThreads && row0 + x > b0) {
-        const int y = static_cast<int>(max(row0 - b0, 0ll));
-        m.seq[y] = i;
-        m.first[y] = static_cast<int>(row0 - b0);
-        m.a[y] = len;
-        m.b[y] = static_cast<int>(pg0);
-      }
-    }
+  each([&](int, int, int x, int pages, long long row0, long long pg0) {
+    if (x > 0) rows = row0 + x;
+    if (x > 0 && pages > 0) taken = pg0 + pages;
   });
   // all rows and pages that are given: the largest, as the threads' sequences are in order
 #pragma unroll
@@ -219,7 +207,20 @@ __global__ void __launch_bounds__(kThreads) admit_kernel(const PoolArgs p, const
     rows = max(rows, __shfl_xor_sync(0xffffffffu, rows, o));
     taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
   }
-  if (b0 < total_new) {
+  for (long long b0 = static_cast<long long>(blockIdx.x) * kThreads; b0 < total_new;
+       b0 += static_cast<long long>(gridDim.x) * kThreads) {
+    m.seq[tid] = -1;
+    __syncthreads();
+    each([&](int i, int len, int x, int, long long row0, long long pg0) {
+      if (x > 0 && row0 < b0 + kThreads && row0 + x > b0) {
+        const int y = static_cast<int>(max(row0 - b0, 0ll));
+        m.seq[y] = i;
+        m.first[y] = static_cast<int>(row0 - b0);
+        m.a[y] = len;
+        m.b[y] = static_cast<int>(pg0);
+      }
+    });
+    __syncthreads();
     const int y = max_scan(m.seq[tid] >= 0 ? tid : -1, m.warp_max);
     const long long row = b0 + tid;
     if (row < total_new) {
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(kThreads) admit_kernel(const PoolArgs p, const
       if (positions) positions[row] = pos;
       if (slots) slots[row] = slot;
     }
+    __syncthreads();
   }
   if (!last_block(p)) return;
   each([&](int i, int len, int x, int, long long row0, long long) {
@@ -371,7 +373,11 @@ extern "C" fcp_status fcp_pool_admit(const fcp_page_pool* pool, const int32_t* n
     return FCP_ERR_INVALID;
   if (p.n_seqs > 0 && (!new_tokens || !granted || !aligned4(new_tokens) || !aligned4(granted) || new_tokens == granted))
     return FCP_ERR_INVALID;
-  const unsigned blocks = static_cast<unsigned>(std::max(1, (total_new + kThreads - 1) / kThreads));
+  int dev = 0, n_sm = 0;
+  if (const fcp_status st = this_device(&dev, &n_sm); st != FCP_OK) return st;
+  // a block for 1 K rows, and no more blocks than run at once: each adds all sequences up (354000 rows of 300
+  // sequences, released and admitted: 17.9 us with a block for each 1 K rows, 12.6 so)
+  const unsigned blocks = static_cast<unsigned>(std::max(1, std::min((total_new + kThreads - 1) / kThreads, n_sm)));
   return launch_overlapped(admit_kernel, dim3(blocks), kThreads, 0, static_cast<cudaStream_t>(stream),
                            "page pool admit launch", p, new_tokens, static_cast<int>(total_new), cu_new, granted, positions,
                            reinterpret_cast<long long*>(slots));

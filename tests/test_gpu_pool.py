@@ -82,7 +82,8 @@ def same(pool, m):
 
 
 CASES = [(1, 16, 3, 2, 8), (5, 16, 4, 0, 40), (128, 64, 9, 40, 700), (300, 16, 130, 900, 5000), (1030, 32, 2, 50, 3000),
-         (2500, 16, 3, 300, 2100), (70, 4096, 2, 5, 9000), (7, 16, 700, 100, 1024)]
+         (2500, 16, 3, 300, 2100), (70, 4096, 2, 5, 9000), (7, 16, 700, 100, 1024),
+         (6, 64, 2200, 9000, 400000)]
 
 
 @pytest.mark.parametrize("n,page,width,spare,total", CASES, ids=str)
