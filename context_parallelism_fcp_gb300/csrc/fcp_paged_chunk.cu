@@ -10,9 +10,11 @@
 // keys come from. A key tile is 128 positions, gathered from their pages into the
 // 128-byte-swizzled layout that the matrix instructions read: a bf16 cache by TMA, one box for
 // each page and 64 channels, an e4m3 cache by six warps that turn codes into scaled bf16 on
-// their way to shared memory. That product with a power of two is exact, so the kernel computes
-// the attention over what reading the cache gives, and the tensor core runs the same bf16
-// instructions for both. Rows of V past the sequence become zeros, since a zero weight times
+// their way to shared memory, a 4-bit cache by the same warps into f16. These products with scales are exact,
+// so the kernel computes the attention over what reading the cache gives. The tensor core runs bf16
+// instructions for the first two and f16 ones for 4 bits, where Q's rows become f16 in place (each scaled
+// by a power of two, by the softmax warps) and P starts at 2^7: to bf16 a code would take five
+// operations for two instead of two. Rows of V past the sequence become zeros, since a zero weight times
 // whatever such a row holds may be NaN. So do an e4m3 cache's NaN rows of V, which rows that come
 // before them must not meet: a unit keeps the first position of one, and o of the rows that see it
 // becomes NaN when it is stored.
@@ -23,10 +25,16 @@
 // cache (1600 TFLOP/s) and 1710 us from an e4m3 one (1245), 8192 over 8192 735 and 965 us, 16 chunks
 // of 512 with nothing before them 156 and 192 us (a quarter of it writes o; what a unit costs beside
 // its one to four key tiles is most of the rest). Call after call the first two are 1440 to 1520 and
-// 1880 us: blocks then land on other SMs, and the slowest decides.
+// 1880 us: blocks then land on other SMs, and the slowest decides. A 4-bit cache: the first 1440 us (1480
+// TFLOP/s, call after call), the 16 chunks 221 us: Q's conversion and S wait for what the unit before stores.
+// Not faster for 4 bits: that conversion before the store (229 us) or by the loaders (233); loaders' groups
+// of 16 rows (16 chunks 199 us, but the first 1535 and 16 x 5 tokens over up to 8192 keys 488 instead of 338);
+// both by a unit's length in one code (1487); two groups of 16 in registers (1772: the fence that hands a
+// group over waits for loads in flight); groups by cp.async (1527) or by bulk copies of the walk's warp
+// (2908, one slot for each loader being all that fits) into shared memory first; prefetches to L2 (1490).
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1 (thread = row = TMEM lane); 8: the walk along the
-// block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 only): loaders.
+// block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 and e2m1): loaders.
 // TMEM columns: S_t at [128 t, 128 t + 128), overwritten by P_t as bf16; O_t at [256 + 128 t,
 // 256 + 128 t + D).
 #include <algorithm>

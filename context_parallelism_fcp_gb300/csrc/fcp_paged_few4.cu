@@ -11,6 +11,15 @@
 // channels of a key. V goes through ldmatrix.trans as 16-bit elements of four channels: a register
 // then has those of two keys, in its halves, and byte permutations put the same channel of both side by
 // side, as the product over keys wants them.
+//
+// Measured (8 KV heads, D = 128): 128 sequences of up to 8192 tokens, 8 query heads a KV head, 103 us (4970
+// GB/s, 74% of a copy's rate); of up to 32768, 348 us (87%): some 20 us are launch, merge and the beginnings and
+// ends of three pieces a block. 32 sequences of up to 4096 with 4 drafted tokens and 2, 4, 8 query heads a KV
+// head: 24.2, 28.6, 43.0 us. Issue slots 60% busy, the unit that converts and permutes 58%; with the
+// conversions of codes taken out the first case took 105.6 instead of 108.8 us (then), so it is the sum of
+// instructions and latencies at 12 warps an SM, not one of them. Not faster: copies that run on into the next
+// piece (106), codes put side by side by logic before the conversion (111 instead of 108.5), one chunk a
+// stage (114 instead of 108.5).
 #include <algorithm>
 
 #include "fcp_paged_few.cuh"
@@ -21,14 +30,19 @@ namespace {
 using namespace dev;
 using namespace few;
 
+// Blocks to an SM: more registers are worth more than more warps (one tile: 128 sequences of up to 8192 103 us
+// with three, 108 with four, of up to 32768 349 and 371; two tiles, 32 x 4 tokens: 28.9 with two, 30.4 with
+// three, but 21.2 and 20.3 at D = 64).
 template <int NT>
-constexpr int kPerSm = NT == 1 ? 3 : 2;  // blocks to an SM
+constexpr int kPerSm = NT == 1 ? 3 : 2;
+// A piece's beginning and end are as long on the line as 3 granules: with 1, 2, 3, 5 the first case took 107.4,
+// 104.2, 103.2, 104.9 us, 32 x 4 tokens of 8 heads 59.9, 46.4, 44.6, 47.6.
 template <int NT>
 using Rows = FewRows<8 * NT, 3>;
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kBudget = (kPerSm<NT> == 4 ? 50 : (kPerSm<NT> == 3 ? 67 : 97)) * 1024;  // of shared memory
+  static constexpr int kBudget = (kPerSm<NT> == 3 ? 67 : 97) * 1024;  // of shared memory
   static constexpr int kRowBytes = D / 2, kScales = D / 16;  // of a row of K or V
   static constexpr int kPieces = kRowBytes / 16;             // 16-byte pieces of a row
   // A stage is two chunks, whose overhead is shared and which are done together, for more independent
