@@ -742,7 +742,8 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
       const int lim_row = !mine ? INT32_MAX : (a.causal ? max(0, T.len - T.n + tok + 1) : T.len);
       float scale = a.scale_log2;
       if constexpr (kE2M1) {
-        if (!idle) scale *= q_to_f16<D>(smem + C::kQ + t * C::kTileBytes, r);
+        // never zero, which would make NaN of a masked score (what this does to others is below 2^-80)
+        if (!idle) scale = fmaxf(scale * q_to_f16<D>(smem + C::kQ + t * C::kTileBytes, r), 0x1p-120f);
         fence_proxy_async_smem();
         mbar_arrive_warp(bar(B_QREADY + t));
       }

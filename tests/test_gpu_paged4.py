@@ -218,6 +218,23 @@ def test_units(fcp, new, units):
     U.check_attention(b, t, o, lse, *before, *units)
 
 
+@pytest.mark.parametrize("unit", [2.0 ** -60, 1.0, 2.0 ** 60])
+@pytest.mark.parametrize("new,hq", [(1, 4), (3, 4), (3, 16), (50, 4)], ids=["few8", "few16", "few32", "chunk"])
+def test_rows_of_zeros_and_of_the_smallest_and_largest_numbers(fcp, new, hq, unit):
+    """A q of zeros weighs all keys the same, whatever the unit; so do q and units whose products are below float32's
+    range, beside rows that are masked."""
+    b = Batch([new, new], [100, 2 * new], hq=hq, hkv=1, d=128, page=32, seed=new)
+    t = U.make(b)
+    t["q"][0] = 0
+    t["q"][1] = torch.finfo(torch.bfloat16).tiny
+    t["q"][2, :, ::2] = 0
+    t["q"][2, :, 1::2] *= 2.0 ** -100 if unit >= 1 else 2.0 ** 50
+    o, lse, before = attend(fcp, b, t, *U.handles(fcp, b, t, unit, 1.0))
+    for h in (0, 1, 2):  # one head at a time, as a batch of its own
+        one = Batch(b.new, b.lens, hq=1, hkv=1, d=128, page=32)
+        U.check_attention(one, {**t, "q": t["q"][h:h + 1]}, o[h:h + 1], lse[h:h + 1], before[0][h:h + 1], before[1][h:h + 1], unit, 1.0)
+
+
 @pytest.mark.parametrize("new,hq", [(1, 2), (4, 2), (4, 4), (4, 8), (50, 2)], ids=["few1", "few8", "few16", "few32", "chunk"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_nan_scale_reaches_its_readers_only(fcp, new, hq, d):
