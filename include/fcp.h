@@ -440,7 +440,7 @@ size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
  * query head h, the softmax of q . k / sqrt(D) over the sequence's keys 0 .. p (causal != 0) or
  * 0 .. lens[i] - 1 (causal = 0) of KV head h / (Hq / Hkv), giving o (bf16) and the natural
  * log-sum-exp lse. q and o are [Hq, total_new, D], lse [Hq, total_new] float32. The new tokens'
- * own K and V have to be in the cache already (fcp_cache_write). An e4m3 cache gives the
+ * own K and V have to be in the cache already (fcp_cache_write). An e4m3 or 4-bit cache gives the
  * attention over what fcp_cache_read returns. A row that sees no key gets o = 0, lse = -inf.
  * Rows of the pages past a sequence's length may hold anything, NaN included. A NaN row of an
  * e4m3 cache (scale byte 255) reaches the rows that see it and no others; a NaN or infinity that a
@@ -448,7 +448,10 @@ size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
  * (pages filled otherwise than by fcp_cache_write), may reach, in its channel, the new tokens of
  * the same sequence that come before it. Sums, maxima and the softmax's statistics are float32; P is
  * rounded to bf16 (f16 in the kernel for few rows of an e4m3 cache: off by 2^-11 of itself, or
- * 2^-22 of the row's largest weight) for the product with V.
+ * 2^-22 of the row's largest weight; f16 for a 4-bit cache: 2^-11 or 2^-32) for the product with V. A
+ * NaN scale of a 4-bit cache's V reaches the rows that see it and no others, in its 16 channels or in
+ * all of o; one of K makes the rows that see it NaN. A 4-bit cache's q is taken as f16 times a power of two
+ * for each row: what is below 2^-28 of a row's largest element may be lost.
  * Results do not depend on timing: no atomics are used. o and lse must not overlap the inputs.
  * workspace: fcp_paged_attn_workspace_bytes, 256-byte aligned, its contents need not be
  * kept or cleared; calls whose work may overlap need one each. Errors: FCP_ERR_INVALID (also
