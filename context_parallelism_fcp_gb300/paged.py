@@ -6,7 +6,8 @@ of the same names. ``PagePool`` gives pages to sequences and takes them back, on
 and all the work is done by the library's kernels, on the caller's stream. That may be any stream: what a
 cache or an attention allocates stays theirs until the work of every stream that they were used on is done.
 (Tensors of the caller's follow torch's rule: one that is used on another stream than its own and then dropped
-is the caller's to record there. A graph's tensors and objects have to outlive it.)
+is the caller's to record there. A batch of a PagePool's keeps the pool. A graph's tensors and objects have
+to outlive it.)
 """
 from __future__ import annotations
 
@@ -182,6 +183,7 @@ class CacheBatch:
         self.cu_new, self.lens, self.block_table = cu_new, lens, block_table
         self.n_seqs, self.total_new, self.max_new, self.device = n, int(total_new), int(max_new), lens.device
         self._index = lens.get_device()
+        self._pool = None  # the PagePool whose tensors these are
         self._struct = _CacheBatchStruct(cu_new.data_ptr(), lens.data_ptr(), block_table.data_ptr(), n,
                                          block_table.shape[1], self.total_new, self.max_new)
         self._ref = ctypes.byref(self._struct)
@@ -197,6 +199,8 @@ def _move(fn, name, cache: PagedCache, batch: CacheBatch, k, v, stream) -> None:
     raw = _here(index, stream)
     if raw not in cache._streams:
         cache._note(raw, stream)
+    if batch._pool is not None and raw not in batch._pool._streams:
+        batch._pool._note(raw, stream)
     status = fn(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), raw)
     if status:
         _check(status, name)
@@ -240,6 +244,8 @@ def _attend(fn, cache, batch, q, o, lse, workspace, workspace_bytes, causal, hq,
         cache._note(raw, stream)
     if owner is not None and raw not in owner._streams:
         owner._note(raw, stream)
+    if batch._pool is not None and raw not in batch._pool._streams:
+        batch._pool._note(raw, stream)
     status = fn(cache._ref, batch._ref, q.data_ptr(), hq, causal, o.data_ptr(), lse.data_ptr(), workspace,
                 workspace_bytes, raw)
     if status:
@@ -364,7 +370,9 @@ class PagePool(_Owner):
     def batch(self, total_new: int, max_new: int) -> CacheBatch:
         """The CacheBatch of the tokens that were admitted last: it reads this pool's tensors, so one
         serves every step of ``total_new`` packed rows."""
-        return CacheBatch(self.cu_new, self.lens, self.block_table, total_new, max_new)
+        batch = CacheBatch(self.cu_new, self.lens, self.block_table, total_new, max_new)
+        batch._pool = self
+        return batch
 
     def check_device_error(self, stream=None) -> None:
         """Synchronise and raise if a call found the pool's state broken (see fcp_page_pool)."""

@@ -195,8 +195,8 @@ def rotary_write(cache: PagedCache, batch: CacheBatch, rotary: Rotary, q, k, v, 
             _want(q_out, torch.bfloat16, (hq, *shape[1:]), index, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    for owner in (cache, rotary):
-        if raw not in owner._streams:
+    for owner in (cache, rotary, batch._pool):
+        if owner is not None and raw not in owner._streams:
             owner._note(raw, stream)
     status = lib().fcp_rotary_write(cache._ref, batch._ref, rotary._ref, q.data_ptr() if hq else None,
                                     q_out.data_ptr() if hq else None, hq, k.data_ptr(), v.data_ptr(), raw)

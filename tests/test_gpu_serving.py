@@ -124,3 +124,43 @@ def test_two_steps_at_once_on_two_streams(fcp):
             o, lse = step(i)
             total = int(pool.cu_new[-1])
             assert torch.equal(o[:, :total], outs[s][i][0][:, :total]) and torch.equal(lse[:, :total], outs[s][i][1][:, :total])
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle"])
+def test_a_pool_and_frequencies_dropped_while_another_stream_works(fcp, kind):
+    """What a pool and a Rotary allocated is not handed out again while a stream that their batch was used on has
+    work left: here their memory is asked for and overwritten before that work has run."""
+    hq, hkv, d, page, n, T = 4, 2, 64, 16, 50, 128
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, k, v = (torch.randn(h, T, d, generator=g, device="cuda", dtype=torch.bfloat16) for h in (hq, hkv, hkv))
+    new = ints([2] * n)
+    cache = fcp.PagedCache(200, page, hkv, d, torch.float4_e2m1fn_x2)
+    att = fcp.PagedAttention(cache, hq)
+
+    def begin():
+        pool, rot = fcp.PagePool(200, page, n, 40), fcp.Rotary(d)
+        pool.admit(new, total_new=T)
+        torch.cuda.synchronize()
+        return pool.batch(T, max_new=2), rot
+
+    out = [[torch.zeros_like(q), torch.zeros_like(q), torch.zeros(hq, T, device="cuda")] for _ in range(2)]
+    batch, rot = begin()
+    fcp.rotary_write(cache, batch, rot, q, k, v, out[0][0])
+    att.forward(batch, out[0][0], *out[0][1:])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = side if kind == "stream" else side.cuda_stream
+    batch, rot = begin()
+    sizes = [x.numel() for x in (batch.lens, batch.cu_new, batch.block_table)] + [2 * rot.turns.numel()]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(1e8))
+    fcp.rotary_write(cache, batch, rot, q, k, v, out[1][0], stream=stream)
+    att.forward(batch, out[1][0], *out[1][1:], stream=stream)
+    del batch, rot
+    junk = [torch.full((x,), 77, dtype=torch.int32, device="cuda") for x in sizes for _ in range(20)]
+    torch.cuda.synchronize()
+    cache.check_device_error()
+    for x, y in zip(*out):
+        assert torch.equal(x, y)
+    del junk
