@@ -195,9 +195,12 @@ def rotary_write(cache: PagedCache, batch: CacheBatch, rotary: Rotary, q, k, v, 
             _want(q_out, torch.bfloat16, (hq, *shape[1:]), index, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    for owner in (cache, rotary, batch._pool):
-        if owner is not None and raw not in owner._streams:
-            owner._note(raw, stream)
+    if raw not in cache._streams:
+        cache._note(raw, stream)
+    if raw not in rotary._streams:
+        rotary._note(raw, stream)
+    if batch._pool is not None and raw not in batch._pool._streams:
+        batch._pool._note(raw, stream)
     status = lib().fcp_rotary_write(cache._ref, batch._ref, rotary._ref, q.data_ptr() if hq else None,
                                     q_out.data_ptr() if hq else None, hq, k.data_ptr(), v.data_ptr(), raw)
     if status:

@@ -182,7 +182,8 @@ def test_offsets_past_32_bits(fcp):
     check(rot, q[:1, :500], out[:1, :500], positions[:500])
 
 
-def test_the_attention_with_rotary(fcp):
+@pytest.mark.parametrize("pipeline", [None, 2])
+def test_the_attention_with_rotary(fcp, pipeline):
     """FcpAttention(rotary=...): the attention over turned q and k, and its gradients turned back; dq and dk are
     bf16 before they are turned, so twice the rounding."""
     seqlens, hq, hkv, d = [300, 77, 1024], 4, 2, 64
@@ -190,8 +191,8 @@ def test_the_attention_with_rotary(fcp):
     g = torch.Generator(device="cuda").manual_seed(0)
     q, k, v, do = (torch.randn(h, T, d, generator=g, device="cuda", dtype=torch.bfloat16) for h in (hq, hkv, hkv, hq))
     rot = fcp.Rotary(d)
-    att = fcp.FcpAttention(seqlens, 512, True, 4, hq, hkv, d, rotary=rot)
-    plain = fcp.FcpAttention(seqlens, 512, True, 4, hq, hkv, d)
+    att = fcp.FcpAttention(seqlens, 512, True, 4, hq, hkv, d, rotary=rot, pipeline=pipeline)
+    plain = fcp.FcpAttention(seqlens, 512, True, 4, hq, hkv, d, pipeline=pipeline)
     positions = torch.cat([torch.arange(n, dtype=torch.int32) for n in seqlens]).cuda()
     assert torch.equal(att.positions, positions)
     keep = q.clone(), k.clone()
@@ -207,8 +208,16 @@ def test_the_attention_with_rotary(fcp):
         want, size = R.turn(raw.double().cpu().numpy(), positions.cpu().numpy(), rot.radians, 1.0, False, backward=True)
         err = np.abs(got.double().cpu().numpy() - want)
         assert (err <= 2.0 ** -8 * np.abs(want) + (2.0 ** -7 + 2.0 ** -20) * size + 1e-4).all()
-    att.replan([77, 300, 1024])
-    assert att.positions[76].item() == 76 and att.positions[77].item() == 0
+    # on another stream, by its handle, the same
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o3, lse3 = torch.zeros_like(o), torch.zeros_like(lse)
+    att.forward(q, k, v, o3, lse3, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(o3, o) and torch.equal(lse3, lse)
+    if pipeline is None:
+        att.replan([77, 300, 1024])
+        assert att.positions[76].item() == 76 and att.positions[77].item() == 0
     with pytest.raises(ValueError, match="rotary_dim"):
         fcp.FcpAttention(seqlens, 512, True, 4, hq, hkv, d, rotary=fcp.Rotary(128))
 
