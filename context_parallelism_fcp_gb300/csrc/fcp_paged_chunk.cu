@@ -26,9 +26,9 @@
 // of 512 with nothing before them 156 and 192 us (a quarter of it writes o; what a unit costs beside
 // its one to four key tiles is most of the rest). Call after call the first two are 1440 to 1520 and
 // 1880 us: blocks then land on other SMs, and the slowest decides. A 4-bit cache: the first 1440 us (1480
-// TFLOP/s, call after call), the 16 chunks 221 us: Q's conversion and S wait for what the unit before stores.
-// Not faster for 4 bits: that conversion before the store (229 us) or by the loaders (233); loaders' groups
-// of 16 rows (16 chunks 199 us, but the first 1535 and 16 x 5 tokens over up to 8192 keys 488 instead of 338);
+// TFLOP/s, call after call), the 16 chunks 207 us: Q's conversion and S wait for what the unit before stores.
+// Not faster for 4 bits (of 221 us then): that conversion before the store (229 us) or by the loaders (233);
+// loaders' groups of 16 rows (199 us, but the first 1535 and 128 x 5 tokens over up to 8192 keys 488 instead of 338);
 // both by a unit's length in one code (1487); two groups of 16 in registers (1772: the fence that hands a
 // group over waits for loads in flight); groups by cp.async (1527) or by bulk copies of the walk's warp
 // (2908, one slot for each loader being all that fits) into shared memory first; prefetches to L2 (1490).
