@@ -28,13 +28,14 @@
 // 1880 us: blocks then land on other SMs, and the slowest decides. A 4-bit cache: the first 1440 us (1480
 // TFLOP/s, call after call), the 16 chunks 207 us: Q's conversion and S wait for what the unit before stores.
 // Not faster for 4 bits (of 221 us then): that conversion before the store (229 us) or by the loaders (233);
-// loaders' groups of 16 rows (199 us, but the first 1535 and 128 x 5 tokens over up to 8192 keys 488 instead of 338);
+// loaders' groups of 16 rows (199 us, but the first 1535), or of 64 (255 and 1945);
 // both by a unit's length in one code (1487); two groups of 16 in registers (1772: the fence that hands a
 // group over waits for loads in flight); groups by cp.async (1527) or by bulk copies of the walk's warp
 // (2908, one slot for each loader being all that fits) into shared memory first; prefetches to L2 (1490).
 //
-// Warps 0-3 and 4-7: softmax of tile 0 and 1 (thread = row = TMEM lane); 8: the walk along the
-// block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 and e2m1): loaders.
+// Warps 0-3 and 4-7: softmax of tile 0 and 1, or of the first and second 64 keys of the only one (thread = row =
+// TMEM lane); 8: the walk along the
+// block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 and e2m1) or 10-17: loaders.
 // TMEM columns: S_t at [128 t, 128 t + 128), overwritten by P_t as bf16; O_t at [256 + 128 t,
 // 256 + 128 t + D).
 #include <algorithm>
@@ -48,17 +49,22 @@ namespace {
 
 using namespace dev;
 
-constexpr int kLoaders = 6;  // warps
-template <int kKind>
-constexpr int kThreads = 32 * (10 + (kKind != FCP_CACHE_BF16 ? kLoaders : 0));
+template <int kKind, bool kHalves>
+constexpr int kLoaders = kKind == FCP_CACHE_BF16 ? 0 : (kHalves ? 8 : 6);  // warps
+template <int kKind, bool kHalves>  // halves: two warps do nothing, as registers are given out to four at a time
+constexpr int kThreads = 32 * (10 + kLoaders<kKind, kHalves> + (kHalves ? 2 : 0));
 constexpr int kPanelBytes = kTileM * 128;  // 128 rows x 64 bf16 channels
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr float kUp = 7.0f;                 // e2m1: P starts at 2^7 and grows to 2^15, the top of f16
 constexpr int kQBox = 16;                   // tokens of a TMA load of Q for tiles of several heads
-// Registers a thread with the loader warps: the launch gives 128, and the softmax warps take
-// what the others leave (they hold a row of 128 scores).
-constexpr int kRegsSoftmax = 168, kRegsOther = 88;
-static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * 128, "the split fits the launch's registers");
+// Registers a thread with the loader warps: the launch gives 128 (halves: 96), and the softmax warps take
+// what the others leave (they hold a row of 128 scores, or of 64).
+template <bool kHalves>
+constexpr int kRegsSoftmax = kHalves ? 120 : 168;
+template <bool kHalves>
+constexpr int kRegsOther = kHalves ? 80 : 88;
+static_assert(2 * kRegsSoftmax<false> + 2 * kRegsOther<false> <= 4 * 128, "the split fits the launch's registers");
+static_assert(2 * kRegsSoftmax<true> + 3 * kRegsOther<true> <= 5 * 96, "the split fits the launch's registers");
 
 enum : int {
   B_QFULL = 0,
@@ -69,13 +75,14 @@ enum : int {
   B_VEMPTY = 8,
   B_SFULL = 10,  // per tile
   B_PFULL = 12,  // per tile and half: keys [0, 64) and [64, 128) of P are in TMEM
-  B_ODONE = 16,  // per tile
+  B_ODONE = 16,  // per tile; halves: of a key tile, and of a unit
   B_OFREE = 18,  // per tile: the epilogue has read O_t out of TMEM
   B_DRAIN = 20,
   B_TFULL = 21,   // 2 slots: the next unit is published
   B_TEMPTY = 23,  // 2 slots: the MMA, softmax and loader warps have read it
   B_QREADY = 25,  // e2m1, per tile: Q is f16
-  B_COUNT = 27
+  B_PAIR = 27,    // halves, twice a unit: Q's rows have been looked at, the groups' sums are there
+  B_COUNT = 28
 };
 
 // A block's piece of a group: key tiles [kt0, kt1) of unit u.
@@ -138,11 +145,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // Row r of a tile of Q in shared memory from bf16 to f16 in place, scaled by 2^(14 - e) with e the row's
-// largest exponent; returns 2^(e - 14). A lane begins at its own 16 bytes of a row, so that neighbours
+// largest exponent; returns 2^(e - 14). Pieces [c0, c1) of 8 channels, behind looked(). A lane begins at its own 16 bytes of a row, so that neighbours
 // are on different banks. (Not unrolled: once a unit, its instructions come from far away. 16 chunks of 512 with
 // nothing before them 220 us instead of 235.)
-template <int D>
-__device__ __forceinline__ float q_to_f16(uint8_t* tile, int r) {
+template <int D, class F>
+__device__ __forceinline__ float q_to_f16(uint8_t* tile, int r, int c0, int c1, F looked) {
   uint32_t top = 0;
   auto piece = [&](int c) -> uint4* {
     return reinterpret_cast<uint4*>(tile + (c >> 3) * kPanelBytes + r * 128 + (((c + r) & 7) << 4));
@@ -156,8 +163,9 @@ __device__ __forceinline__ float q_to_f16(uint8_t* tile, int r) {
   }
   const int up = min(126, 141 - static_cast<int>(top >> 7));  // of rows past 2^-112
   const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+  looked();
 #pragma unroll 1
-  for (int c = 0; c < D / 8; ++c) {
+  for (int c = c0; c < c1; ++c) {
     const uint4 x = *piece(c);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t y[4];
@@ -168,15 +176,25 @@ __device__ __forceinline__ float q_to_f16(uint8_t* tile, int r) {
   return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 }
 
-template <int D, int kKind>
-__global__ void __launch_bounds__(kThreads<kKind>, 1)
+// kHalves (e2m1): units of one tile, of whose key tiles each softmax group takes half the keys, with a
+// running softmax and an O of its own; the two are joined when the unit is stored. S has two buffers then,
+// as P_t lies over group t's half of S, so the next S does not wait for PV: the chain of a key tile is half a
+// softmax, where one group with the other idle had S, a whole softmax and PV one after another. By itself
+// that was no faster: the loaders decided. With eight of them instead of six (and with registers for them, as a
+// row's half is 64 scores) 128 x 5 tokens of 64/8 heads over up to 8192 keys take 284 us instead of 338, 32 x 5 over
+// up to 4096 59 instead of 69, the first at D = 64 223 instead of 276; six loaders 347, sixteen with half the rows each
+// 282, 60, 230. (As a branch of the kernel for two tiles, the groups taking every second key tile: 364, and all
+// batches 5 to 15% slower.)
+template <int D, int kKind, bool kHalves>
+__global__ void __launch_bounds__(kThreads<kKind, kHalves>, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ16,
                  const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
-  constexpr int kThreads = fcp::kThreads<kKind>;
+  constexpr int kThreads = fcp::kThreads<kKind, kHalves>, kLoaders = fcp::kLoaders<kKind, kHalves>;
   constexpr bool kLoad = kKind != FCP_CACHE_BF16, kE2M1 = kKind == FCP_CACHE_E2M1;
   using C = Cfg<D>;
-  using P = ChunkRows;
+  using P = ChunkRowsOf<kHalves ? 1 : 2>;
+  static_assert(!kHalves || kE2M1, "Q is converted by halves, too");
   extern __shared__ __align__(1024) uint8_t smem[];
   // As static variables, and with a base of the dynamic part that the compiler does not see through:
   // with these two laid over the staging area and a constant base, the same steps took 850 us instead
@@ -251,9 +269,10 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
       mbar_init(bar(B_ODONE + s), 1);
       mbar_init(bar(B_OFREE + s), 4);
       mbar_init(bar(B_TFULL + s), 1);
-      mbar_init(bar(B_TEMPTY + s), 9 + (kLoad ? kLoaders : 0));
+      mbar_init(bar(B_TEMPTY + s), 9 + kLoaders);
       mbar_init(bar(B_QREADY + s), 4);
     }
+    mbar_init(bar(B_PAIR), 8);
     mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0;
     *unquiesced = 0;
@@ -269,8 +288,9 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 8) {
-    if constexpr (kLoad) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp >= 10) {
+    if constexpr (kLoad) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther<kHalves>));
+    if (kHalves && warp >= 10 + kLoaders) {
+    } else if (warp >= 10) {
       // ---------------------------------------------------------- loaders (e4m3)
       // The work is 16-row groups, each in one page: K's eight of a tile, V's eight, the next tile's.
       // They go round the six warps; the two that share their scheduler with no other loader take a
@@ -286,10 +306,13 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
       constexpr int kLanes = D / 16, kStep = 32 / kLanes, kLoads = 16 / kStep;
       const int c = lane % kLanes, r0 = D == 128 ? (lane >> 3) ^ ((lane >> 2) & 1) : lane / kLanes;
       const int page_mask = (1 << a.c.page_shift) - 1;
-      const int order = warp == 12 ? 0 : (warp == 13 ? 1 : (warp < 12 ? warp - 8 : warp - 10));
+      // halves: the warp has the same group of every key tile. (More loaders than a tile has groups, in turn,
+      // may come to a stage two phases early, which a wait by parity does not see.)
+      const int order = kHalves ? warp - 10 : warp == 12 ? 0 : (warp == 13 ? 1 : (warp < 12 ? warp - 8 : warp - 10));
       int turn = 0;
       // from a group of this warp to its next: 32 groups are five rounds of six and two more
       auto step = [&]() -> int {
+        if constexpr (kHalves) return 8;
         const int last = order < 2 ? 5 : 4;
         const int d = turn < last ? 6 : (order < 2 ? 2 : 8);
         turn = turn < last ? turn + 1 : 0;
@@ -529,7 +552,7 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
         const volatile Unit* src = unit_slot + k;  // stays until this unit's consumers have read it
         if (!src->valid) break;
         const SeqShape seq{src->a, src->n, src->len};
-        const int h = src->h, kt0 = src->kt0, kt1 = src->kt1, x0 = 2 * src->u;
+        const int h = src->h, kt0 = src->kt0, kt1 = src->kt1, x0 = P::kTiles * src->u;
         const int* table = a.c.table + static_cast<long long>(src->i) * a.c.max_pages;
         ok = mbar_wait(bar(B_QEMPTY), (v & 1) ^ 1, abort_flag, err, kErrPagedWait + 4);
         ok = __all_sync(0xffffffffu, ok);
@@ -537,19 +560,19 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
         {
           // Q: a tile of 128 tokens of one head is one box, others are boxes of 16 tokens of one
           // head; rows of boxes without a new token are never read for a stored row
-          const ChunkRows::Shape z(seq, a.group);
+          const typename P::Shape z(seq, a.group);
           const int x = x0 + (lane >> 4), box = lane & 7, p = (lane >> 3) & 1;
-          const ChunkRows::Tile tile = z.tile(x, a.group);
+          const typename P::Tile tile = z.tile(x, a.group);
           const bool whole = tile.log_tokens == 7;
           int tok, head;
-          const bool mine = p < C::kPanels && x < z.tiles && !(whole && box > 0) &&
+          const bool mine = p < C::kPanels && (lane >> 4) < P::kTiles && x < z.tiles && !(whole && box > 0) &&
                             tile.row(seq, a.group, box * kQBox, tok, head);
           const int large = __popc(__ballot_sync(0xffffffffu, mine && whole));
           const int small = __popc(__ballot_sync(0xffffffffu, mine && !whole));
           if (lane == 0) mbar_arrive_expect_tx(bar(B_QFULL), (large * kTileM + small * kQBox) * 128);
           __syncwarp();
           if (mine)
-            tma_load_3d(sb + C::kQ + (x & 1) * C::kTileBytes + p * kPanelBytes + box * kQBox * 128, whole ? &tmQ : &tmQ16,
+            tma_load_3d(sb + C::kQ + (lane >> 4) * C::kTileBytes + p * kPanelBytes + box * kQBox * 128, whole ? &tmQ : &tmQ16,
                         bar(B_QFULL), p * 64, seq.a + tok, h * a.group + head);
         }
         last_q = v;
@@ -638,6 +661,57 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
       };
       bool ok = true;
       int J = 0;
+      if constexpr (kHalves) {
+        auto issue_next_s = [&](int j) -> bool {  // key tile j of the block
+          const int s = j & 1;
+          if (!wwait(bar(B_KFULL + s), (j >> 1) & 1, kErrPagedWait + 10)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * kPanelBytes + (kk & 3) * 32;
+            mma_ss_w(tmem + s * 128, sdesc_sw128(sb + C::kQ + o, 16, 1024),
+                     sdesc_sw128(sb + C::kK + s * C::kTileBytes + o, 16, 1024), C::template kIdescS<kKind>, kk > 0);
+          }
+          tc_commit_w(bar(B_SFULL + s));
+          tc_commit_w(bar(B_KEMPTY + s));
+          return true;
+        };
+        for (int v = 0; ok; ++v) {
+          const Unit T = next_unit(v, kErrPagedWait + 6);
+          if (T.valid <= 0) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) ok = ok && wwait(bar(B_QREADY + t), v & 1, kErrPagedWait + 7);
+          ok = ok && issue_next_s(J);
+          for (int jl = 0, n = T.kt1 - T.kt0; ok && jl < n; ++jl, ++J) {
+            const int s = J & 1;
+            // S of the next key tile goes over P of the one before, whose PV has been issued
+            if (jl + 1 < n) ok = issue_next_s(J + 1);
+            else tc_commit_w(bar(B_QEMPTY));  // every S of this unit has been issued: Q is free once they complete
+            ok = ok && wwait(bar(B_VFULL + s), (J >> 1) & 1, kErrPagedWait + 8);
+            // the unit's first PV overwrites O_t, of which both groups' epilogues have read halves
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              ok = ok && (jl > 0 || v == 0 || wwait(bar(B_OFREE + t), (v - 1) & 1, kErrPagedWait + 9));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              ok = ok && wwait(bar(B_PFULL + 2 * t + s), (J >> 1) & 1, kErrPagedWait + 5);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts_w(tmem + 256 + t * 128, tmem + s * 128 + t * 64 + k * 8,
+                         sdesc_sw128(sb + C::kV + s * C::kTileBytes + (4 * t + k) * 2048, kPanelBytes, 1024),
+                         C::template kIdescPV<kKind>, jl > 0 || k > 0);
+            }
+            if (!ok) break;
+            tc_commit_w(bar(B_VEMPTY + s));
+            // of every key tile, and of the unit: behind its last S two PVs may be on their way, too many
+            // for a wait by parity
+            tc_commit_w(bar(B_ODONE));
+            if (jl + 1 == n) tc_commit_w(bar(B_ODONE + 1));
+          }
+        }
+      } else
       for (int v = 0; ok; ++v) {
         const Unit T = next_unit(v, kErrPagedWait + 6);
         if (T.valid <= 0) break;
@@ -715,7 +789,7 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax (warps 0-7)
-    if constexpr (kLoad) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    if constexpr (kLoad) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax<kHalves>));
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -723,19 +797,27 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
     const uint32_t o_addr = lane_base + 256 + t * 128;
     bool ok = true;
     int J = 0;  // key tiles of this group
+    int met = 0;
+    [[maybe_unused]] auto meet = [&]() -> bool {  // both groups, all warps
+      mbar_arrive_warp(bar(B_PAIR));
+      const bool here = mbar_wait(bar(B_PAIR), met & 1, abort_flag, err, kErrPagedWait + 15);
+      ++met;
+      return __all_sync(0xffffffffu, here);
+    };
     for (int v = 0; ok; ++v) {
       const Unit T = next_unit(v, kErrPagedWait + 12);
       if (T.valid <= 0) break;
       const SeqShape seq{T.a, T.n, T.len};
-      const ChunkRows::Shape z(seq, a.group);
-      const int x = 2 * T.u + t;
+      const typename P::Shape z(seq, a.group);
+      const int at = kHalves ? 0 : t;  // tile of the unit
+      const int x = P::kTiles * T.u + at;
       if constexpr (kE2M1) {  // also for a unit of one tile, so that no phase is missed
         ok = mbar_wait(bar(B_QFULL), v & 1, abort_flag, err, kErrPagedWait + 7);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
       if (x >= z.tiles) continue;  // a unit of one tile
-      const ChunkRows::Tile tile = z.tile(x, a.group);
+      const typename P::Tile tile = z.tile(x, a.group);
       int tok, head;
       const bool mine = tile.row(seq, a.group, r, tok, head);
       const bool idle = !__any_sync(0xffffffffu, mine);  // a warp without a row keeps the barriers only
@@ -744,7 +826,14 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
       float scale = a.scale_log2;
       if constexpr (kE2M1) {
         // never zero, which would make NaN of a masked score (what this does to others is below 2^-80)
-        if (!idle) scale = fmaxf(scale * q_to_f16<D>(smem + C::kQ + t * C::kTileBytes, r), 0x1p-120f);
+        uint8_t* q = smem + C::kQ + at * C::kTileBytes;
+        if constexpr (kHalves) {  // half a row each, once both groups have looked at all of it
+          if (idle) ok = meet();
+          else scale = fmaxf(scale * q_to_f16<D>(q, r, t * (D / 16), (t + 1) * (D / 16), [&]() { ok = meet(); }), 0x1p-120f);
+          if (!ok) break;
+        } else if (!idle) {
+          scale = fmaxf(scale * q_to_f16<D>(q, r, 0, D / 8, []() {}), 0x1p-120f);
+        }
         fence_proxy_async_smem();
         mbar_arrive_warp(bar(B_QREADY + t));
       }
@@ -753,6 +842,74 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
       float l = 0.f;
       int jl = 0;
       for (int kt = T.kt0; kt < T.kt1; ++kt, ++J, ++jl) {
+        if constexpr (kHalves) {
+          const int buf = J & 1;
+          ok = mbar_wait(bar(B_SFULL + buf), (J >> 1) & 1, abort_flag, err, kErrPagedWait + 13);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (idle) {
+            mbar_arrive_warp(bar(B_PFULL + 2 * t + buf));
+            continue;
+          }
+          const uint32_t half = lane_base + buf * 128 + t * 64;
+          const int lim = lim_row - kt * kTileN - 64 * t;  // visible columns of this half
+          tc_fence_after();
+          uint32_t sv[2][32];
+          tmem_ld32x2(half, half + 32, sv[0], sv[1]);
+          if (!__all_sync(0xffffffffu, lim >= 64)) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (e >= lim) sv[e >> 5][e & 31] = 0xff800000u;
+          }
+          float mc[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            mc[c] = fmaxf(__uint_as_float(sv[c][0]), __uint_as_float(sv[c][31]));
+#pragma unroll
+            for (int e = 0; e < 15; ++e)
+              mc[c] = max3f(mc[c], __uint_as_float(sv[c][1 + 2 * e]), __uint_as_float(sv[c][2 + 2 * e]));
+          }
+          const float m_new = fmaxf(m_used, fmaf(fmaxf(mc[0], mc[1]), scale, -kUp));
+          float alpha = 1.f;
+          const bool grow = m_new > m_used + kRescaleThreshold;
+          if (grow) {
+            alpha = fast_exp2(m_used - m_new);
+            m_used = m_new;
+          }
+          const float mb = m_used == -INFINITY ? 0.f : m_used;
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = ffma2(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1]), scale, scale, -mb, -mb);
+              const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+              sum = fadd2(sum.x, sum.y, p0, p1);
+              pk[e] = pack_f16(p0, p1);
+            }
+            tmem_st16(half + c * 16, pk);
+          }
+          if (__any_sync(0xffffffffu, grow && jl > 0)) {  // as below
+            ok = mbar_wait(bar(B_ODONE), (J - 1) & 1, abort_flag, err, kErrPagedWait + 14);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld32(o_addr + c * 32, ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st32(o_addr + c * 32, ov);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive_warp(bar(B_PFULL + 2 * t + buf));
+          l = l * alpha + (sum.x + sum.y);
+          continue;
+        }
         ok = mbar_wait(bar(B_SFULL + t), J & 1, abort_flag, err, kErrPagedWait + 13);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -839,10 +996,30 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
       if (!ok) break;
       // epilogue: O_t is read out of TMEM (then released to the next unit's first PV) and stored:
       // normalised as bf16 when this block has the whole group, else as float32 sums for the merge
-      ok = mbar_wait(bar(B_ODONE + t), (J - 1) & 1, abort_flag, err, kErrPagedWait + 15);
+      ok = kHalves ? mbar_wait(bar(B_ODONE + 1), v & 1, abort_flag, err, kErrPagedWait + 15)
+                   : mbar_wait(bar(B_ODONE + t), (J - 1) & 1, abort_flag, err, kErrPagedWait + 15);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      uint8_t* stg = smem + C::kStage + warp * 4096;
+      float own = 1.f, others = 0.f;  // factors of the two groups' sums
+      if constexpr (kHalves) {
+        // The groups' maxima and sums, each through the other warp's block, which that warp has been done with
+        // since the two met over Q and writes to only after this. Both then have the rows' whole softmax, and
+        // store half of the channels each.
+        *reinterpret_cast<float2*>(smem + C::kStage + (warp ^ 4) * 4096 + 8 * lane) = make_float2(m_used, l);
+        tc_fence_before();
+        if (!(ok = meet())) break;
+        tc_fence_after();
+        const float2 y = *reinterpret_cast<const float2*>(stg + 8 * lane);
+        const float m = fmaxf(m_used, y.x);
+        if (m != -INFINITY) {
+          own = fast_exp2(m_used - m);
+          others = fast_exp2(y.x - m);
+        }
+        m_used = m;
+        l = l * own + y.y * others;
+      }
       if (idle) {
         tc_fence_before();
         mbar_arrive_warp(bar(B_OFREE + t));
@@ -857,13 +1034,26 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
       // by row), 64 bf16 or 32 float32 channels at a time, so that stores write whole row segments:
       // lane l writes slot l % 8 of rows l / 8 + 4 i
       auto unit = [&](uint32_t y) -> uint32_t { return __float_as_uint(__uint_as_float(y) * a.c.v_unit); };
-      uint8_t* stg = smem + C::kStage + warp * 4096;
       const int wrow = (warp & 3) * 32, sub = lane >> 3, e8 = lane & 7;
+      // 64 channels at a time, so that group 0 stores all of D = 64
+      const int first_c = kHalves ? 2 * t : 0, last_c = kHalves ? min(2 * t + 2, D / 32) : D / 32;
+      if (kHalves && first_c == last_c) {
+        tc_fence_before();
+        mbar_arrive_warp(bar(B_OFREE + t));
+      }
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = first_c; c < last_c; ++c) {
         uint32_t ov[32];
-        tmem_ld32(o_addr + c * 32, ov);
-        if (c == D / 32 - 1) {
+        if constexpr (kHalves) {
+          uint32_t ow[32];
+          tmem_ld32x2(o_addr + c * 32, lane_base + 256 + (t ^ 1) * 128 + c * 32, ov, ow);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), own, __uint_as_float(ow[e]) * others));
+        } else {
+          tmem_ld32(o_addr + c * 32, ov);
+        }
+        if (c == last_c - 1) {
           tc_fence_before();
           mbar_arrive_warp(bar(B_OFREE + t));
         }
@@ -900,15 +1090,15 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
           if (!tile.row(seq, a.group, rt, tk, hd)) continue;
           const uint4 y = *reinterpret_cast<const uint4*>(stg + rr * 128 + ((e8 ^ (rr & 7)) << 4));
           if (wide)
-            reinterpret_cast<uint4*>(a.part_o + (static_cast<long long>(T.slot) * P::kRows + t * kTileM + rt) * D)[c * 8 + e8] = y;
+            reinterpret_cast<uint4*>(a.part_o + (static_cast<long long>(T.slot) * P::kRows + at * kTileM + rt) * D)[c * 8 + e8] = y;
           else
             reinterpret_cast<uint4*>(a.o + (static_cast<long long>(T.h * a.group + hd) * a.c.total_new + T.a + tk) * D)[(c >> 1) * 8 + e8] = y;
         }
       }
       __syncwarp();  // the block is free for the next unit's epilogue
-      if (mine) {
+      if (mine && !(kHalves && t == 1)) {
         if (T.slot >= 0)
-          a.part_ml[static_cast<long long>(T.slot) * P::kRows + t * kTileM + r] = make_float2(m_used, l);
+          a.part_ml[static_cast<long long>(T.slot) * P::kRows + at * kTileM + r] = make_float2(m_used, l);
         else
           a.lse[static_cast<long long>(T.h * a.group + head) * a.c.total_new + T.a + tok] =
               l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
@@ -929,9 +1119,10 @@ __global__ void __launch_bounds__(kThreads<kKind>, 1)
   }
 }
 
-template <int D, int kKind>
+template <int D, int kKind, bool kHalves = false>
 fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaStream_t s) {
   using C = Cfg<D>;
+  using P = ChunkRowsOf<kHalves ? 1 : 2>;
   CUtensorMap mq, mq16, mk = {}, mv = {};
   if (const fcp_status st = make_bf16_map(&mq, a.q, hq, a.c.total_new, D, kTileM); st != FCP_OK) return st;
   if (const fcp_status st = make_bf16_map(&mq16, a.q, hq, a.c.total_new, D, kQBox); st != FCP_OK) return st;
@@ -948,26 +1139,31 @@ fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaSt
   // on the line mostly read the same keys, and do so from one pair of SMs (4 sequences of 512 new
   // tokens over up to 16384 keys: 195 to 190 us; other shapes, and an e4m3 cache, within a percent or two either way).
   const int blocks = std::max(2, std::min(n_sm, kMaxChunkBlocks) & ~1);
-  set_workspace<ChunkRows>(a, workspace, D, kMaxChunkBlocks);
+  set_workspace<P>(a, workspace, D, kMaxChunkBlocks);
   static std::atomic<uint64_t> allowed{0};
-  if (const fcp_status st = allow_smem(chunk_kernel<D, kKind>, C::kSmemBytes, dev, allowed, "paged chunk smem attribute");
+  if (const fcp_status st = allow_smem(chunk_kernel<D, kKind, kHalves>, C::kSmemBytes, dev, allowed, "paged chunk smem attribute");
       st != FCP_OK)
     return st;
-  if (const fcp_status st = launch_overlapped<kKind == FCP_CACHE_BF16 ? 2 : 1>(chunk_kernel<D, kKind>, dim3(blocks), kThreads<kKind>, C::kSmemBytes, s,
+  if (const fcp_status st = launch_overlapped<kKind == FCP_CACHE_BF16 ? 2 : 1>(chunk_kernel<D, kKind, kHalves>, dim3(blocks), kThreads<kKind, kHalves>, C::kSmemBytes, s,
                                               "paged chunk launch", mq, mq16, mk, mv, a);
       st != FCP_OK)
     return st;
-  return launch_merge<ChunkRows, D>(a, blocks, 32, s);
+  return launch_merge<P, D>(a, blocks, 32, s);
 }
 
 }  // namespace
 
-fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int dev, int n_sm,
-                              cudaStream_t s) {
+fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, int max_new, void* workspace, int dev,
+                              int n_sm, cudaStream_t s) {
   const auto run = [&](auto kind) {
     constexpr int kKind = decltype(kind)::value;
     return d == 128 ? launch<128, kKind>(a, workspace, dev, n_sm, hq, s) : launch<64, kKind>(a, workspace, dev, n_sm, hq, s);
   };
+  // Batches whose sequences have one tile of rows (one that is longer than max_new says is several units then).
+  const int tokens = max_new > 64 ? 128 : (max_new > 32 ? 64 : (max_new > 16 ? 32 : 16));
+  if (dtype == FCP_CACHE_E2M1 && max_new <= 128 && a.group <= kTileM / tokens)
+    return d == 128 ? launch<128, FCP_CACHE_E2M1, true>(a, workspace, dev, n_sm, hq, s)
+                    : launch<64, FCP_CACHE_E2M1, true>(a, workspace, dev, n_sm, hq, s);
   if (dtype == FCP_CACHE_E2M1) return run(std::integral_constant<int, FCP_CACHE_E2M1>());
   if (dtype == FCP_CACHE_E4M3) return run(std::integral_constant<int, FCP_CACHE_E4M3>());
   return run(std::integral_constant<int, FCP_CACHE_BF16>());

@@ -624,7 +624,7 @@ fcp_status launch_attn(const AttnArgs& a, int dtype, int hq, int max_new, void* 
   // core's tiles of 128. (With 64 rows as the border, in two units: 48 rows took 19.0 us instead of
   // 20.8 from an e4m3 cache and 16.6 instead of 19.6 from a bf16 one, 60 rows 21.4 instead of 18.5,
   // 64 rows of long sequences 37.4 instead of 36.7, 128 rows far more.)
-  if (rows > 32) return launch_paged_chunk(a, dtype, D, hq, workspace, dev, n_sm, s);
+  if (rows > 32) return launch_paged_chunk(a, dtype, D, hq, max_new, workspace, dev, n_sm, s);
   if (dtype == FCP_CACHE_E2M1) return launch_paged_few4(a, D, static_cast<int>(rows), workspace, dev, n_sm, max_new, s);
   const bool e = dtype == FCP_CACHE_E4M3;
   auto* launch = rows <= 8    ? (e ? launch_few<D, true, 1> : launch_few<D, false, 1>)

@@ -93,9 +93,12 @@ struct FewRows {
 // Chunks: a tile is 128 rows of a KV head, 2^log_tokens new tokens of each of 128 / 2^log_tokens query
 // heads, head by head. Whole 128s of tokens make tiles of one head each, the tokens that are left
 // tiles of 128, 64, 32 or 16 tokens, so that short chunks and remainders fill tiles with heads
-// instead of padding. Tiles are ordered tokens first, heads within them, and a unit is two.
-struct ChunkRows {
-  static constexpr int kRows = 2 * kTileM;
+// instead of padding. Tiles are ordered tokens first, heads within them, and a unit is two (kTiles), or
+// one for batches whose sequences have no more rows than that.
+template <int kTilesPerUnit>
+struct ChunkRowsOf {
+  static constexpr int kTiles = kTilesPerUnit;
+  static constexpr int kRows = kTiles * kTileM;
   static constexpr int kLeastShare = 1;  // 4, 6 and 8 were slower on every small batch tried
   static constexpr int kWarpPieces = 32;
   static constexpr int kOverhead = 3;
@@ -124,20 +127,20 @@ struct ChunkRows {
     }
     // Units whose last tile comes before token tile tt (n128: the rest).
     __device__ __forceinline__ int first_unit(int tt, int group) const {
-      return tt > n128 ? (tiles + 1) >> 1 : (tt * group) >> 1;
+      return tt > n128 ? (tiles + kTiles - 1) / kTiles : tt * group / kTiles;
     }
   };
   // Length on the line of a unit whose last tile is of token tile tt.
   static __device__ __forceinline__ int length(const SeqShape& s, int tt, int causal) {
     return kOverhead + granules_of(key_end(s, (tt << 7) + 127, causal));
   }
-  static __device__ __forceinline__ int units(const SeqShape& s, int group) { return (Shape(s, group).tiles + 1) >> 1; }
+  static __device__ __forceinline__ int units(const SeqShape& s, int group) { return (Shape(s, group).tiles + kTiles - 1) / kTiles; }
   static __device__ __forceinline__ int tiles_of(const SeqShape& s, int group, int u) {
-    return min(2, Shape(s, group).tiles - 2 * u);
+    return min(kTiles, Shape(s, group).tiles - kTiles * u);
   }
   static __device__ __forceinline__ int end(const SeqShape& s, int group, int u, int causal) {
     const Shape z(s, group);
-    const int x = min(2 * u + 1, z.tiles - 1);
+    const int x = min(kTiles * u + kTiles - 1, z.tiles - 1);
     return key_end(s, ((x < z.full ? x / group : z.n128) << 7) + 127, causal);
   }
   static __device__ __forceinline__ long long head_length(const SeqShape& s, int group, int causal) {
@@ -166,10 +169,11 @@ struct ChunkRows {
   }
   static __device__ __forceinline__ bool row(const SeqShape& s, int group, int u, int r, int& tok, int& head) {
     const Shape z(s, group);
-    const int x = 2 * u + (r >> 7);
+    const int x = kTiles * u + (r >> 7);
     return x < z.tiles && z.tile(x, group).row(s, group, r & (kTileM - 1), tok, head);
   }
 };
+using ChunkRows = ChunkRowsOf<2>;
 
 // What each warp's sequences add to the line, and how many those are.
 template <int kThreads>
@@ -501,7 +505,7 @@ inline fcp_status launch_merge(const AttnArgs& a, int blocks, int slices, cudaSt
 
 fcp_status launch_paged_few4(const AttnArgs& a, int d, int rows, void* workspace, int dev, int n_sm, int max_new,
                              cudaStream_t s);
-fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, void* workspace, int dev, int n_sm,
-                              cudaStream_t s);
+fcp_status launch_paged_chunk(const AttnArgs& a, int dtype, int d, int hq, int max_new, void* workspace, int dev,
+                              int n_sm, cudaStream_t s);
 
 }  // namespace fcp

@@ -191,6 +191,58 @@ def test_attention(fcp, b):
     U.check_attention(b, t, o, lse, *before)
 
 
+# Sequences of one tile of rows at most, of whose key tiles two groups of warps take half the keys each: one key tile,
+# two, an odd number, many over several blocks; beside them batches with longer sequences, and one that says it has none.
+ONE_TILE = [
+    Batch([5], [129], hq=8, hkv=1, d=128),
+    Batch([5], [257], hq=8, hkv=1),
+    Batch([16, 5, 12, 9, 7], [300, 128, 40, 1000, 513], hq=8, hkv=1, d=128, pad=1),
+    Batch([40, 6, 17, 5, 100], [400, 800, 17, 300, 100], hq=8, hkv=2, d=128, page=32),
+    Batch([40, 6, 17, 5, 100], [400, 800, 17, 300, 100], hq=8, hkv=2),
+    Batch([6], [20000], hq=8, hkv=1, d=128, page=256, std=3.0),
+    Batch([1, 1, 1], [700, 2000, 129], hq=48, hkv=1, d=128, page=64),
+    Batch([1, 1], [640, 130], hq=100, hkv=2, page=64, causal=False),
+    Batch([5] * 60, [100 + (i * 97) % 900 for i in range(60)], hq=32, hkv=4, d=128),
+    Batch([5, 37] * 20, [37 + (i * 97) % 900 for i in range(40)], hq=16, hkv=2),
+    Batch([150, 5], [140, 300], hq=8, hkv=1, d=128),                     # rows before position 0 see nothing
+    Batch([70], [300], hq=1, hkv=1, d=128, causal=False),
+    Batch([128, 100, 0, 33], [128, 500, 40, 300], hq=3, hkv=3, d=128),
+    Batch([30, 17], [30, 1000], hq=8, hkv=2, pad=1, std=3.0),
+    Batch([5, 12], [64, 65], hq=8, hkv=1, d=128, page=64),
+    Batch([200, 5, 17], [900, 300, 100], hq=8, hkv=1, d=128, max_new=5),  # a wrong max_new is only slow
+]
+ONE_TILE = [b.__class__(**{**b.__dict__, "seed": 50 + i}) for i, b in enumerate(ONE_TILE)]
+
+
+@pytest.mark.parametrize("b", ONE_TILE, ids=str)
+def test_attention_of_one_tile(fcp, b):
+    t = U.make(b)
+    o, lse, before = attend(fcp, b, t, *U.handles(fcp, b, t))
+    U.check_attention(b, t, o, lse, *before)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_scale_in_either_half_of_a_key_tile(fcp, d):
+    """As below, with the scale among the keys of either group of warps."""
+    new, n, hq = 9, 400, 8
+    for x in "kv":
+        for pos in (19, 100, 150, 300, n - 5, n - 1):
+            b = Batch([new, new], [n, n], hq=hq, hkv=1, d=d, page=16)
+            t = U.make(b)
+            page, group = int(t["table"][0, pos // 16]), (pos * 7) % (d // 16)
+            t[x + "_scales"].view(torch.uint8)[page, 0, pos % 16, group] = 0x7F
+            o, lse, _ = attend(fcp, b, t, *U.handles(fcp, b, t))
+            sees = (torch.arange(new) + n - new >= pos)[None].expand(hq, -1)
+            assert o[:, :new].isnan().cpu().any(-1).equal(sees), (x, pos)
+            if x == "k":
+                assert lse[:, :new].isnan().cpu().equal(sees)
+            t[x + "_scales"].view(torch.uint8)[page, 0, pos % 16, group] = 0x20
+            want, _, _ = attend(fcp, b, t, *U.handles(fcp, b, t))
+            assert torch.equal(o[:, new:], want[:, new:])
+            clear = ~sees.cuda()
+            assert torch.equal(o[:, :new][clear], want[:, :new][clear])
+
+
 @pytest.mark.parametrize("new", [1, 4, 8, 60], ids=["few8", "few16", "few32", "chunk"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_with_scales_across_the_range(fcp, new, d):
