@@ -31,7 +31,8 @@
 // loaders' groups of 16 rows (199 us, but the first 1535), or of 64 (255 and 1945);
 // both by a unit's length in one code (1487); two groups of 16 in registers (1772: the fence that hands a
 // group over waits for loads in flight); groups by cp.async (1527) or by bulk copies of the walk's warp
-// (2908, one slot for each loader being all that fits) into shared memory first; prefetches to L2 (1490).
+// (2908, one slot for each loader being all that fits) into shared memory first; prefetches to L2 (1490);
+// eight loaders, whose registers the softmax warps lack then (1701, the 16 chunks 238).
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, or of the first and second 64 keys of the only one (thread = row =
 // TMEM lane); 8: the walk along the
