@@ -56,7 +56,8 @@ def frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] 
     elif kind == "yarn":
         factor, original, fast, slow, magnitude = need("factor", "original", fast=32.0, slow=1.0, magnitude=None)
         low, high = (rotary_dim * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow))
-        low, high = max(math.floor(low), 0), min(math.ceil(high), half - 1)
+        # the upper end may lie past the last pair, which then keeps a part of its frequency
+        low, high = max(math.floor(low), 0), min(math.ceil(high), rotary_dim - 1)
         ramp = np.clip((i - low) / max(high - low, 0.001), 0.0, 1.0)
         f = f * (1 - ramp) + f / factor * ramp
         if magnitude is None:
