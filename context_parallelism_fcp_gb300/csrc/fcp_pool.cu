@@ -29,7 +29,7 @@ struct PoolArgs {
   int32_t* n_free;
   int32_t* lens;
   int32_t* table;
-  int32_t* status;  // [0] the error, [1] blocks that are done
+  int32_t* status;  // [0] the error, [1] blocks that are done, and 2^16 times those that report something
   int32_t n_pages, page_shift, n_seqs, max_pages;
 };
 
@@ -79,18 +79,23 @@ __device__ __forceinline__ int max_scan(int x, int* warps) {
   return max(x, before);
 }
 
-// Whether this block is the last to come here (its threads then see the others as done). The counter
-// is left at zero.
-__device__ __forceinline__ bool last_block(const PoolArgs& p) {
-  __shared__ int last;
+// Whether this block is the last to come here (its threads then see the others as done), and whether any block
+// came with `found`, the same for all of its threads (they then see what the others wrote). The counter is left
+// at zero.
+__device__ __forceinline__ bool last_block(const PoolArgs& p, bool& found) {
+  __shared__ int last, any;
   if (gridDim.x == 1) return true;
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    last = atomicAdd(p.status + 1, 1) == static_cast<int>(gridDim.x) - 1;
+    const int before = atomicAdd(p.status + 1, found ? 0x10001 : 1);
+    last = (before & 0xffff) == static_cast<int>(gridDim.x) - 1;
+    any = found || (before >> 16) != 0;
     if (last) p.status[1] = 0;
+    if (any) __threadfence();
   }
   __syncthreads();
+  found = any != 0;
   return last != 0;
 }
 
@@ -241,7 +246,8 @@ __global__ void __launch_bounds__(kThreads) admit_kernel(const PoolArgs p, const
     }
     __syncthreads();
   }
-  if (!last_block(p)) return;
+  bool found = false;
+  if (!last_block(p, found)) return;
   each([&](int i, int len, int x, int, long long row0, long long) {
     cu[i] = static_cast<int>(min(row0, rows));
     granted[i] = x;
@@ -282,6 +288,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PoolArgs p, con
   // a stack that is too high afterwards has pages twice: nothing is given back
   const bool fits = n_free >= 0 && n_free + total <= p.n_pages;
   if (!fits && first_block && tid == 0) report(p, kErrCacheBatch);
+  bool lost = false;  // an id that is no page's was among those given back
   for (long long b0 = static_cast<long long>(blockIdx.x) * kThreads; fits && b0 < total;
        b0 += static_cast<long long>(gridDim.x) * kThreads) {
     m.seq[tid] = -1;
@@ -303,18 +310,36 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PoolArgs p, con
     if (b0 + tid < total) {
       int32_t* entry = p.table + static_cast<long long>(m.seq[y]) * p.max_pages + m.a[y] + (tid - m.first[y]);
       const int page = load(entry);
-      if (page < 0 || page >= p.n_pages) report(p, kErrCachePage);
+      if (page < 0 || page >= p.n_pages) {
+        report(p, kErrCachePage);
+        lost = true;
+      }
       p.free_pages[n_free + b0 + tid] = page;
       *entry = -1;
     }
-    __syncthreads();
+    lost = __syncthreads_or(lost) != 0;
   }
-  if (!last_block(p) || !fits) return;
+  if (!last_block(p, lost) || !fits) return;
   mine.each(p, [&](int i, int len, int x) {
     int first, left;
     given(len, x, first, left);
     if (left != len) p.lens[i] = left;
   });
+  if (lost) {
+    // It is left out of the stack: the others of this call move together, in order, 1 K at a time, which are
+    // read before any of them is written over. (Past L1, which knows nothing of other blocks' writes.)
+    int32_t* given_back = p.free_pages + n_free;
+    long long kept = 0;
+    for (long long b0 = 0; b0 < total; b0 += kThreads) {
+      const int page = b0 + tid < total ? __ldcg(given_back + b0 + tid) : -1;
+      const bool good = page >= 0 && page < p.n_pages;
+      long long n;
+      const long long at = kept + scan(good ? 1 : 0, m.warps, n);
+      if (good) given_back[at] = page;
+      kept += n;
+    }
+    total = kept;
+  }
   if (tid == 0 && total > 0) *p.n_free = n_free + static_cast<int>(total);
 }
 

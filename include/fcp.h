@@ -501,7 +501,10 @@ fcp_status fcp_rotary_write(const fcp_cache* cache, const fcp_cache_batch* batch
  * clear it with fcp_device_error), the others the calls' own. 0x50: a length that does not fit its row,
  * a negative number of new tokens, a stack height outside [0, n_pages], or a release that would pass
  * n_pages (that sequence, or the call's whole release, is left out); 0x51: a page id outside
- * [0, n_pages) in what was released or taken. */
+ * [0, n_pages) in what was released or taken. Such an id does not go on the stack (its entry of the block
+ * table becomes -1 like the others, and the page that should have been there is lost to the pool until
+ * the caller puts it back); one that the caller's stack holds is handed out as it is, and its sequence's
+ * rows in that page have slot -1 and no place in the cache. */
 typedef struct {
   int32_t* free_pages;  /* [n_pages] */
   int32_t* n_free;      /* [1] */
