@@ -2,9 +2,10 @@
 
 ``PagedCache`` holds one layer's pages, ``CacheBatch`` says which rows of a packed batch belong
 to which cached sequence, and ``cache_write``, ``cache_read`` and ``paged_attn`` are the C calls
-of the same names. ``PagePool`` gives pages to sequences and takes them back, on the GPU. As in the rest of the package the arguments are checked and marshalled here
-and all the work is done by the library's kernels, on the caller's stream. That may be any stream: what a
-cache or an attention allocates stays theirs until the work of every stream that they were used on is done.
+of the same names. ``PagePool`` gives pages to sequences and takes them back, on the GPU. As in the
+rest of the package the arguments are checked and marshalled here and all the work is done by the
+library's kernels, on the caller's stream. That may be any stream: what a cache or an attention allocates
+stays theirs until the work of every stream that they were used on is done.
 (Tensors of the caller's follow torch's rule: one that is used on another stream than its own and then dropped
 is the caller's to record there. A batch of a PagePool's keeps the pool. A graph's tensors and objects have
 to outlive it.)
@@ -23,8 +24,10 @@ from . import _CacheBatchStruct, _CacheStruct, _PagePoolStruct, _check, _need, _
 
 __all__ = ["PagedCache", "CacheBatch", "cache_write", "cache_read", "paged_attn", "PagedAttention", "PagePool"]
 
-_E2M1 = torch.float4_e2m1fn_x2  # two codes to an element
-_DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, _E2M1: 2}
+_DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+_E2M1 = getattr(torch, "float4_e2m1fn_x2", None)  # two codes to an element; a torch without it has the other caches
+if _E2M1 is not None:
+    _DTYPES[_E2M1] = 2
 
 
 def _here(index: int, stream, what: str = "cache") -> int:
