@@ -826,14 +826,16 @@ __global__ void __launch_bounds__(kThreads<kKind, kHalves>, 1)
       const int lim_row = !mine ? INT32_MAX : (a.causal ? max(0, T.len - T.n + tok + 1) : T.len);
       float scale = a.scale_log2;
       if constexpr (kE2M1) {
-        // never zero, which would make NaN of a masked score (what this does to others is below 2^-80)
+        // Neither zero, which would make NaN of a masked score (what this does to others is below 2^-80), nor
+        // infinite, which would of a score of zero (others may be wrong then: they are past what the header allows).
+        auto factor = [&](float f) { return fminf(fmaxf(scale * f, 0x1p-120f), 0x1p127f); };
         uint8_t* q = smem + C::kQ + at * C::kTileBytes;
         if constexpr (kHalves) {  // half a row each, once both groups have looked at all of it
           if (idle) ok = meet();
-          else scale = fmaxf(scale * q_to_f16<D>(q, r, t * (D / 16), (t + 1) * (D / 16), [&]() { ok = meet(); }), 0x1p-120f);
+          else scale = factor(q_to_f16<D>(q, r, t * (D / 16), (t + 1) * (D / 16), [&]() { ok = meet(); }));
           if (!ok) break;
         } else if (!idle) {
-          scale = fmaxf(scale * q_to_f16<D>(q, r, 0, D / 8, []() {}), 0x1p-120f);
+          scale = factor(q_to_f16<D>(q, r, 0, D / 8, []() {}));
         }
         fence_proxy_async_smem();
         mbar_arrive_warp(bar(B_QREADY + t));

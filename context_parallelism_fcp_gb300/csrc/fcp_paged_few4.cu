@@ -333,8 +333,9 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm<NT>) few4_kernel(const Att
 #pragma unroll
         for (int y = 0; y < 2; ++y)
           q[t][c][y] = pack_f16(__uint_as_float(q[t][c][y] << 16) * f, __uint_as_float(q[t][c][y] & 0xffff0000u) * f);
-      // never zero, which would make NaN of a masked score (what this does to others is below 2^-80)
-      back[t] = fmaxf(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 0x1p-120f);
+      // Neither zero, which would make NaN of a masked score (what this does to others is below 2^-80), nor
+      // infinite, which would of a score of zero (others may be wrong then: they are past what the header allows).
+      back[t] = fminf(fmaxf(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 0x1p-120f), 0x1p127f);
     }
     if constexpr (kSharedQ) {
 #pragma unroll

@@ -452,6 +452,9 @@ size_t fcp_paged_attn_workspace_bytes(int32_t head_dim);
  * NaN scale of a 4-bit cache's V reaches the rows that see it and no others, in its 16 channels or in
  * all of o; one of K makes the rows that see it NaN. A 4-bit cache's q is taken as f16 times a power of two
  * for each row: what is below 2^-28 of a row's largest element may be lost.
+ * Scores (times log2 e) are float32 in every cache: one past 2^127 may make its row NaN. A 4-bit cache with
+ * max|q| * k_unit up to 2^111 for a row cannot get there; rows past that may have scores that are wrong or NaN, but
+ * for scores of zero, which are zero.
  * Results do not depend on timing: no atomics are used. o and lse must not overlap the inputs.
  * workspace: fcp_paged_attn_workspace_bytes, 256-byte aligned, its contents need not be
  * kept or cleared; calls whose work may overlap need one each. Errors: FCP_ERR_INVALID (also
