@@ -556,7 +556,9 @@ class FcpAttention:
         """Plan a new batch (by default the same lengths again) with the same block size,
         mask, workers, cap and coalescing, as a training loop does for every batch: partition,
         distribute and coalesce run on the host, and the new device image is uploaded in
-        ``stream`` order, so kernels enqueued earlier on that stream still see the old plan.
+        ``stream`` order, so kernels enqueued earlier on that stream still see the old plan
+        (and with ``rotary`` the old positions). An image of over 64 KB (some 3000 tokens) is copied
+        from ordinary host memory, for which CUDA waits until the stream comes to it.
         The batch must fit the buffers allocated at construction (same total tokens, no more
         partial rows or device-image bytes)."""
         if getattr(self, "_recipe", None) is None:
@@ -571,12 +573,7 @@ class FcpAttention:
         plan.upload(self.d_plan, stream)
         self.plan = plan
         if self.rotary is not None:
-            import torch
-
-            if stream is not None and not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(_stream(stream), device=self.device)
-            with torch.cuda.stream(stream):
-                self.positions.copy_(self._packed_positions())
+            self._place(stream)
 
     @classmethod
     def from_plan(cls, plan: "Plan", hq: int, hkv: int, head_dim: int, device="cuda",
@@ -587,11 +584,18 @@ class FcpAttention:
         self._setup(plan, hq, hkv, head_dim, device, backward, rotary)
         return self
 
-    def _packed_positions(self):
+    def _place(self, stream=None) -> None:
+        """Every packed row's position in its sequence, in ``stream`` order and without a wait: from pinned
+        memory, which torch does not hand out again until the copy is done."""
         import torch
 
-        return torch.from_numpy(np.concatenate([np.arange(int(n), dtype=np.int32) for n in self.plan.seqlens] or
-                                               [np.zeros(0, np.int32)]))
+        rows = torch.empty(self.T, dtype=torch.int32, pin_memory=True)
+        if self.T:
+            np.concatenate([np.arange(int(n), dtype=np.int32) for n in self.plan.seqlens], out=rows.numpy())
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            self.positions.copy_(rows, non_blocking=True)
 
     def _setup(self, plan, hq, hkv, head_dim, device, backward, rotary=None):
         import torch
@@ -620,7 +624,8 @@ class FcpAttention:
         if rotary is not None:
             if rotary.rotary_dim > head_dim:
                 raise ValueError(f"rotary_dim {rotary.rotary_dim} is larger than head_dim {head_dim}")
-            self.positions = self._packed_positions().to(self.device)
+            self.positions = torch.empty(self.T, dtype=torch.int32, device=self.device)
+            self._place()
             self._turned = [torch.empty((h, self.T, head_dim), dtype=torch.bfloat16, device=self.device)
                             for h in (hq, hkv)]
 
