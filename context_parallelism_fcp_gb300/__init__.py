@@ -532,7 +532,9 @@ class FcpAttention:
     backward's query bands (Plan.set_bwd_band; None keeps the plan's own choice); the
     workspace holds their dK/dV sums, so a plan with bands runs its backward banded. With
     ``rotary`` (a Rotary) q and k are turned by their positions in their sequences before the
-    attention, in the backward again, and dq and dk (rounded to bf16) are turned back."""
+    attention, in the backward again, and dq and dk (rounded to bf16) are turned back. Calls may
+    run on any stream; those that may overlap on the GPU need an FcpAttention each, as they
+    share its buffers."""
 
     def __init__(self, seqlens: Sequence[int], block_size: int, causal: bool, n_workers: int, hq: int, hkv: int,
                  head_dim: int, token_cap: Optional[int] = None, coalesce: int = 1, device="cuda",
@@ -570,6 +572,7 @@ class FcpAttention:
             raise ValueError("the new batch does not fit the buffers of this FcpAttention")
         if int(v["n_exec_stages"]) != self.n_stages:
             raise ValueError("the new batch has a different number of pipeline stages")
+        self._use(stream)
         plan.upload(self.d_plan, stream)
         self.plan = plan
         if self.rotary is not None:
@@ -628,6 +631,18 @@ class FcpAttention:
             self._place()
             self._turned = [torch.empty((h, self.T, head_dim), dtype=torch.bfloat16, device=self.device)
                             for h in (hq, hkv)]
+        from .paged import _Owner
+
+        mine = [self.d_plan, self.part_o, self.part_lse]
+        mine += [] if self.workspace is None else [self.workspace]
+        mine += [] if rotary is None else [self.positions, *self._turned]
+        self._memory = _Owner()  # of all streams that use it; the plan's upload is done from here on
+        self._memory._own(mine, self.d_plan.get_device())
+
+    def _use(self, stream) -> None:
+        raw = _stream(stream)
+        if raw not in self._memory._streams:
+            self._memory._note(raw, stream)
 
     def _turn(self, q, k, stream):
         if self.rotary is None:
@@ -643,6 +658,7 @@ class FcpAttention:
             o = torch.empty((self.hq, self.T, self.head_dim), dtype=torch.bfloat16, device=self.device)
         if lse is None:
             lse = torch.empty((self.hq, self.T), dtype=torch.float32, device=self.device)
+        self._use(stream)
         q, k = self._turn(q, k, stream)
         if self.n_stages > 1:
             for st in range(self.n_stages):
@@ -660,6 +676,7 @@ class FcpAttention:
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
+        self._use(stream)
         q, k = self._turn(q, k, stream)
         block_attn_bwd(self.plan, self.d_plan, q, k, v, o, dout, lse, dq, dk, dv, self.workspace, stream)
         if self.rotary is not None:
