@@ -257,10 +257,10 @@ fcp_status launch_move(const PagedArgs& p, int dtype, void* k, void* v, cudaStre
       return FCP_OK;
     }
   }
-  constexpr int kRead4 = kRead ? FCP_CACHE_E2M1 : FCP_CACHE_BF16;  // e2m1 is written above
-  auto* kernel = dtype == FCP_CACHE_E2M1   ? move_kernel<D, kRead4, kRead>
-                 : dtype == FCP_CACHE_E4M3 ? move_kernel<D, FCP_CACHE_E4M3, kRead>
-                                           : move_kernel<D, FCP_CACHE_BF16, kRead>;
+  auto* kernel = dtype == FCP_CACHE_E4M3 ? move_kernel<D, FCP_CACHE_E4M3, kRead> : move_kernel<D, FCP_CACHE_BF16, kRead>;
+  if constexpr (kRead) {
+    if (dtype == FCP_CACHE_E2M1) kernel = move_kernel<D, FCP_CACHE_E2M1, true>;
+  }
   const char* where = kRead ? "cache read launch" : "cache write launch";
   if (fills(heads)) return launch_overlapped(kernel, grid, kMoveThreads, 0, s, where, p, pk, pv, heads);
   kernel<<<grid, kMoveThreads, 0, s>>>(p, pk, pv, heads);

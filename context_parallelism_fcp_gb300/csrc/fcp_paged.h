@@ -174,6 +174,15 @@ __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t eight, uint32_t (&r)[4]
       : "r"(eight));
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // An e4m3 scale as float32.
 __device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
   uint32_t lo, hi;

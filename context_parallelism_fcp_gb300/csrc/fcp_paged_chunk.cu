@@ -136,15 +136,6 @@ __device__ __forceinline__ void times(uint32_t (&r)[4], uint32_t f) {
   }
 }
 
-__device__ __forceinline__ uint32_t times_f16(uint32_t x, uint32_t f) {
-  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f));
-  return *reinterpret_cast<const uint32_t*>(&y);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Row r of a tile of Q in shared memory from bf16 to f16 in place, scaled by 2^(14 - e) with e the row's
 // largest exponent; returns 2^(e - 14). Pieces [c0, c1) of 8 channels, behind looked(). A lane begins at its own 16 bytes of a row, so that neighbours
 // are on different banks. (Not unrolled: once a unit, its instructions come from far away. 16 chunks of 512 with
@@ -395,8 +386,8 @@ __global__ void __launch_bounds__(kThreads<kKind, kHalves>, 1)
                 e2m1x8_to_f16x2(word[y], h);
                 const int q = 4 * c4 + y;
                 *reinterpret_cast<uint4*>(dst + (q >> 3) * kPanelBytes + r * 128 + (((q ^ r) & 7) << 4)) =
-                    make_uint4(times_f16(h[0], f[y >> 1]), times_f16(h[1], f[y >> 1]), times_f16(h[2], f[y >> 1]),
-                               times_f16(h[3], f[y >> 1]));
+                    make_uint4(mul_f16x2(h[0], f[y >> 1]), mul_f16x2(h[1], f[y >> 1]), mul_f16x2(h[2], f[y >> 1]),
+                               mul_f16x2(h[3], f[y >> 1]));
               }
             }
             fence_proxy_async_smem();

@@ -65,10 +65,6 @@ __device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4],
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // The 8x8 matrix of 16-bit elements that the warp holds, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {

@@ -75,10 +75,6 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
 __device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 // One half of a register, twice.
 __device__ __forceinline__ uint32_t half_of(uint32_t x, int high) {
   const __half2 h = *reinterpret_cast<const __half2*>(&x), r = high ? __high2half2(h) : __low2half2(h);
