@@ -141,10 +141,11 @@ __device__ __forceinline__ uint2 quantise(const uint4 x, uint32_t& scale_byte) {
   return quantise8(x, max(two & 0xffffu, two >> 16), scale_byte);
 }
 
-// Quantise 8 channels to e2m1, of 16 whose largest magnitude is top: 8 codes and the scale's byte. (Division by 6 and by the scale as products, rounded to 12 bits and to
-// 2^-13: quotients that lie on a border between two codes become that border exactly, and others are
-// at least 2^-9 of themselves away from one, since x has 8 significant bits and a border times a scale
-// at most 7. So this rounds as the quotients themselves would.)
+// Quantise 8 channels to e2m1, of 16 whose largest magnitude is top: 8 codes and the scale's byte.
+// (Division by 6 and by the scale as products, rounded to 12 bits and to 2^-13: quotients that lie on a
+// border between two codes become that border exactly, and others are at least 2^-9 of themselves away
+// from one, since x has 8 significant bits and a border times a scale at most 7. So this rounds as the
+// quotients themselves would.)
 __device__ __forceinline__ uint32_t quantise4(const uint4 x, uint32_t top, float per_unit, uint32_t& scale_byte) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   const float sixth = __uint_as_float(top << 16) * per_unit * (1.f / 6.f);

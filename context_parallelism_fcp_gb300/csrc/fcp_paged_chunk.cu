@@ -34,11 +34,12 @@
 // (2908, one slot for each loader being all that fits) into shared memory first; prefetches to L2 (1490);
 // eight loaders, whose registers the softmax warps lack then (1701, the 16 chunks 238).
 //
-// Warps 0-3 and 4-7: softmax of tile 0 and 1, or of the first and second 64 keys of the only one (thread = row =
-// TMEM lane); 8: the walk along the
-// block's share of the work, Q's loads and a bf16 cache's; 9: MMA; 10-15 (e4m3 and e2m1) or 10-17: loaders.
-// TMEM columns: S_t at [128 t, 128 t + 128), overwritten by P_t as bf16; O_t at [256 + 128 t,
-// 256 + 128 t + D).
+// Warps 0-3 and 4-7: softmax of tile 0 and 1, or of the first and second 64 keys of the only one
+// (thread = row = TMEM lane); 8: the walk along the block's share of the work, Q's loads and a bf16
+// cache's; 9: MMA; 10-15 (e4m3 and e2m1) or 10-17: loaders.
+// TMEM columns: S_t at [128 t, 128 t + 128), overwritten by P_t as bf16 (4 bits: f16); O_t at
+// [256 + 128 t, 256 + 128 t + D). In units of one tile S_t is that of every second key tile, and O_t
+// the sum over group t's keys.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -137,9 +138,9 @@ __device__ __forceinline__ void times(uint32_t (&r)[4], uint32_t f) {
 }
 
 // Row r of a tile of Q in shared memory from bf16 to f16 in place, scaled by 2^(14 - e) with e the row's
-// largest exponent; returns 2^(e - 14). Pieces [c0, c1) of 8 channels, behind looked(). A lane begins at its own 16 bytes of a row, so that neighbours
-// are on different banks. (Not unrolled: once a unit, its instructions come from far away. 16 chunks of 512 with
-// nothing before them 220 us instead of 235.)
+// largest exponent; returns 2^(e - 14). Pieces [c0, c1) of 8 channels, behind looked(). A lane begins at
+// its own 16 bytes of a row, so that neighbours are on different banks. (Not unrolled: once a unit, its
+// instructions come from far away. 16 chunks of 512 with nothing before them 220 us instead of 235.)
 template <int D, class F>
 __device__ __forceinline__ float q_to_f16(uint8_t* tile, int r, int c0, int c1, F looked) {
   uint32_t top = 0;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kThreads<kKind, kHalves>, 1)
     if constexpr (kLoad) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther<kHalves>));
     if (kHalves && warp >= 10 + kLoaders) {
     } else if (warp >= 10) {
-      // ---------------------------------------------------------- loaders (e4m3)
+      // ---------------------------------------------------------- loaders (e4m3 and e2m1)
       // The work is 16-row groups, each in one page: K's eight of a tile, V's eight, the next tile's.
       // They go round the six warps; the two that share their scheduler with no other loader take a
       // sixth turn in every 32. A warp fetches its next group as soon as it has handed one over, and
@@ -1138,8 +1139,9 @@ fcp_status launch(AttnArgs a, void* workspace, int dev, int n_sm, int hq, cudaSt
   if (const fcp_status st = allow_smem(chunk_kernel<D, kKind, kHalves>, C::kSmemBytes, dev, allowed, "paged chunk smem attribute");
       st != FCP_OK)
     return st;
-  if (const fcp_status st = launch_overlapped<kKind == FCP_CACHE_BF16 ? 2 : 1>(chunk_kernel<D, kKind, kHalves>, dim3(blocks), kThreads<kKind, kHalves>, C::kSmemBytes, s,
-                                              "paged chunk launch", mq, mq16, mk, mv, a);
+  if (const fcp_status st = launch_overlapped<kKind == FCP_CACHE_BF16 ? 2 : 1>(
+          chunk_kernel<D, kKind, kHalves>, dim3(blocks), kThreads<kKind, kHalves>, C::kSmemBytes, s, "paged chunk launch",
+          mq, mq16, mk, mv, a);
       st != FCP_OK)
     return st;
   return launch_merge<P, D>(a, blocks, 32, s);

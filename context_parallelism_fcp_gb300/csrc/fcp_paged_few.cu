@@ -13,8 +13,9 @@
 // The products are S^T = K Q^T and O^T += V^T P^T, m16n8k16 with float32 sums: keys and channels
 // take the 16, rows the 8, so 8 rows (one token of 8 heads) fill the instruction, and K's and
 // V's fragments serve all of a unit's rows. (With rows as the 16, half empty, 128 e4m3 sequences
-// of up to 8192 keys took 171 us; tcgen05's 128 rows would be fifteen sixteenths empty.) A lane
-// has two keys and two rows of S^T; movmatrix turns the weights into P^T's fragment.
+// of up to 8192 keys took 171 us; tcgen05 with rows as its 128 would be fifteen sixteenths empty, with
+// keys as its 128 it was not tried.) A lane has two keys and two rows of S^T; movmatrix turns the weights
+// into P^T's fragment.
 //
 // K is read from shared memory 16 bytes to a lane: the product over channels does not care for
 // their order, so lane j of a quad takes 8 (bf16) or 16 (e4m3) neighbouring channels and Q's
